@@ -218,24 +218,30 @@ def _values(packed, scales):
     return (table[both.int()].unflatten(-1, (D // G, G)) * scales.float()[..., None]).flatten(-2)
 
 
+def _swap_halves(packed):
+    """The 32-byte halves of the rows (64 packed bytes) of tokens with bit 1 set change places."""
+    odd = (torch.arange(TILE, device=packed.device) & 2 > 0)[:, None]
+    return torch.where(odd, packed.roll(D // 4, -1), packed)
+
+
 def _records(k, v):
     """[n, 16, 128] keys and values -> [n, 2304] records.  Scale order: K byte (tok % 8) * 16 +
-    (block / 2) * 4 + (tok / 8) * 2 + block % 2; V byte block * 16 + (tok % 4) * 4 + tok / 4."""
+    (block / 2) * 4 + (tok / 8) * 2 + block % 2; V byte block * 16 + (tok % 8 / 2) * 4 + (tok / 8) * 2 + tok % 2."""
     n = k.shape[0]
     kc, ks = _quantise(k)
     vc, vs = _quantise(v)
-    ks = ks.view(torch.uint8).view(n, 2, 8, 4, 2).permute(0, 2, 3, 1, 4).reshape(n, 128)     # tok/8, tok%8, blk/2, blk%2
-    vs = vs.view(torch.uint8).view(n, 4, 4, 8).permute(0, 3, 2, 1).reshape(n, 128)           # tok/4, tok%4, blk
-    return torch.cat((_pack(kc).reshape(n, 1024), _pack(vc).reshape(n, 1024), ks, vs), 1)
+    ks = ks.view(torch.uint8).view(n, 2, 8, 4, 2).permute(0, 2, 3, 1, 4).reshape(n, 128)
+    vs = vs.view(torch.uint8).view(n, 2, 4, 2, 8).permute(0, 4, 2, 1, 3).reshape(n, 128)
+    return torch.cat((_pack(kc).reshape(n, 1024), _swap_halves(_pack(vc)).reshape(n, 1024), ks, vs), 1)
 
 
 def _unrecord(rec):
     """Records [..., 2304] -> float32 keys and values [..., 16, 128]."""
     lead = rec.shape[:-1]
     ks = rec[..., 2048:2176].reshape(*lead, 8, 4, 2, 2).movedim(-2, -4).reshape(*lead, 16, 8)
-    vs = rec[..., 2176:2304].reshape(*lead, 8, 4, 4).movedim(-3, -1).transpose(-3, -2).reshape(*lead, 16, 8)
+    vs = rec[..., 2176:2304].reshape(*lead, 8, 4, 2, 2).movedim(-4, -1).transpose(-4, -3).reshape(*lead, 16, 8)
     k = _values(rec[..., :1024].reshape(*lead, 16, 64), ks.contiguous().view(torch.float8_e4m3fn))
-    v = _values(rec[..., 1024:2048].reshape(*lead, 16, 64), vs.contiguous().view(torch.float8_e4m3fn))
+    v = _values(_swap_halves(rec[..., 1024:2048].reshape(*lead, 16, 64)), vs.contiguous().view(torch.float8_e4m3fn))
     return k, v
 
 
@@ -382,7 +388,8 @@ def exact(case, seed):
     tok = torch.arange(TILE, device="cuda")
     blk = torch.arange(D // G, device="cuda")
     k_at = 2048 + (tok % 8 * 16 + tok // 8 * 2)[:, None] + (blk // 2 * 4 + blk % 2)[None]
-    v_at = 2176 + (tok % 4 * 4 + tok // 4)[:, None] + (blk * 16)[None]
+    v_at = 2176 + (tok % 8 // 2 * 4 + tok // 8 * 2 + tok % 2)[:, None] + (blk * 16)[None]
+    byte_at = torch.arange(D // 2, device="cuda")[None] ^ (tok // 2 % 2 * 32)[:, None]      # V: halves swapped
     for b in range(B):
         L = int(s["lens"][b])
         if L == 0:
@@ -391,6 +398,8 @@ def exact(case, seed):
         kv = []
         for code_at, scale_at in ((0, k_at), (1024, v_at)):
             byte = rec[..., code_at:code_at + 1024].reshape(hkv, -1, TILE, 64)
+            if code_at:
+                byte = byte.gather(-1, byte_at.expand(byte.shape))
             x = torch.empty(hkv, byte.shape[1], TILE, D, dtype=torch.float64, device="cuda")
             x[..., 0::2] = _exact_e2m1(byte & 15)
             x[..., 1::2] = _exact_e2m1(byte >> 4)
