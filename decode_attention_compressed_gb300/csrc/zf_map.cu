@@ -1,0 +1,318 @@
+// zf_map_tokens: block tables and slot maps from request lengths.
+//
+// need_b = ceil((len_b + new_b) / P), extra_b = max(0, need_b - held_b); exclusive prefix sums of new
+// and extra in request order give each request its entries of the lists and its free pages; entry i
+// of request b sits at position p = len_b + i, on page table[b][p / P] (or the free page that row
+// entry is about to get), index p % P.
+//
+// A decode step is bound by latency (one launch, two dependent round trips), a batch of prompts by
+// the 12 bytes it writes per token.  One launch either way: a single cluster of 1, 8 or 16 CTAs, every
+// one of which scans the whole batch (three loads per request) into its shared memory; the cluster
+// barrier after that scan is what lets the outputs be the same arrays as the inputs.  The CTAs then
+// share out the table entries (a warp per request) and the list entries (four per thread: one
+// binary search and one division for each four, 16-byte stores).
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <climits>
+#include <mutex>
+
+#include "zf_device.cuh"
+#include "zf_host.h"
+
+namespace zf {
+
+namespace {
+
+constexpr int kMapThreads = 1024;
+constexpr int kMapPer = ZF_MAX_BATCH / kMapThreads;        // requests per thread of the scan
+
+struct MapArgs {
+  const int32_t* seq_lens;
+  const int32_t* pages_held;
+  const int32_t* new_tokens;
+  int32_t* page_table;
+  const int32_t* free_pages;
+  const int32_t* free_pos;
+  int32_t* out_lens;
+  int32_t* out_held;
+  int32_t* out_pos;
+  int32_t* token_start;
+  int32_t* page_ids;
+  int32_t* positions;
+  int32_t* seq_positions;
+  int32_t* status;
+  int32_t batch, page_size, max_pages, num_free, max_tokens;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
+__global__ void __launch_bounds__(kMapThreads) map_kernel(const MapArgs a) {
+  extern __shared__ int32_t sm[];
+  __shared__ long long warp_new[32], warp_extra[32];
+  int32_t* start = sm;                          // [batch + 1] first list entry of each request
+  int32_t* base = start + a.batch + 1;          // [batch] index of its first new page in free_pages
+  int32_t* len = base + a.batch;                // [batch]
+  int32_t* held = len + a.batch;                // [batch]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank(), ranks = cluster_size();
+  allow_next_grid();
+  wait_prior_grid();
+
+  // ---- the batch: this thread's consecutive requests
+  const int per = (a.batch + kMapThreads - 1) / kMapThreads;
+  const int P = a.page_size;
+  int nw[kMapPer], ex[kMapPer];
+  long long sum_new = 0, sum_extra = 0;
+  const int pos0 = *a.free_pos;
+#pragma unroll
+  for (int k = 0; k < kMapPer; ++k) {
+    const int b = tid * per + k;
+    nw[k] = ex[k] = 0;
+    if (k < per && b < a.batch) {
+      const int L = a.seq_lens[b], h = a.pages_held[b], n = a.new_tokens[b];
+      len[b] = L;
+      held[b] = h;
+      const long long cap = static_cast<long long>(a.max_pages) * P;
+      const bool ok = L >= 0 && n >= 0 && h >= 0 && h <= a.max_pages && L <= static_cast<long long>(h) * P &&
+                      static_cast<long long>(L) + n <= cap;
+      if (ok) {
+        nw[k] = n;
+        ex[k] = max(0, (L + n + P - 1) / P - h);
+        sum_new += nw[k];
+        sum_extra += ex[k];
+      } else if (rank == 0) {
+        report(a.status, ZF_DEV_BAD_SEQ_LEN);
+      }
+    }
+  }
+  // ---- prefix sums over the threads (64 bits: a refused call's totals may not fit 32)
+  long long in_new = sum_new, in_extra = sum_extra;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, in_new, d), y = __shfl_up_sync(0xFFFFFFFFu, in_extra, d);
+    if (lane >= d) {
+      in_new += x;
+      in_extra += y;
+    }
+  }
+  if (lane == 31) {
+    warp_new[warp] = in_new;
+    warp_extra[warp] = in_extra;
+  }
+  __syncthreads();
+  long long off_new = 0, off_extra = 0, total_new = 0, total_extra = 0;
+#pragma unroll 8
+  for (int w = 0; w < kMapThreads / 32; ++w) {
+    const long long x = warp_new[w], y = warp_extra[w];
+    if (w < warp) {
+      off_new += x;
+      off_extra += y;
+    }
+    total_new += x;
+    total_extra += y;
+  }
+  const bool fits = pos0 >= 0 && total_new <= a.max_tokens && total_extra + pos0 <= a.num_free;
+  if (!fits && rank == 0 && tid == 0) report(a.status, ZF_DEV_CAPACITY);
+  long long at_new = off_new + in_new - sum_new, at_extra = pos0 + off_extra + in_extra - sum_extra;
+#pragma unroll
+  for (int k = 0; k < kMapPer; ++k) {
+    const int b = tid * per + k;
+    if (k < per && b < a.batch) {
+      start[b] = fits ? static_cast<int>(at_new) : 0;
+      base[b] = fits ? static_cast<int>(at_extra) : 0;
+      at_new += nw[k];
+      at_extra += ex[k];
+    }
+  }
+  if (tid == 0) start[a.batch] = fits ? static_cast<int>(total_new) : 0;
+  __syncthreads();
+  // every CTA has read the inputs: from here on they may be overwritten
+  cluster_sync();
+
+  // ---- per request: lengths, pages, list starts (CTA 0)
+  if (rank == 0) {
+#pragma unroll
+    for (int k = 0; k < kMapPer; ++k) {
+      const int b = tid * per + k;
+      if (k < per && b < a.batch) {
+        a.out_lens[b] = len[b] + (fits ? nw[k] : 0);
+        a.out_held[b] = held[b] + (fits ? ex[k] : 0);
+        a.token_start[b] = start[b];
+      }
+    }
+    if (tid == 0) {
+      a.token_start[a.batch] = start[a.batch];
+      *a.out_pos = pos0 + (fits ? static_cast<int>(total_extra) : 0);
+    }
+  }
+  const int total = start[a.batch];
+
+  // ---- list entries, four per thread.  A page past those held is read from the free list, not from
+  // the table, whose new entries are being written below at the same time.
+  const int chunks = static_cast<int>((static_cast<long long>(a.max_tokens) + 3) >> 2);
+  for (int c = rank * kMapThreads + tid; c < chunks; c += ranks * kMapThreads) {
+    const int i0 = c * 4;
+    int pid[4], pos[4], seq[4];
+    int b = 0;
+    if (i0 < total) {                    // largest b with start[b] <= i0 (so start[b + 1] > i0)
+      int lo = 0, hi = a.batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= i0) lo = mid; else hi = mid;
+      }
+      b = lo;
+    }
+    int page = 0, in = -1, page_id = -1;
+    bool fresh = true;                   // the page id has to be fetched
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e;
+      if (i >= total) {
+        pid[e] = pos[e] = seq[e] = -1;
+        continue;
+      }
+      bool moved = e == 0;
+      while (start[b + 1] <= i) {
+        ++b;
+        moved = true;
+      }
+      const int p = len[b] + (i - start[b]);
+      if (moved) {
+        page = p / P;
+        in = p - page * P;
+        fresh = true;
+      } else if (++in == P) {
+        in = 0;
+        ++page;
+        fresh = true;
+      }
+      if (fresh) {
+        page_id = page < held[b] ? a.page_table[static_cast<size_t>(b) * a.max_pages + page]
+                                 : a.free_pages[base[b] + page - held[b]];
+        fresh = false;
+      }
+      pid[e] = page_id;
+      pos[e] = in;
+      seq[e] = p;
+    }
+    if (i0 + 4 <= a.max_tokens) {
+      *reinterpret_cast<int4*>(a.page_ids + i0) = make_int4(pid[0], pid[1], pid[2], pid[3]);
+      *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(a.seq_positions + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (i0 + e < a.max_tokens) {
+          a.page_ids[i0 + e] = pid[e];
+          a.positions[i0 + e] = pos[e];
+          a.seq_positions[i0 + e] = seq[e];
+        }
+      }
+    }
+  }
+
+  // ---- new table entries: a warp per request
+  if (fits && total_extra > 0) {
+    for (int b = rank * (kMapThreads / 32) + warp; b < a.batch; b += ranks * (kMapThreads / 32)) {
+      const int end = b + 1 < a.batch ? base[b + 1] : pos0 + static_cast<int>(total_extra);
+      int32_t* row = a.page_table + static_cast<size_t>(b) * a.max_pages + held[b];
+      for (int j = base[b] + lane; j < end; j += 32) row[j - base[b]] = a.free_pages[j];
+    }
+  }
+}
+
+}  // namespace
+}  // namespace zf
+
+using namespace zf;
+
+extern "C" zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max_pages, const int32_t* seq_lens,
+                                   const int32_t* pages_held, const int32_t* new_tokens, int32_t* page_table,
+                                   const int32_t* free_pages, int32_t num_free, const int32_t* free_pos,
+                                   int32_t* new_seq_lens, int32_t* new_pages_held, int32_t* new_free_pos,
+                                   int32_t* token_start, int32_t* page_ids, int32_t* positions,
+                                   int32_t* seq_positions, int32_t max_tokens, int32_t* status, void* stream) {
+  if (batch < 0 || batch > ZF_MAX_BATCH || max_pages < 1 || num_free < 0 || max_tokens < 0)
+    return ZF_ERR_INVALID_ARGUMENT;
+  if (page_size < ZF_BLOCK_TOKENS || page_size % ZF_BLOCK_TOKENS) return ZF_ERR_INVALID_ARGUMENT;
+  if (page_size > ZF_MAX_PAGE_SIZE) return ZF_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page_size >= INT_MAX) return ZF_ERR_INVALID_ARGUMENT;
+  const void* always[] = {free_pos, new_free_pos, token_start};
+  for (const void* p : always)
+    if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return ZF_ERR_INVALID_ARGUMENT;
+  const void* per_request[] = {seq_lens, pages_held, new_tokens, page_table, new_seq_lens, new_pages_held};
+  for (const void* p : per_request)
+    if ((batch > 0 && !p) || (reinterpret_cast<uintptr_t>(p) & 3u)) return ZF_ERR_INVALID_ARGUMENT;
+  if ((num_free > 0 && !free_pages) || (reinterpret_cast<uintptr_t>(free_pages) & 3u) ||
+      (reinterpret_cast<uintptr_t>(status) & 3u))
+    return ZF_ERR_INVALID_ARGUMENT;
+  const void* lists[] = {page_ids, positions, seq_positions};
+  for (const void* p : lists)
+    if (max_tokens > 0 && (!p || !aligned16(p))) return ZF_ERR_INVALID_ARGUMENT;
+  MapArgs a{};
+  a.seq_lens = seq_lens;
+  a.pages_held = pages_held;
+  a.new_tokens = new_tokens;
+  a.page_table = page_table;
+  a.free_pages = free_pages;
+  a.free_pos = free_pos;
+  a.out_lens = new_seq_lens;
+  a.out_held = new_pages_held;
+  a.out_pos = new_free_pos;
+  a.token_start = token_start;
+  a.page_ids = page_ids;
+  a.positions = positions;
+  a.seq_positions = seq_positions;
+  a.status = status;
+  a.batch = batch;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.num_free = num_free;
+  a.max_tokens = max_tokens;
+  // One CTA handles 4096 list entries in one pass; longer lists are shared out over a cluster.
+  const int ctas = max_tokens <= 4096 ? 1 : max_tokens <= 65536 ? 8 : 16;
+  const size_t smem = (static_cast<size_t>(batch) * 4 + 1) * 4;
+  static std::mutex mu;
+  static bool ready[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ZF_ERR_CUDA;
+  if (dev < 0 || dev >= 64) return ZF_ERR_UNSUPPORTED;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!ready[dev]) {
+      const int most = (ZF_MAX_BATCH * 4 + 1) * 4;
+      if (cudaFuncSetAttribute(map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
+          cudaFuncSetAttribute(map_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return ZF_ERR_CUDA;
+      ready[dev] = true;
+    }
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kMapThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, map_kernel, a) == cudaSuccess ? ZF_OK : ZF_ERR_CUDA;
+}

@@ -1,0 +1,727 @@
+// zf_q4_decode_attn: split-KV decode attention over the 4-bit paged cache (one or several new tokens
+// per request), followed by the split-result merge of zf_attn.cu.
+//
+// Mathematics.  K and V are code * s (16-channel blocks, e2m1 codes of two significant bits, e4m3
+// scales of four): every product code * s has at most six significant bits and is exact in fp16, so
+// the operands of the matrix instructions are the stored values themselves.  q (BF16) is brought into
+// fp16 by a power of two per row, which its scores take back: exact down to 2^-36 of the row's
+// largest value.  Scores, running maximum and sum and the output are float32.  The softmax weights p
+// (times 2^7, so that the remainder of a small weight stays clear of fp16's subnormals) are split
+// into an fp16 high part and an fp16 remainder, two MMAs: about 22 bits.
+//
+// Structure: as the attention kernels over the other caches (zf_attn.cu): one persistent CTA per SM,
+// the same work split (balanced page ranges, or fixed chunks), a metadata warp one item ahead,
+// consumer warps that each stream their own units of kUnitTiles 16-token records into two private
+// stages, and a combine of the warps' states at the end of an item.
+//  * A record holds K and V of 16 tokens of one kv head: one bulk copy (2304 bytes).
+//  * K^T: a lane's A fragments of all eight k-steps are 16 contiguous bytes of a token's row (the order
+//    of channels within the k-steps is free as long as q follows it), two 16-byte reads per record, and
+//    it meets two scale blocks per token, four scale bytes in one 4-byte read.
+//  * V: a lane's rows are the 16 channels of one block (eight m-tiles x two rows), so it needs one scale
+//    per token: four tokens' codes in four 8-byte reads, their scales in one 4-byte read.  The codes
+//    of two tokens are interleaved by nibble, so that one conversion gives a register of the
+//    operand (two tokens, one channel).
+//  * e2m1 pairs become half pairs in one conversion, and one multiplication applies the scale.
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include <climits>
+#include <mutex>
+
+#include "zf_attn_common.cuh"
+#include "zf_q4.cuh"
+
+namespace zf {
+
+namespace {
+
+constexpr int kUnitTiles = 2;                            // records per stage
+constexpr int kStageQ4 = kUnitTiles * kQ4Record;         // 4608
+constexpr int kQ4QRowBytes = 320;                        // q row in shared memory (see q_at)
+constexpr float kPShift = 7.f;                           // weights are 2^7 times their usual size
+static_assert(kStageQ4 >= (8 * kOStride + 16) * 4, "a stage holds a warp's combine state of 8 columns");
+
+// Consumer warps by the number of 8-column tiles of a pass (kNT), from the registers they need.
+template <int kNT>
+struct Q4Cfg {
+  static constexpr int kWarps = kNT == 1 ? 15 : kNT == 2 ? 11 : 7;
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kCols = 8 * kNT;
+};
+
+struct Q4Smem {
+  size_t stages, item_full, q_full, item_empty, misc, desc, meta, qbuf, qscale, bars, prefix, lens, total;
+};
+
+template <int kNT>
+__host__ __device__ inline Q4Smem q4_smem(int batch) {
+  using C = Q4Cfg<kNT>;
+  Q4Smem s;
+  size_t at = 0;
+  s.stages = at; at += static_cast<size_t>(C::kWarps) * kWarpStages * kStageQ4;
+  s.item_full = at; at += 2 * 8;
+  s.q_full = at; at += 2 * 8;
+  s.item_empty = at; at += 2 * 8;
+  s.misc = at; at += 16 + 16 * 4;               // [0] abort flag, [16..] combine stage per warp
+  s.desc = at; at += 2 * 64;
+  s.meta = at; at += 2 * kMaxItemTiles * 4;
+  s.qbuf = at; at += 2 * C::kCols * kQ4QRowBytes;
+  s.qscale = at; at += 2 * C::kCols * 4;
+  s.bars = at; at += static_cast<size_t>(C::kWarps) * kWarpStages * 8;
+  s.prefix = at; at += static_cast<size_t>(batch + 1) * 4;
+  s.lens = at; at += static_cast<size_t>(batch) * 4;
+  s.total = (at + 127) & ~static_cast<size_t>(127);
+  return s;
+}
+
+template <int kWarps>
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+}
+
+// Barrier over the consumer warps that also ORs a predicate across them.
+template <int kWarps>
+__device__ __forceinline__ bool consumers_any(bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(v)), "n"(kWarps * 32)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Start the copies of unit u (records u * kUnitTiles ..) of an item: lane i issues record i's.
+__device__ __forceinline__ bool issue_unit(const AttnArgs& a, const ItemDesc& d, const int* meta, int u,
+                                           uint8_t* stage, uint64_t* bar, int lane, uint64_t policy) {
+  const int t = u * kUnitTiles + lane;
+  int m = kKindInvalid;
+  if (lane < kUnitTiles && t < d.units) m = meta[t];
+  const bool ok = (m & 3) != kKindInvalid;
+  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
+  if (mask == 0) return false;
+  if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * kQ4Record);
+  __syncwarp();
+  if (ok) {
+    const size_t head = static_cast<size_t>(m >> 5) * a.hkv + d.g;
+    bulk_copy_g2s(stage + lane * kQ4Record,
+                  a.k_comp + head * a.comp_head_bytes + static_cast<size_t>((m >> 2) & 7) * kQ4Record, kQ4Record, bar,
+                  policy);
+  }
+  return true;
+}
+
+// One q row of 128 BF16 values (lane holds words lane and lane + 32) into shared memory as fp16 times
+// a power of two that brings its largest exponent to 11; returns the inverse factor.  Channel c =
+// 32 t + 8 j + e goes to byte 64 j + 16 t + 2 e: lane t's words of k-steps 2j, 2j+1 are 16 bytes,
+// and the rows' stride spreads a warp's reads over the banks.
+__device__ __forceinline__ float store_q_row(uint8_t* row, int lane, uint32_t w0, uint32_t w1) {
+  const uint32_t m0 = w0 & 0x7FFF7FFFu, m1 = w1 & 0x7FFF7FFFu;
+  const uint32_t big = max(max(m0 & 0xFFFFu, m0 >> 16), max(m1 & 0xFFFFu, m1 >> 16));
+  const int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, big) >> 7);        // biased exponent
+  const int k = min(138 - e, 126);
+  const float f = __int_as_float((127 + k) << 23);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w = h ? w1 : w0;
+    const int c = 2 * (lane + 32 * h);
+    const int t = c >> 5, j = (c >> 3) & 3, r = c & 7;
+    *reinterpret_cast<uint32_t*>(row + 64 * j + 16 * t + 2 * r) = pack_f16x2(bf16lo_to_f32(w) * f, bf16hi_to_f32(w) * f);
+  }
+  return __int_as_float((127 - k) << 23);
+}
+
+template <int kNT>
+__device__ __forceinline__ void stage_q(const AttnArgs& a, const ItemDesc& d, uint8_t* qb, float* qs, int lane) {
+  constexpr int kCols = Q4Cfg<kNT>::kCols;
+#pragma unroll
+  for (int r0 = 0; r0 < kCols; r0 += 8) {
+    uint32_t v[8][2];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int qh = d.h0 + min(r0 + r, d.nh - 1);
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + query_row(d.b, qh, a.tokens, a.hq) * ZF_HEAD_DIM);
+      v[r][0] = r0 + r < d.nh ? src[lane] : 0u;
+      v[r][1] = r0 + r < d.nh ? src[lane + 32] : 0u;
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float inv = store_q_row(qb + (r0 + r) * kQ4QRowBytes, lane, v[r][0], v[r][1]);
+      if (lane == 0) qs[r0 + r] = inv * a.scale_log2;
+    }
+  }
+}
+
+// kMulti: several new tokens per request (a causal mask on the last positions).
+template <int kNT, bool kMulti>
+__global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const AttnArgs a, const float v_factor) {
+  using C = Q4Cfg<kNT>;
+  constexpr int kWarps = C::kWarps;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const Q4Smem L = q4_smem<kNT>(a.batch);
+  uint64_t* item_full = reinterpret_cast<uint64_t*>(smem + L.item_full);
+  uint64_t* item_empty = reinterpret_cast<uint64_t*>(smem + L.item_empty);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L.q_full);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L.misc);
+  int* combine_stage = reinterpret_cast<int*>(smem + L.misc + 16);
+  ItemDesc* desc = reinterpret_cast<ItemDesc*>(smem + L.desc);
+  int* meta = reinterpret_cast<int*>(smem + L.meta);
+  uint8_t* qbuf = smem + L.qbuf;
+  float* qscale = reinterpret_cast<float*>(smem + L.qscale);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
+  int* prefix = reinterpret_cast<int*>(smem + L.prefix);
+  int* lens = reinterpret_cast<int*>(smem + L.lens);
+  uint8_t* stages = smem + L.stages;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid < 2) {
+    mbar_init(&item_full[tid], 1);
+    mbar_init(&q_full[tid], 1);
+    mbar_init(&item_empty[tid], kWarps);
+  }
+  if (tid < kWarps * kWarpStages) mbar_init(&bars[tid], 1);
+  if (tid == 0) *abort_flag = 0;
+  fence_mbar_init();
+  const int HS = a.hkv * a.slices;
+  wait_prior_grid();          // inputs may come from the preceding grid
+  allow_next_grid();
+  const uint64_t policy = l2_evict_first_policy();
+  load_lengths<false, C::kThreads>(a, prefix, lens, tid);       // ends with a barrier (also for the barriers above)
+  const Ranges g = make_ranges(a, HS * prefix[a.batch]);
+
+  if (warp == kWarps) {
+    // ============================================================== metadata warp
+    int k = 0;
+    if (a.publish_delay_ns) sleep_for_ns(a.publish_delay_ns);
+    auto publish = [&](const ItemDesc& d) -> bool {
+      const int buf = k & 1;
+      bool good = true;
+      if (lane == 0) good = !*abort_flag && mbar_wait(&item_empty[buf], ((k >> 1) & 1u) ^ 1u);
+      good = __shfl_sync(0xFFFFFFFFu, good, 0);
+      if (!good) {
+        if (lane == 0) {
+          report(a.status, ZF_DEV_TIMEOUT);
+          *abort_flag = 1;
+        }
+        return false;
+      }
+      if (d.b >= 0) resolve_tiles<false>(a, d, meta + buf * kMaxItemTiles, lane);
+      __syncwarp();
+      if (lane == 0) {
+        desc[buf] = d;
+        mbar_arrive(&item_full[buf]);        // release: the records can be fetched
+      }
+      if (d.b >= 0) {
+        stage_q<kNT>(a, d, qbuf + buf * C::kCols * kQ4QRowBytes, qscale + buf * C::kCols, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[buf]);   // release: the q rows
+      }
+      ++k;
+      return true;
+    };
+    if (walk_range(a, prefix, lens, g, HS, publish)) {
+      ItemDesc end_marker{};
+      end_marker.b = -1;
+      publish(end_marker);
+    }
+    return;
+  }
+
+  // ================================================================== consumer warps
+  // partials per pair, for the merge kernel (spread over all CTAs)
+  for (int p = blockIdx.x * (kWarps * 32) + tid; p < a.batch * HS; p += gridDim.x * (kWarps * 32)) {
+    const int b = p / HS, r = p - b * HS;
+    const int n = prefix[b + 1] - prefix[b];
+    a.chunk_counts[p] = a.chunk_pages > 0 ? n : n > 0 ? pair_chunks(g, HS * prefix[b] + r * n, n) : 0;
+  }
+  const int gi = lane >> 2, ti = lane & 3;
+  uint8_t* my_stages = stages + static_cast<size_t>(warp) * kWarpStages * kStageQ4;
+  uint64_t* my_bars = bars + warp * kWarpStages;
+  const int v_lane = kQ4VCodes + 128 * ti + 8 * (gi ^ ((ti & 1) << 2));     // V codes of tokens 2ti (+1, +8, +9)
+  uint32_t inflight = 0;        // bit s: stage s has copies armed and not yet waited for
+  bool prefetched = false;      // this warp's first unit of the current item is already in flight
+  bool aborted = false;
+  int sidx = 0;
+  uint32_t phase = 0;
+  auto give_up = [&]() {
+    aborted = true;
+    *abort_flag = 1;
+    report(a.status, ZF_DEV_TIMEOUT);
+  };
+  for (int k = 0;; ++k) {
+    const int buf = k & 1;
+    if (!aborted && (*abort_flag || !mbar_wait(&item_full[buf], (k >> 1) & 1u, a.wait_limit_ns))) give_up();
+    // one decision for all consumer warps: stop at the end marker, or once any wait gave up
+    if (consumers_any<kWarps>(aborted || desc[buf].b < 0)) break;
+    const ItemDesc d = desc[buf];
+    const int* m = meta + buf * kMaxItemTiles;
+    const int nu = (d.units + kUnitTiles - 1) / kUnitTiles;
+    const uint8_t* qrow = qbuf + (buf * C::kCols + gi) * kQ4QRowBytes + 16 * ti;
+
+    float mx[kNT][2], l[kNT][2], cs[kNT][2];      // running maximum less kPShift, sum, score factor; columns 2ti, 2ti+1
+    int seen[kNT][2];                             // kMulti: last position those columns see
+    float o[kNT][8][4];
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[n][e] = kNoScore;
+        l[n][e] = 0.f;
+        seen[n][e] = kMulti ? lens[d.b] - a.tokens + (d.h0 + 8 * n + 2 * ti + e) % a.tokens : 0;
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) o[n][mt][0] = o[n][mt][1] = o[n][mt][2] = o[n][mt][3] = 0.f;
+    }
+    const int causal_lim = kMulti ? lens[d.b] - a.tokens : 0;
+
+    if (!prefetched && warp < nu &&
+        issue_unit(a, d, m, warp, my_stages + sidx * kStageQ4, &my_bars[sidx], lane, policy))
+      inflight |= 1u << sidx;
+    prefetched = false;
+    if (!aborted && (*abort_flag || !mbar_wait(&q_full[buf], (k >> 1) & 1u, a.wait_limit_ns))) give_up();
+    if (!aborted) {
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) cs[n][e] = qscale[buf * C::kCols + 8 * n + 2 * ti + e];
+    }
+
+    for (int u = warp; u < nu && !aborted; u += kWarps) {
+      // start the warp's next unit: of this item, or its first one of the next item
+      const int un = u + kWarps;
+      const int ns = sidx ^ 1;
+      uint8_t* next_stage = my_stages + ns * kStageQ4;
+      if (un < nu) {
+        if (issue_unit(a, d, m, un, next_stage, &my_bars[ns], lane, policy)) inflight |= 1u << ns;
+      } else {
+        const int nb = buf ^ 1;       // the next item (or the end marker) is published after this one
+        if (*abort_flag || !mbar_wait(&item_full[nb], ((k + 1) >> 1) & 1u, a.wait_limit_ns)) {
+          give_up();
+          break;
+        } else if (desc[nb].b >= 0 && warp < (desc[nb].units + kUnitTiles - 1) / kUnitTiles) {
+          if (issue_unit(a, desc[nb], meta + nb * kMaxItemTiles, warp, next_stage, &my_bars[ns], lane, policy))
+            inflight |= 1u << ns;
+          prefetched = true;
+        }
+      }
+      // wait for the current unit (nothing armed: all its pages are bad, and it is skipped)
+      const bool armed = (inflight >> sidx) & 1u;
+      if (armed) {
+        if (*abort_flag || !mbar_wait(&my_bars[sidx], (phase >> sidx) & 1u)) {
+          give_up();
+          break;
+        }
+        phase ^= 1u << sidx;
+        inflight &= ~(1u << sidx);
+
+        const uint8_t* st = my_stages + sidx * kStageQ4;
+        int ntok[kUnitTiles];       // tokens of each record that count (0: past the item, or a bad page)
+#pragma unroll
+        for (int i = 0; i < kUnitTiles; ++i) {
+          const int t = u * kUnitTiles + i;
+          ntok[i] = t < d.units && (m[t] & 3) != kKindInvalid ? min(16, d.t1 - (d.t0 + 16 * t)) : 0;
+        }
+
+        // ---- S^T (16 tokens x 8 kNT columns) = K (16 x 128) . Q^T, per record
+        float x[kNT][kUnitTiles][4];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int i = 0; i < kUnitTiles; ++i) x[n][i][0] = x[n][i][1] = x[n][i][2] = x[n][i][3] = 0.f;
+        uint4 kc[kUnitTiles][2];
+        uint32_t ks[kUnitTiles][4];      // scale pairs: (row gi, row gi + 8) x (block 2ti, 2ti + 1)
+#pragma unroll
+        for (int i = 0; i < kUnitTiles; ++i) {
+          const uint8_t* rec = st + i * kQ4Record;
+          kc[i][0] = *reinterpret_cast<const uint4*>(rec + 64 * gi + 16 * ti);
+          kc[i][1] = *reinterpret_cast<const uint4*>(rec + 64 * (gi + 8) + 16 * ti);
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + kQ4KScales + 16 * gi + 4 * ti) & 0x7F7F7F7Fu;
+          ks[i][0] = __byte_perm(w, 0u, 0x4040u) << 7;      // token gi, block 2ti
+          ks[i][1] = __byte_perm(w, 0u, 0x4242u) << 7;      // token gi + 8, block 2ti
+          ks[i][2] = __byte_perm(w, 0u, 0x4141u) << 7;      // token gi, block 2ti + 1
+          ks[i][3] = __byte_perm(w, 0u, 0x4343u) << 7;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {    // k-steps 2j and 2j + 1: channels 32 ti + 8 j .. + 7
+          uint4 q[kNT];
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) q[n] = *reinterpret_cast<const uint4*>(qrow + 8 * n * kQ4QRowBytes + 64 * j);
+#pragma unroll
+          for (int i = 0; i < kUnitTiles; ++i) {
+            uint32_t ka[4], kb[4];
+            q4_decode4(j == 0 ? kc[i][0].x : j == 1 ? kc[i][0].y : j == 2 ? kc[i][0].z : kc[i][0].w, ka);
+            q4_decode4(j == 0 ? kc[i][1].x : j == 1 ? kc[i][1].y : j == 2 ? kc[i][1].z : kc[i][1].w, kb);
+            const uint32_t sa = ks[i][j < 2 ? 0 : 2], sb = ks[i][j < 2 ? 1 : 3];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              ka[e] = mul_f16x2(ka[e], sa);
+              kb[e] = mul_f16x2(kb[e], sb);
+            }
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+              mma_f16(x[n][i], ka[0], kb[0], ka[1], kb[1], q[n].x, q[n].y);
+              mma_f16(x[n][i], ka[2], kb[2], ka[3], kb[3], q[n].z, q[n].w);
+            }
+          }
+        }
+
+        // ---- online softmax, log2 domain.  lane: tokens gi, gi + 8 x columns 2ti, 2ti + 1 (per n)
+        bool grow = false;
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+          for (int i = 0; i < kUnitTiles; ++i) {
+            x[n][i][0] *= cs[n][0];
+            x[n][i][1] *= cs[n][1];
+            x[n][i][2] *= cs[n][0];
+            x[n][i][3] *= cs[n][1];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnitTiles; ++i) {
+          if (ntok[i] < 16) {
+#pragma unroll
+            for (int n = 0; n < kNT; ++n) {
+              if (gi >= ntok[i]) x[n][i][0] = x[n][i][1] = -CUDART_INF_F;
+              if (gi + 8 >= ntok[i]) x[n][i][2] = x[n][i][3] = -CUDART_INF_F;
+            }
+          }
+          if (kMulti) {
+            const int pos = d.t0 + 16 * (u * kUnitTiles + i) + gi;       // this lane's first row; the second is pos + 8
+            if (pos - gi + 15 > causal_lim) {
+#pragma unroll
+              for (int n = 0; n < kNT; ++n) {
+                if (pos > seen[n][0]) x[n][i][0] = -CUDART_INF_F;
+                if (pos > seen[n][1]) x[n][i][1] = -CUDART_INF_F;
+                if (pos + 8 > seen[n][0]) x[n][i][2] = -CUDART_INF_F;
+                if (pos + 8 > seen[n][1]) x[n][i][3] = -CUDART_INF_F;
+              }
+            }
+          }
+        }
+        float top[kNT][2];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            top[n][e] = fmaxf(x[n][0][e], x[n][0][e + 2]);
+#pragma unroll
+            for (int i = 1; i < kUnitTiles; ++i) top[n][e] = fmaxf(top[n][e], fmaxf(x[n][i][e], x[n][i][e + 2]));
+            grow |= top[n][e] > mx[n][e] + (kRescaleThreshold + kPShift);
+          }
+        }
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            float al[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float v = top[n][e];
+#pragma unroll
+              for (int dd = 4; dd < 32; dd <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, dd));
+              const float mn = fmaxf(mx[n][e], v - kPShift);      // finite: kNoScore at least
+              al[e] = fast_exp2(mx[n][e] - mn);
+              mx[n][e] = mn;
+              l[n][e] *= al[e];
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+              o[n][mt][0] *= al[0];
+              o[n][mt][1] *= al[1];
+              o[n][mt][2] *= al[0];
+              o[n][mt][3] *= al[1];
+            }
+          }
+        }
+
+#pragma unroll
+        for (int i = 0; i < kUnitTiles; ++i) {
+          // P^T as the B operand (k = token, n = column): fp16 high part (the float's first 11 bits)
+          // and fp16 remainder
+          uint32_t bh[kNT][2], bl[kNT][2];
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            float p[4], hi[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              p[r] = fast_exp2(x[n][i][r] - mx[n][r & 1]);
+              l[n][r & 1] += p[r];
+              hi[r] = __uint_as_float(__float_as_uint(p[r]) & 0xFFFFE000u);
+            }
+            bh[n][0] = transpose8x8(pack_f16x2(hi[0], hi[1]));
+            bh[n][1] = transpose8x8(pack_f16x2(hi[2], hi[3]));
+            bl[n][0] = transpose8x8(pack_f16x2(p[0] - hi[0], p[1] - hi[1]));
+            bl[n][1] = transpose8x8(pack_f16x2(p[2] - hi[2], p[3] - hi[3]));
+          }
+
+          // ---- O^T (128 channels x columns) += V^T (128 x 16 tokens) . P^T.  m-tile mt: row gi is
+          // channel 16 gi + 2 mt, row gi + 8 the next one; k: tokens 2ti, 2ti+1, 2ti+8, 2ti+9.
+          const uint8_t* rec = st + i * kQ4Record;
+          uint32_t w = *reinterpret_cast<const uint32_t*>(rec + kQ4VScales + 16 * gi + 4 * ti) & 0x7F7F7F7Fu;
+          if (ntok[i] < 16) {       // what lies past the context counts as 0
+            w &= (2 * ti < ntok[i] ? 0x000000FFu : 0u) | (2 * ti + 1 < ntok[i] ? 0x0000FF00u : 0u) |
+                 (2 * ti + 8 < ntok[i] ? 0x00FF0000u : 0u) | (2 * ti + 9 < ntok[i] ? 0xFF000000u : 0u);
+          }
+          const uint32_t s0 = __byte_perm(w, 0u, 0x4140u) << 7, s1 = __byte_perm(w, 0u, 0x4342u) << 7;
+          const uint2 va = *reinterpret_cast<const uint2*>(rec + v_lane);
+          const uint2 vb = *reinterpret_cast<const uint2*>(rec + v_lane + 64);
+          const uint2 vc = *reinterpret_cast<const uint2*>(rec + v_lane + 512);
+          const uint2 vd = *reinterpret_cast<const uint2*>(rec + v_lane + 576);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t wa = h ? va.y : va.x, wb = h ? vb.y : vb.x, wc = h ? vc.y : vc.x, wd = h ? vd.y : vd.x;
+            uint32_t a0[4], a1[4], a2[4], a3[4];
+            q4_decode4((wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u), a0);
+            q4_decode4(((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u), a1);
+            q4_decode4((wc & 0x0F0F0F0Fu) | ((wd << 4) & 0xF0F0F0F0u), a2);
+            q4_decode4(((wc >> 4) & 0x0F0F0F0Fu) | (wd & 0xF0F0F0F0u), a3);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              a0[e] = mul_f16x2(a0[e], s0);
+              a1[e] = mul_f16x2(a1[e], s0);
+              a2[e] = mul_f16x2(a2[e], s1);
+              a3[e] = mul_f16x2(a3[e], s1);
+            }
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mma_f16(o[n][4 * h + e], a0[e], a1[e], a2[e], a3[e], bh[n][0], bh[n][1]);
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mma_f16(o[n][4 * h + e], a0[e], a1[e], a2[e], a3[e], bl[n][0], bl[n][1]);
+          }
+        }
+      }
+      __syncwarp();                // the stage may now be refilled
+      sidx ^= 1;
+    }
+
+    // ---- merge the warps' states of this item through shared memory, 8 columns at a time.  Each warp
+    // writes into its stage that holds no unit in flight (the one it consumed last).
+    if (lane == 0) combine_stage[warp] = sidx ^ 1;
+    float* my_combine = reinterpret_cast<float*>(my_stages + (sidx ^ 1) * kStageQ4);
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) {
+      if (n > 0 && 8 * n >= d.nh) break;                 // uniform: no such columns
+      float* cm = my_combine + 8 * kOStride;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = l[n][e];
+#pragma unroll
+        for (int dd = 4; dd < 32; dd <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, dd);
+        if (gi == 0) {
+          cm[2 * ti + e] = mx[n][e];
+          cm[8 + 2 * ti + e] = v;
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2*>(my_combine + (2 * ti + e) * kOStride + 16 * gi + 2 * mt) =
+              make_float2(o[n][mt][e], o[n][mt][2 + e]);
+      }
+      consumers_sync<kWarps>();
+      for (int hh = warp; hh < 8 && 8 * n + hh < d.nh && !aborted; hh += kWarps) {     // a warp finishes whole columns
+        float mw[kWarps];
+        float M = kNoScore;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float* cwp = reinterpret_cast<const float*>(
+              stages + (static_cast<size_t>(w) * kWarpStages + combine_stage[w]) * kStageQ4);
+          mw[w] = cwp[8 * kOStride + hh];
+          M = fmaxf(M, mw[w]);
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float lsum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float* cwp = reinterpret_cast<const float*>(
+              stages + (static_cast<size_t>(w) * kWarpStages + combine_stage[w]) * kStageQ4);
+          const float f = fast_exp2(mw[w] - M);
+          lsum += f * cwp[8 * kOStride + 8 + hh];
+          const float4 v = *reinterpret_cast<const float4*>(cwp + hh * kOStride + 4 * lane);
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
+        }
+        const float inv = lsum == 0.f ? 0.f : v_factor / lsum;           // a NaN sum stays a NaN
+        acc.x *= inv;
+        acc.y *= inv;
+        acc.z *= inv;
+        acc.w *= inv;
+        const size_t bh = static_cast<size_t>(d.b) * a.hq + d.h0 + 8 * n + hh;
+        if (d.single) {
+          const size_t row = query_row(d.b, d.h0 + 8 * n + hh, a.tokens, a.hq);
+          *reinterpret_cast<float4*>(a.out + row * ZF_HEAD_DIM + 4 * lane) = acc;
+          if (lane == 0) a.lse[row] = lsum == 0.f ? -CUDART_INF_F : (M + log2f(lsum)) * kLn2;
+        } else {
+          const size_t pidx = bh * a.max_chunks + d.c;
+          *reinterpret_cast<float4*>(a.part_o + pidx * ZF_HEAD_DIM + 4 * lane) = acc;
+          // a NaN partial counts as +inf for the merge, whose weights and sum then are NaN
+          if (lane == 0)
+            a.part_lse[pidx] = lsum == 0.f ? -CUDART_INF_F : lsum == lsum ? M + log2f(lsum) : CUDART_INF_F;
+        }
+      }
+      consumers_sync<kWarps>();
+    }
+    fence_proxy_async_smem();          // the combine states' stages are refilled by bulk copies
+    if (lane == 0) mbar_arrive(&item_empty[buf]);     // this item's metadata and q are free
+  }
+  // copies still in flight (only after a wait gave up) must land before the CTA exits
+  for (int st = 0; st < kWarpStages; ++st)
+    if (inflight & (1u << st)) mbar_wait(&my_bars[st], (phase >> st) & 1u);
+}
+
+// 8-column tiles per pass: 1, 2 or 4 (the kernel reads a kv head's records once per 8, 16 or 32 columns).
+int q4_col_tiles(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
+
+template <int kNT>
+Plan q4_plan_nt(int batch, int hq, int hkv, int page_size, int max_pages, int sms) {
+  return make_plan(batch, hq, hkv, page_size, max_pages, sms, Q4Cfg<kNT>::kWarps, 8 * kNT);
+}
+
+Plan q4_plan(int batch, int hq, int hkv, int page_size, int max_pages, int sms) {
+  switch (q4_col_tiles(hq / hkv)) {
+    case 1: return q4_plan_nt<1>(batch, hq, hkv, page_size, max_pages, sms);
+    case 2: return q4_plan_nt<2>(batch, hq, hkv, page_size, max_pages, sms);
+    default: return q4_plan_nt<4>(batch, hq, hkv, page_size, max_pages, sms);
+  }
+}
+
+template <int kNT, bool kMulti>
+zf_status launch_q4(const AttnArgs& a, float v_factor, int grid, int which, cudaStream_t s) {
+  const size_t smem = q4_smem<kNT>(a.batch).total;
+  const zf_status st = ensure_smem_limit(reinterpret_cast<const void*>(attn_q4_kernel<kNT, kMulti>), which, smem);
+  if (st != ZF_OK) return st;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(Q4Cfg<kNT>::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attn_q4_kernel<kNT, kMulti>, a, v_factor) == cudaSuccess ? ZF_OK : ZF_ERR_CUDA;
+}
+
+}  // namespace
+
+static bool q4_shape_ok(int32_t batch, int32_t tokens, int32_t hq, int32_t hkv, int32_t max_pages) {
+  return tokens_ok(tokens, hq) && attn_shape_ok(batch, hq, hkv, max_pages) &&
+         attn_shape_ok(batch, hq * tokens, hkv, max_pages);
+}
+
+}  // namespace zf
+
+using namespace zf;
+
+extern "C" size_t zf_q4_decode_attn_workspace_size(int32_t batch, int32_t tokens, int32_t num_q_heads,
+                                                   int32_t num_kv_heads, int32_t page_size,
+                                                   int32_t max_pages_per_req) {
+  if (!q4_shape_ok(batch, tokens, num_q_heads, num_kv_heads, max_pages_per_req)) return 0;
+  if (page_size < ZF_BLOCK_TOKENS || page_size % ZF_BLOCK_TOKENS || page_size > ZF_MAX_PAGE_SIZE) return 0;
+  int sms = 0;
+  if (current_sm_count(&sms) != ZF_OK) return 0;
+  const size_t ws = q4_plan(batch, num_q_heads * tokens, num_kv_heads, page_size, max_pages_per_req, sms).ws_bytes;
+  return ws > 0 ? ws : 256;
+}
+
+extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, int32_t batch, int32_t tokens,
+                                       int32_t num_q_heads, const int32_t* page_table, int32_t max_pages,
+                                       const int32_t* seq_lens, float softmax_scale, float* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  zf_status st = check_q4_cache(c);
+  if (st != ZF_OK) return st;
+  if (!q4_shape_ok(batch, tokens, num_q_heads, c->num_kv_heads, max_pages)) return ZF_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return ZF_OK;
+  if (!q || !page_table || !seq_lens || !out || !lse || !workspace) return ZF_ERR_INVALID_ARGUMENT;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+      (reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(seq_lens) & 3u))
+    return ZF_ERR_INVALID_ARGUMENT;
+  // the scores' factor, with the cache's scale and the scale decoding's 2^-8 in it, must be a float
+  const float scale_log2 = softmax_scale * c->k_scale * (1.4426950408889634f * kQ4ScaleFactor);
+  if (!(scale_log2 >= -1e37f && scale_log2 <= 1e37f)) return ZF_ERR_INVALID_ARGUMENT;
+  if (c->num_pages >= (1 << 26)) return ZF_ERR_UNSUPPORTED;       // record entries pack a page id into 26 bits
+  int sms = 0;
+  if ((st = current_sm_count(&sms)) != ZF_OK) return st;
+  const int32_t hq = num_q_heads * tokens;
+  const int nt = q4_col_tiles(hq / c->num_kv_heads);
+  const Plan p = q4_plan(batch, hq, c->num_kv_heads, c->page_size, max_pages, sms);
+  if (workspace_bytes < p.ws_bytes) return ZF_ERR_WORKSPACE_TOO_SMALL;
+
+  AttnArgs a{};
+  a.k_comp = c->records;
+  a.status = c->status;
+  a.q = q;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.out = out;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + p.part_o_bytes);
+  a.chunk_counts = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + p.part_o_bytes + p.part_lse_bytes);
+  a.batch = batch;
+  a.hq = hq;
+  a.hkv = c->num_kv_heads;
+  a.group = hq / c->num_kv_heads;
+  a.tokens = tokens;
+  a.hps = 8 * nt;
+  a.slices = p.slices;
+  a.page_size = c->page_size;
+  a.num_pages = c->num_pages;
+  a.num_raw = c->num_pages;             // what resolve_tiles<false> bounds page ids by
+  a.max_pages = max_pages;
+  a.max_chunks = p.max_chunks;
+  a.min_range_pages = p.min_range_pages;
+  a.chunk_pages = p.chunk_pages;
+  a.comp_head_bytes = static_cast<int64_t>(c->page_size / 16) * kQ4Record;
+  a.scale_log2 = scale_log2;
+  a.wait_limit_ns = kWaitTimeoutNs;
+  const float v_factor = c->v_scale * kQ4ScaleFactor;
+
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool multi = tokens > 1;
+  if (nt == 1) st = multi ? launch_q4<1, true>(a, v_factor, p.grid, 0, s) : launch_q4<1, false>(a, v_factor, p.grid, 1, s);
+  else if (nt == 2) st = launch_q4<2, true>(a, v_factor, p.grid, 2, s);
+  else st = launch_q4<4, true>(a, v_factor, p.grid, 3, s);
+  if (st != ZF_OK) return st;
+
+  MergeArgs m{};
+  m.part_o = a.part_o;
+  m.part_lse = a.part_lse;
+  m.out = out;
+  m.lse = lse;
+  m.batch = batch;
+  m.hq = hq;
+  m.chunk_counts = a.chunk_counts;
+  m.group = a.group;
+  m.slices = a.slices;
+  m.max_chunks = p.max_chunks;
+  m.tokens = tokens;
+  m.hps = a.hps;
+  return launch_merge(m, multi, s);
+}

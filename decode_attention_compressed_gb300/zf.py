@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -22,6 +23,8 @@ DIR_INVALID = -2
 ENCODE_FORCE_RAW = 1
 DEV_BAD_PAGE_ID, DEV_BAD_RAW_SLOT, DEV_BAD_N_VALID = 0x1, 0x2, 0x4
 DEV_BAD_SEQ_LEN, DEV_BAD_DIR, DEV_TIMEOUT, DEV_BAD_SLOT = 0x8, 0x10, 0x20, 0x40
+DEV_NOT_FINITE, DEV_CAPACITY, DEV_BAD_DRAFT, DEV_BAD_PROBS = 0x80, 0x100, 0x200, 0x400
+Q4_RECORD_BYTES = 2304
 
 _c_int32, _c_void_p, _c_size_t, _c_float = ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
 
@@ -32,6 +35,13 @@ class ZfCacheDesc(ctypes.Structure):
         ("page_size", _c_int32), ("num_raw_slots", _c_int32), ("reserved", _c_int32),
         ("k_comp", _c_void_p), ("v_comp", _c_void_p), ("k_raw", _c_void_p), ("v_raw", _c_void_p),
         ("dir", _c_void_p), ("status", _c_void_p),
+    ]
+
+
+class ZfQ4CacheDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", _c_int32), ("num_kv_heads", _c_int32), ("head_dim", _c_int32), ("page_size", _c_int32),
+        ("k_scale", _c_float), ("v_scale", _c_float), ("records", _c_void_p), ("status", _c_void_p),
     ]
 
 
@@ -81,6 +91,19 @@ SIGNATURES = {
     "zf_dense_decode_attn_multi": (_c_int32, [ctypes.POINTER(ZfCacheDesc), _c_void_p, _c_int32, _c_int32, _c_int32,
                                               _c_void_p, _c_int32, _c_void_p, _c_float, _c_void_p, _c_void_p,
                                               _c_void_p, _c_size_t, _c_void_p]),
+    "zf_q4_write_tokens": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int32,
+                                      _c_void_p]),
+    "zf_q4_read_tokens": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_void_p, _c_int32, _c_void_p, _c_void_p,
+                                     _c_void_p]),
+    "zf_q4_decode_attn_workspace_size": (_c_size_t, [_c_int32, _c_int32, _c_int32, _c_int32, _c_int32, _c_int32]),
+    "zf_q4_decode_attn": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_int32, _c_int32, _c_int32, _c_void_p,
+                                     _c_int32, _c_void_p, _c_float, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
+                                     _c_void_p]),
+    "zf_map_tokens": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                 _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                 _c_void_p, _c_int32, _c_void_p, _c_void_p]),
+    "zf_verify_drafts": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
     "zf_kv_create": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_int32, _c_int32, _c_int32, ctypes.POINTER(_c_void_p)]),
     "zf_kv_destroy": (None, [_c_void_p]),
     "zf_kv_admit": (_c_int32, [_c_void_p, _c_int32, _c_int32, _P32, _P32, _P32, _P32]),
@@ -455,6 +478,228 @@ def decode_attn_static(cache: Cache, q, page_table, seq_lens, scale=None, out=No
                                        _ptr(seq_lens), scale, _ptr(out), _ptr(lse), _stream(stream))
     _check("zf_decode_attn_static", code)
     return out, lse
+
+
+# ------------------------------------------------------------------ the 4-bit cache (zf_q4_*)
+class Q4Cache:
+    """One layer's 4-bit paged cache in device memory (layout and numbers: include/zf.h, zf_q4).
+
+    records: [num_pages][Hkv][P/16][2304] uint8, given or allocated (zeros: every token reads as 0);
+    status: one int32 device word.  k_scale / v_scale multiply the stored values (1 suits values up
+    to about 2688).
+    """
+
+    def __init__(self, num_pages, num_kv_heads, page_size, device="cuda", k_scale=1.0, v_scale=1.0, records=None):
+        self.num_pages, self.num_kv_heads, self.page_size = num_pages, num_kv_heads, page_size
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        shape = (num_pages, num_kv_heads, page_size // 16, Q4_RECORD_BYTES)
+        if records is None:
+            records = torch.zeros(shape, dtype=torch.uint8, device=torch.device(device))
+        elif records.dtype != torch.uint8 or tuple(records.shape) != shape or not records.is_contiguous():
+            raise ValueError(f"records must be contiguous uint8 of shape {list(shape)}")
+        self.records = records
+        self.status = torch.zeros(1, dtype=torch.int32, device=records.device)
+
+    @property
+    def device(self):
+        return self.status.device
+
+    def desc(self) -> ZfQ4CacheDesc:
+        return ZfQ4CacheDesc(self.num_pages, self.num_kv_heads, HEAD_DIM, self.page_size, self.k_scale, self.v_scale,
+                             _ptr(self.records), _ptr(self.status))
+
+    def status_word(self) -> int:
+        return int(self.status.item())
+
+    def stored_bytes(self) -> int:
+        return self.records.numel()
+
+
+def q4_write_tokens(cache: Q4Cache, k_tok, v_tok, page_ids, positions, stream=None):
+    """zf_q4_write_tokens: k_tok/v_tok [n][Hkv][128] int16 BF16 bits (or bfloat16) on the device; entry i
+    is token positions[i] of page page_ids[i] (position -1: skipped).  Returns the index tensors (keep
+    them alive until the stream has consumed them)."""
+    k_tok = _arg(k_tok, "k_tok", cache, _BITS16, (None, cache.num_kv_heads, HEAD_DIM))
+    v_tok = _arg(v_tok, "v_tok", cache, _BITS16, tuple(k_tok.shape))
+    n = int(k_tok.shape[0])
+    ids, pos = _places(cache, page_ids, positions, n)
+    _on_current(cache.device)
+    d = cache.desc()
+    _check("zf_q4_write_tokens", lib().zf_q4_write_tokens(ctypes.byref(d), _ptr(k_tok), _ptr(v_tok), _ptr(ids),
+                                                           _ptr(pos), n, _stream(stream)))
+    return ids, pos
+
+
+def q4_read_tokens(cache: Q4Cache, page_ids, positions, stream=None):
+    """zf_q4_read_tokens: the values held at the listed places, (k, v) [n][Hkv][128] int16 BF16 bits."""
+    n = _count(page_ids)
+    ids, pos = _places(cache, page_ids, positions, n)
+    _on_current(cache.device)
+    k = torch.empty((n, cache.num_kv_heads, HEAD_DIM), dtype=torch.int16, device=cache.device)
+    v = torch.empty_like(k)
+    d = cache.desc()
+    _check("zf_q4_read_tokens", lib().zf_q4_read_tokens(ctypes.byref(d), _ptr(ids), _ptr(pos), n, _ptr(k), _ptr(v),
+                                                         _stream(stream)))
+    return k, v
+
+
+def _on_current(device):
+    """The kernels run on the current CUDA device and take its pointers."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}: a CUDA device is needed")
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _places(cache, page_ids, positions, n):
+    for name, x in (("page_ids", page_ids), ("positions", positions)):
+        if _count(x) != n:
+            raise ValueError(f"{name}: {_count(x)} entries for {n} tokens")
+    return _dev_i32(page_ids, cache.device), _dev_i32(positions, cache.device)
+
+
+def q4_workspace_size(batch, tokens, num_q_heads, num_kv_heads, page_size, max_pages) -> int:
+    return int(lib().zf_q4_decode_attn_workspace_size(batch, tokens, num_q_heads, num_kv_heads, page_size, max_pages))
+
+
+def q4_decode_attn(cache: Q4Cache, q, page_table, seq_lens, scale=None, out=None, lse=None, workspace=None,
+                   stream=None):
+    """zf_q4_decode_attn: decode attention over the 4-bit cache.  q [B][Hq][128], or [B][T][Hq][128] for T
+    new tokens per request (token t attends to positions 0 .. seq_lens[b] - T + t), int16 BF16 bits or
+    bfloat16.  Returns (out f32 of q's shape, lse f32 without the last dimension)."""
+    q = _arg(q, "q", cache, _BITS16)
+    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM:
+        raise ValueError(f"q: shape {list(q.shape)}, expected [*][*][{HEAD_DIM}] or [*][*][*][{HEAD_DIM}]")
+    shape = tuple(q.shape)
+    B, T, Hq = (shape[0], 1, shape[1]) if len(shape) == 3 else shape[:3]
+    page_table, seq_lens = _attn_args(cache, q, page_table, seq_lens, B)
+    max_pages = int(page_table.shape[1])
+    scale = 1.0 / math.sqrt(HEAD_DIM) if scale is None else scale
+    dev = cache.device
+    out = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else _result(out, "out", cache, shape)
+    lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if lse is None else \
+        _result(lse, "lse", cache, shape[:-1])
+    _on_current(dev)
+    if workspace is None:
+        workspace = new_workspace(q4_workspace_size(B, T, Hq, cache.num_kv_heads, cache.page_size, max_pages), dev)
+    d = cache.desc()
+    _check("zf_q4_decode_attn",
+           lib().zf_q4_decode_attn(ctypes.byref(d), _ptr(q), B, T, Hq, _ptr(page_table), max_pages, _ptr(seq_lens), scale,
+                                   _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                   _stream(stream)))
+    return out, lse
+
+
+# ---------------------------------------------------------- slot maps and draft verification
+class TokenMap(NamedTuple):
+    """What zf_map_tokens gives (int32 device tensors): the requests' lengths and pages after the call, the
+    position in the free list, where each request's entries start, and per new token its page, its
+    index in the page and its position in the request (-1 past the last)."""
+    seq_lens: torch.Tensor
+    pages_held: torch.Tensor
+    free_pos: torch.Tensor
+    token_start: torch.Tensor
+    page_ids: torch.Tensor
+    positions: torch.Tensor
+    seq_positions: torch.Tensor
+
+
+def _ints(t, name, like, shape, write=False):
+    """An int32 argument on the device of `like`, a tensor; written in place when `write`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {list(t.shape)}, expected {list(shape)}")
+    if write and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (it is written in place)")
+    return t.contiguous()
+
+
+def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_pos, page_size, max_tokens, out=None,
+               status=None, stream=None) -> TokenMap:
+    """zf_map_tokens: places for new_tokens[b] tokens of every request b, on the GPU.  page_table [B][max_pages]
+    is extended in place with pages free_pages[free_pos ..]; seq_lens, pages_held, new_tokens [B], free_pages
+    [F], free_pos [1], all int32 on the device.  out: a TokenMap to write into (its seq_lens, pages_held and
+    free_pos may be the arguments themselves); status: an int32 device word."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [batch][max_pages] tensor")
+    B, max_pages = page_table.shape
+    page_table = _ints(page_table, "page_table", page_table, (B, max_pages), write=True)
+    seq_lens = _ints(seq_lens, "seq_lens", page_table, (B,))
+    pages_held = _ints(pages_held, "pages_held", page_table, (B,))
+    new_tokens = _ints(new_tokens, "new_tokens", page_table, (B,))
+    free_pages = _ints(free_pages, "free_pages", page_table, (_count(free_pages),))
+    free_pos = _ints(free_pos, "free_pos", page_table, (1,))
+    max_tokens = int(max_tokens)
+    shapes = ((B,), (B,), (1,), (B + 1,), (max(max_tokens, 0),), (max(max_tokens, 0),), (max(max_tokens, 0),))
+    if out is None:
+        out = TokenMap(*(torch.empty(s, dtype=torch.int32, device=page_table.device) for s in shapes))
+    else:
+        out = TokenMap(*(_ints(t, f"out.{name}", page_table, s, write=True)
+                         for t, name, s in zip(out, TokenMap._fields, shapes)))
+    if status is not None:
+        status = _ints(status, "status", page_table, (1,), write=True)
+    _on_current(page_table.device)
+    _check("zf_map_tokens",
+           lib().zf_map_tokens(B, int(page_size), max_pages, _ptr(seq_lens), _ptr(pages_held), _ptr(new_tokens),
+                               _ptr(page_table), _ptr(free_pages), _count(free_pages), _ptr(free_pos),
+                               _ptr(out.seq_lens), _ptr(out.pages_held), _ptr(out.free_pos), _ptr(out.token_start),
+                               _ptr(out.page_ids), _ptr(out.positions), _ptr(out.seq_positions), max_tokens,
+                               _ptr(status), _stream(stream)))
+    return out
+
+
+def _floats(t, name, like, shape):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.float32")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {list(t.shape)}, expected {list(shape)}")
+    return t.contiguous()
+
+
+def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_drafts=None, seq_lens=None,
+                  new_seq_lens=None, status=None, stream=None):
+    """zf_verify_drafts: target_probs [B][T+1][V] float32, draft_tokens [B][T] int32, uniform [B][T+1] float32 in
+    [0, 1), draft_probs [B][T][V] float32 (None: the drafts were not sampled), n_drafts [B] int32 (None: T
+    each).  Returns (accepted [B], tokens [B][T+1]) int32: the accepted drafts, one sampled token, then -1.
+    With seq_lens (and new_seq_lens, which may be the same tensor) the lengths are shortened by the
+    refused drafts."""
+    if not isinstance(draft_tokens, torch.Tensor) or draft_tokens.dim() != 2:
+        raise ValueError("draft_tokens must be a [batch][drafts] tensor")
+    B, T = draft_tokens.shape
+    if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 3:
+        raise ValueError("target_probs must be a [batch][drafts + 1][vocab] tensor")
+    V = target_probs.shape[2]
+    draft_tokens = _ints(draft_tokens, "draft_tokens", draft_tokens, (B, T))
+    target_probs = _floats(target_probs, "target_probs", draft_tokens, (B, T + 1, V))
+    uniform = _floats(uniform, "uniform", draft_tokens, (B, T + 1))
+    if draft_probs is not None:
+        draft_probs = _floats(draft_probs, "draft_probs", draft_tokens, (B, T, V))
+    if n_drafts is not None:
+        n_drafts = _ints(n_drafts, "n_drafts", draft_tokens, (B,))
+    if (seq_lens is None) != (new_seq_lens is None):
+        raise ValueError("seq_lens and new_seq_lens go together")
+    if seq_lens is not None:
+        new_seq_lens = _ints(new_seq_lens, "new_seq_lens", draft_tokens, (B,), write=True)
+        seq_lens = _ints(seq_lens, "seq_lens", draft_tokens, (B,))
+    if status is not None:
+        status = _ints(status, "status", draft_tokens, (1,), write=True)
+    _on_current(draft_tokens.device)
+    accepted = torch.empty(B, dtype=torch.int32, device=draft_tokens.device)
+    tokens = torch.empty((B, T + 1), dtype=torch.int32, device=draft_tokens.device)
+    _check("zf_verify_drafts",
+           lib().zf_verify_drafts(B, T, V, _ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(n_drafts),
+                                  _ptr(uniform), _ptr(accepted), _ptr(tokens), _ptr(seq_lens), _ptr(new_seq_lens),
+                                  _ptr(status), _stream(stream)))
+    return accepted, tokens
 
 
 # --------------------------------------------------------------------------------- page manager

@@ -78,6 +78,10 @@ typedef int32_t zf_status;
 #define ZF_DEV_BAD_DIR 0x10            /* directory entry neither compressed nor a valid raw slot */
 #define ZF_DEV_TIMEOUT 0x20            /* a shared-memory pipeline wait gave up */
 #define ZF_DEV_BAD_SLOT 0x40           /* zf_validate_pages: a compressed slot's metadata is malformed */
+#define ZF_DEV_NOT_FINITE 0x80         /* zf_q4_write_tokens: a NaN or an infinity was stored (as 0 / the largest value) */
+#define ZF_DEV_CAPACITY 0x100          /* zf_map_tokens: too few free pages or token entries; nothing was mapped */
+#define ZF_DEV_BAD_DRAFT 0x200         /* zf_verify_drafts: a draft token or count out of range */
+#define ZF_DEV_BAD_PROBS 0x400         /* zf_verify_drafts: a row with no positive or no finite sum to sample from */
 
 #define ZF_HEAD_DIM 128
 #define ZF_BLOCK_TOKENS 16
@@ -91,6 +95,9 @@ typedef int32_t zf_status;
 #define ZF_MAX_BATCH 4096              /* requests per zf_decode_attn call */
 #define ZF_MAX_TOKENS 64               /* new tokens per request in zf_decode_attn_multi */
 #define ZF_MAX_PAGE_SIZE 128
+
+#define ZF_Q4_RECORD_BYTES 2304        /* 4-bit cache: 16 tokens of one (page, kv head), K and V */
+#define ZF_MAX_VOCAB (1 << 24)         /* zf_verify_drafts */
 
 #define ZF_ENCODE_FORCE_RAW 1          /* zf_encode_pages flag: store every page raw */
 
@@ -372,6 +379,143 @@ zf_status zf_decode_attn_static(const zf_cache* cache, const uint16_t* q, int32_
                                 int32_t num_q_heads, const int32_t* page_table,
                                 int32_t max_pages_per_req, const int32_t* seq_lens,
                                 float softmax_scale, float* out, float* lse, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * zf_q4 — a paged cache held in 4 bits, and the attention that reads it.  Lossy (the caches above
+ * are lossless): 144 bytes per token and kv head (K and V) instead of 512 dense or 392 compressed.
+ * There are no raw slots and no directory: a token is quantised as it is written, so a page needs no
+ * storage besides its records, and the page table and lengths are those of the other caches.
+ *
+ * Numbers.  The 128 channels of a token's K (or V) of one kv head form 8 blocks of 16.  With
+ * t = x * (1 / scale), scale = k_scale or v_scale and the reciprocal and the product rounded to float:
+ *   s    = 0 when every t of the block is 0, otherwise max|t| / 6 (float) rounded to e4m3 (nearest
+ *          even; at least 2^-9, at most 448);
+ *   code = t / s rounded to e2m1 (+-0, 0.5, 1, 1.5, 2, 3, 4, 6; nearest even, saturating at 6).
+ * The stored value is code * s * scale.  A NaN is stored as 0 and an infinity as +-6 * 448 * scale
+ * (both set ZF_DEV_NOT_FINITE); every stored byte pattern reads as a finite value.
+ *
+ * Layout: records[num_pages][num_kv_heads][page_size/16][ZF_Q4_RECORD_BYTES]; a record holds 16
+ * tokens.  Codes: two per byte, channel 2i in the low nibble of byte i of a token's 64-byte row.
+ *   [0,1024)     K codes: token j at 64 j
+ *   [1024,2048)  V codes: token j at 1024 + 64 j, with the row's two 32-byte halves exchanged when
+ *                bit 1 of j is set (the attention kernel's reads then spread over the banks)
+ *   [2048,2176)  K scales (e4m3 bytes): token j, block c at 2048 + 16 (j%8) + 4 (c/2) + 2 (j/8) + c%2
+ *   [2176,2304)  V scales: token j, block c at 2176 + 16 c + 4 (j%8/2) + 2 (j/8) + j%2
+ * ------------------------------------------------------------------------------------------ */
+typedef struct zf_q4_cache {
+  int32_t num_pages;      /* page ids are in [0, num_pages); below 2^26 for zf_q4_decode_attn */
+  int32_t num_kv_heads;
+  int32_t head_dim;       /* must be 128 */
+  int32_t page_size;      /* tokens per page, multiple of 16, <= ZF_MAX_PAGE_SIZE */
+  float k_scale;          /* in [1e-37, 1e37]; 1 suits values up to about 2688 */
+  float v_scale;
+  uint8_t* records;       /* [num_pages][num_kv_heads][page_size/16][ZF_Q4_RECORD_BYTES] */
+  int32_t* status;        /* optional device word; ZF_DEV_* bits are OR-ed in; NULL = not reported */
+} zf_q4_cache;
+
+/*
+ * zf_q4_write_tokens — quantise n tokens into their places (a decode step's new tokens, or a prompt).
+ *   k_tok, v_tok: [n][num_kv_heads][128] BF16: entry i is token positions[i] (0..page_size-1) of page
+ *                 page_ids[i]; other tokens of the page are left as they are.
+ *   page_ids, positions: [n]; a place must not be named twice in one call.  An entry with position
+ *                 -1 is skipped (the padding zf_map_tokens writes).  A bad page id sets
+ *                 ZF_DEV_BAD_PAGE_ID, a bad position ZF_DEV_BAD_N_VALID; the entry is skipped.
+ *   n == 0 is a no-op.  The source must not alias the cache.  Launched with programmatic stream
+ *   serialisation (it waits for the preceding kernel before reading).
+ */
+zf_status zf_q4_write_tokens(const zf_q4_cache* cache, const uint16_t* k_tok, const uint16_t* v_tok,
+                             const int32_t* page_ids, const int32_t* positions, int32_t n, void* stream);
+
+/* zf_q4_read_tokens — the values that the listed places hold, rounded to BF16 (exact when the cache's
+ * scale is a power of two): k_out, v_out [n][num_kv_heads][128].  Skipped and bad entries (as for
+ * zf_q4_write_tokens) read as zeros.  Places may repeat. */
+zf_status zf_q4_read_tokens(const zf_q4_cache* cache, const int32_t* page_ids, const int32_t* positions,
+                            int32_t n, uint16_t* k_out, uint16_t* v_out, void* stream);
+
+/* Workspace bytes zf_q4_decode_attn needs for these sizes on the current device.  0 on invalid sizes. */
+size_t zf_q4_decode_attn_workspace_size(int32_t batch, int32_t tokens, int32_t num_q_heads,
+                                        int32_t num_kv_heads, int32_t page_size,
+                                        int32_t max_pages_per_req);
+
+/*
+ * zf_q4_decode_attn — zf_decode_attn_multi over the 4-bit cache: decode attention for `tokens` (T)
+ * new tokens per request, whose keys and values are already in the cache.
+ *   q [batch][T][num_q_heads][128] BF16; page_table, seq_lens, softmax_scale, out [batch][T]
+ *   [num_q_heads][128] float32, lse [batch][T][num_q_heads] float32 and the workspace as for
+ *   zf_decode_attn_multi: token t of request b attends to positions 0 .. seq_lens[b] - T + t, one
+ *   that sees none gets out = 0 and lse = -inf.  A NaN or an infinity in a query row stays in that row.
+ *   A (kv head)'s records are read once per 32 columns (query heads per kv head x T).
+ *   K and V are multiplied as the exact stored values, scores and sums in float32; the softmax
+ *   weights enter the second product as two fp16 parts (about 22 bits).
+ *   Two kernels are enqueued (attention, then merge), launched with programmatic stream
+ *   serialisation; results are deterministic (no atomics).  A page id out of range sets
+ *   ZF_DEV_BAD_PAGE_ID and its tokens are skipped.
+ */
+zf_status zf_q4_decode_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t batch, int32_t tokens,
+                            int32_t num_q_heads, const int32_t* page_table, int32_t max_pages_per_req,
+                            const int32_t* seq_lens, float softmax_scale, float* out, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * zf_map_tokens — block tables and slot maps on the GPU: gives every request's new tokens their
+ * places, taking pages from a free list, without a host round trip (zf_kv below does the same
+ * bookkeeping on the host; here only lengths and pages exist, as the 4-bit cache needs no raw slots).
+ *   seq_lens [batch]: tokens held; pages_held [batch]: pages of each row of page_table that are in
+ *                 use, at least ceil(seq_len / page_size) (more after a request was shortened, for
+ *                 example by zf_verify_drafts: such pages are used before new ones are taken).
+ *   new_tokens [batch]: tokens to place (0 or more): positions seq_len .. seq_len + new - 1.
+ *   page_table [batch][max_pages_per_req], in and out: entries pages_held .. of a request that needs
+ *                 more pages are written; nothing else is.
+ *   free_pages [num_free], free_pos [1]: entry free_pos and those after it are free; requests take
+ *                 them in request order.
+ *   Outputs: new_seq_lens, new_pages_held [batch], new_free_pos [1] (each may be the same array as its
+ *   input); token_start [batch + 1]: request b's tokens are entries token_start[b] .. token_start[b+1]
+ *   - 1 of the lists; page_ids, positions [max_tokens]: page and index within it (what
+ *   zf_q4_write_tokens takes), seq_positions [max_tokens]: position in the request.  Entries from
+ *   token_start[batch] on are set to -1.
+ *   When the pages or the max_tokens entries do not suffice, nothing is mapped: every request is
+ *   treated as if it had no new tokens, and ZF_DEV_CAPACITY is set.  A request with a negative length or
+ *   count, more pages than max_pages_per_req, or more tokens than its pages hold gets no tokens and
+ *   sets ZF_DEV_BAD_SEQ_LEN.
+ *   status: optional device word.  batch <= ZF_MAX_BATCH; max_pages_per_req * page_size < 2^31.  One
+ *   kernel, launched with programmatic stream serialisation.
+ */
+zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max_pages_per_req, const int32_t* seq_lens,
+                        const int32_t* pages_held, const int32_t* new_tokens, int32_t* page_table,
+                        const int32_t* free_pages, int32_t num_free, const int32_t* free_pos,
+                        int32_t* new_seq_lens, int32_t* new_pages_held, int32_t* new_free_pos,
+                        int32_t* token_start, int32_t* page_ids, int32_t* positions, int32_t* seq_positions,
+                        int32_t max_tokens, int32_t* status, void* stream);
+
+/*
+ * zf_verify_drafts — verification of drafted tokens against the target's probabilities, from given
+ * random numbers (speculative sampling: the accepted tokens and the one sampled after them are
+ * distributed as the target's own).  Follows zf_decode_attn_multi / zf_q4_decode_attn on a request's
+ * last token and its T drafts.
+ *   target_probs: [batch][T+1][vocab] float32: row t is the target's distribution at draft t's place.
+ *   draft_probs:  [batch][T][vocab] float32, or NULL when the drafts were not sampled (a lookup): each
+ *                 draft then counts as proposed with probability 1.
+ *   draft_tokens: [batch][T]; n_drafts: [batch] drafts used (0..T), or NULL for T each.
+ *   uniform:      [batch][T+1] in [0, 1): entry t decides about draft t, entry T samples.
+ *   Draft t is accepted when uniform[t] * q_t(x) < p_t(x) (the product rounded to float); accepted[b]
+ *   counts the accepted ones before the first that is not.  With a = accepted[b], one more token is sampled: from
+ *   the weights max(p_a - q_a, 0) (float) when a draft was refused (from p_a when they are all 0), from
+ *   p_n when none was: the first i whose running sum of weights is above uniform[T] * (their sum),
+ *   sums being kept to at least 44 bits; the last i with a positive weight when there is none.
+ *   Weights that are NaN count as 0.
+ *   tokens: [batch][T+1]: the accepted drafts, the sampled token, then -1.
+ *   seq_lens, new_seq_lens: optional (both or neither; may be the same array): new_seq_lens[b] =
+ *                 seq_lens[b] - (n - a), the length without the refused drafts' places.
+ *   A draft token outside [0, vocab) is refused (the sample then excludes nothing) and an n_drafts outside
+ *   [0, T] is clamped, both setting ZF_DEV_BAD_DRAFT; a row whose weights have no positive finite sum
+ *   gives token -1 and sets ZF_DEV_BAD_PROBS.  status: optional device word.
+ *   batch <= ZF_MAX_BATCH, 1 <= T <= ZF_MAX_TOKENS, vocab <= ZF_MAX_VOCAB.  One kernel, launched with
+ *   programmatic stream serialisation; results do not depend on how the work is split.
+ */
+zf_status zf_verify_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, const float* target_probs,
+                           const float* draft_probs, const int32_t* draft_tokens, const int32_t* n_drafts,
+                           const float* uniform, int32_t* accepted, int32_t* tokens, const int32_t* seq_lens,
+                           int32_t* new_seq_lens, int32_t* status, void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * zf_kv — host-side page manager for the caches above.  ZipFusion §III.D (KV Cache Management and
