@@ -390,7 +390,8 @@ zf_status zf_decode_attn_static(const zf_cache* cache, const uint16_t* q, int32_
  * t = x * (1 / scale), scale = k_scale or v_scale and the reciprocal and the product rounded to float:
  *   s    = 0 when every t of the block is 0, otherwise max|t| / 6 (float) rounded to e4m3 (nearest
  *          even; at least 2^-9, at most 448);
- *   code = t / s rounded to e2m1 (+-0, 0.5, 1, 1.5, 2, 3, 4, 6; nearest even, saturating at 6).
+ *   code = t / s rounded to e2m1 (+-0, 0.5, 1, 1.5, 2, 3, 4, 6; nearest even, saturating at 6; a t of
+ *          -0 gives code 0, a negative t that rounds to zero keeps its sign bit).
  * The stored value is code * s * scale.  A NaN is stored as 0 and an infinity as +-6 * 448 * scale
  * (both set ZF_DEV_NOT_FINITE); every stored byte pattern reads as a finite value.
  *

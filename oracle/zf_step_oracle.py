@@ -52,10 +52,10 @@ def quantise_block(bits: np.ndarray, scale: float = 1.0):
     t[np.isnan(t)] = 0.0
     a = np.abs(t).max()
     if a == 0:
-        return np.where(np.signbit(t), 8, 0).astype(np.uint8), 0, odd
+        return np.zeros(BLOCK, np.uint8), 0, odd
     want = min(max(float(np.float32(a) / np.float32(6.0)) if np.isfinite(a) else math.inf, E4M3[1]), 448.0)
     byte = nearest_even(E4M3, want)
-    codes = [nearest_even(E2M1, abs(v) / E4M3[byte]) + (8 if np.signbit(v) else 0) for v in t]
+    codes = [nearest_even(E2M1, abs(v) / E4M3[byte]) + (8 if v < 0 else 0) for v in t]
     return np.array(codes, np.uint8), byte, odd
 
 

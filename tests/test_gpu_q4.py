@@ -85,7 +85,8 @@ def test_borders_between_codes_and_scales(zf):
     flip = x.flip(0).contiguous()
     zf.q4_write_tokens(c, x.cuda(), flip.cuda(), ids, pos)
     o.write(H.np_bits(x), H.np_bits(flip), ids, pos)
-    assert (c.records.cpu().numpy() == o.records).all()
+    got = c.records.cpu().numpy()
+    assert (got == o.records).all(), [(i.tolist(), got[tuple(i)], o.records[tuple(i)]) for i in np.argwhere(got != o.records)[:8]]
 
 
 def test_values_that_are_not_finite(zf):
