@@ -1,5 +1,5 @@
 // zf_q4_decode_attn: split-KV decode attention over the 4-bit paged cache (one or several new tokens
-// per request), followed by the split-result merge of zf_attn.cu.
+// per request), and its split-result merge.
 //
 // Mathematics.  K and V are code * s (16-channel blocks, e2m1 codes of two significant bits, e4m3
 // scales of four): every product code * s has at most six significant bits and is exact in fp16, so
@@ -110,24 +110,41 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// Start the copies of unit u (records u * kUnitTiles ..) of an item: lane i issues record i's.
-__device__ __forceinline__ bool issue_unit(const AttnArgs& a, const ItemDesc& d, const int* meta, int u,
-                                           uint8_t* stage, uint64_t* bar, int lane, uint64_t policy) {
+constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
+
+// The item's records into rec[u] (index into the cache, kNoRecord for a bad page), by all 32 lanes.
+__device__ __forceinline__ void resolve_records(const AttnArgs& a, const ItemDesc& d, uint32_t* rec, int lane) {
+  const int tpp = a.page_size >> 4;
+  const int32_t* row = a.page_table + static_cast<size_t>(d.b) * a.max_pages + d.pg0;
+  int pid[kPagesPerLane];
+#pragma unroll
+  for (int k = 0; k < kPagesPerLane; ++k) pid[k] = lane + 32 * k < d.npg ? row[lane + 32 * k] : -1;
+#pragma unroll
+  for (int k = 0; k < kPagesPerLane; ++k) {
+    const int i = lane + 32 * k;
+    if (i >= d.npg) break;
+    const bool ok = pid[k] >= 0 && pid[k] < a.num_pages;
+    if (!ok) report(a.status, ZF_DEV_BAD_PAGE_ID);
+    const uint32_t first = (static_cast<uint32_t>(pid[k]) * a.hkv + d.g) * tpp;
+    for (int t = 0; t < tpp; ++t)
+      if (i * tpp + t < d.units) rec[i * tpp + t] = ok ? first + t : kNoRecord;
+  }
+}
+
+// Start the copies of unit u (records u * kUnitTiles ..) of an item: lane i issues record i's.  Returns
+// which records were started (bit i).
+__device__ __forceinline__ uint32_t issue_unit(const uint8_t* records, const uint32_t* rec, int units, int u,
+                                               uint8_t* stage, uint64_t* bar, int lane, uint64_t policy) {
   const int t = u * kUnitTiles + lane;
-  int m = kKindInvalid;
-  if (lane < kUnitTiles && t < d.units) m = meta[t];
-  const bool ok = (m & 3) != kKindInvalid;
-  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
-  if (mask == 0) return false;
+  uint32_t r = kNoRecord;
+  if (lane < kUnitTiles && t < units) r = rec[t];
+  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, r != kNoRecord);
+  if (mask == 0) return 0;
   if (lane == 0) mbar_arrive_expect_tx(bar, __popc(mask) * kQ4Record);
   __syncwarp();
-  if (ok) {
-    const size_t head = static_cast<size_t>(m >> 5) * a.hkv + d.g;
-    bulk_copy_g2s(stage + lane * kQ4Record,
-                  a.k_comp + head * a.comp_head_bytes + static_cast<size_t>((m >> 2) & 7) * kQ4Record, kQ4Record, bar,
-                  policy);
-  }
-  return true;
+  if (r != kNoRecord)
+    bulk_copy_g2s(stage + lane * kQ4Record, records + static_cast<size_t>(r) * kQ4Record, kQ4Record, bar, policy);
+  return mask;
 }
 
 // One q row of 128 BF16 values (lane holds words lane and lane + 32) into shared memory as fp16 times
@@ -171,6 +188,16 @@ __device__ __forceinline__ void stage_q(const AttnArgs& a, const ItemDesc& d, ui
   }
 }
 
+// A row's result from its weighted sum of values (lane: channels 4 lane ..), its maximum M and its sum.
+// A sum of 0: nothing was seen; a NaN sum stays a NaN.
+__device__ __forceinline__ void finish_row(float* out, float* lse, size_t row, int lane, float4 acc, float M, float sum,
+                                           float v_factor) {
+  const float inv = sum == 0.f ? 0.f : v_factor / sum;
+  *reinterpret_cast<float4*>(out + row * ZF_HEAD_DIM + 4 * lane) =
+      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (lane == 0) lse[row] = sum == 0.f ? -CUDART_INF_F : (M + log2f(sum)) * kLn2;
+}
+
 // kMulti: several new tokens per request (a causal mask on the last positions).
 template <int kNT, bool kMulti>
 __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const AttnArgs a, const float v_factor) {
@@ -184,7 +211,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L.misc);
   int* combine_stage = reinterpret_cast<int*>(smem + L.misc + 16);
   ItemDesc* desc = reinterpret_cast<ItemDesc*>(smem + L.desc);
-  int* meta = reinterpret_cast<int*>(smem + L.meta);
+  uint32_t* meta = reinterpret_cast<uint32_t*>(smem + L.meta);
   uint8_t* qbuf = smem + L.qbuf;
   float* qscale = reinterpret_cast<float*>(smem + L.qscale);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars);
@@ -224,7 +251,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         }
         return false;
       }
-      if (d.b >= 0) resolve_tiles<false>(a, d, meta + buf * kMaxItemTiles, lane);
+      if (d.b >= 0) resolve_records(a, d, meta + buf * kMaxItemTiles, lane);
       __syncwarp();
       if (lane == 0) {
         desc[buf] = d;
@@ -257,7 +284,8 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   uint8_t* my_stages = stages + static_cast<size_t>(warp) * kWarpStages * kStageQ4;
   uint64_t* my_bars = bars + warp * kWarpStages;
   const int v_lane = kQ4VCodes + 128 * ti + 8 * (gi ^ ((ti & 1) << 2));     // V codes of tokens 2ti (+1, +8, +9)
-  uint32_t inflight = 0;        // bit s: stage s has copies armed and not yet waited for
+  uint32_t inflight = 0;        // per stage s, bits (s * kUnitTiles ..): records whose copies are under way
+  constexpr uint32_t kAll = (1u << kUnitTiles) - 1;
   bool prefetched = false;      // this warp's first unit of the current item is already in flight
   bool aborted = false;
   int sidx = 0;
@@ -273,11 +301,11 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
     // one decision for all consumer warps: stop at the end marker, or once any wait gave up
     if (consumers_any<kWarps>(aborted || desc[buf].b < 0)) break;
     const ItemDesc d = desc[buf];
-    const int* m = meta + buf * kMaxItemTiles;
+    const uint32_t* m = meta + buf * kMaxItemTiles;
     const int nu = (d.units + kUnitTiles - 1) / kUnitTiles;
     const uint8_t* qrow = qbuf + (buf * C::kCols + gi) * kQ4QRowBytes + 16 * ti;
 
-    float mx[kNT][2], l[kNT][2], cs[kNT][2];      // running maximum less kPShift, sum, score factor; columns 2ti, 2ti+1
+    float mx[kNT][2], l[kNT][2], cs[kNT][2];      // running maximum (rounded up) less kPShift, sum, score factor; columns 2ti, 2ti+1
     int seen[kNT][2];                             // kMulti: last position those columns see
     float o[kNT][8][4];
 #pragma unroll
@@ -293,9 +321,9 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
     }
     const int causal_lim = kMulti ? lens[d.b] - a.tokens : 0;
 
-    if (!prefetched && warp < nu &&
-        issue_unit(a, d, m, warp, my_stages + sidx * kStageQ4, &my_bars[sidx], lane, policy))
-      inflight |= 1u << sidx;
+    if (!prefetched && warp < nu)
+      inflight |= issue_unit(a.k_comp, m, d.units, warp, my_stages + sidx * kStageQ4, &my_bars[sidx], lane, policy)
+                  << (sidx * kUnitTiles);
     prefetched = false;
     if (!aborted && (*abort_flag || !mbar_wait(&q_full[buf], (k >> 1) & 1u, a.wait_limit_ns))) give_up();
     if (!aborted) {
@@ -311,35 +339,37 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
       const int ns = sidx ^ 1;
       uint8_t* next_stage = my_stages + ns * kStageQ4;
       if (un < nu) {
-        if (issue_unit(a, d, m, un, next_stage, &my_bars[ns], lane, policy)) inflight |= 1u << ns;
+        inflight |= issue_unit(a.k_comp, m, d.units, un, next_stage, &my_bars[ns], lane, policy) << (ns * kUnitTiles);
       } else {
         const int nb = buf ^ 1;       // the next item (or the end marker) is published after this one
         if (*abort_flag || !mbar_wait(&item_full[nb], ((k + 1) >> 1) & 1u, a.wait_limit_ns)) {
           give_up();
           break;
         } else if (desc[nb].b >= 0 && warp < (desc[nb].units + kUnitTiles - 1) / kUnitTiles) {
-          if (issue_unit(a, desc[nb], meta + nb * kMaxItemTiles, warp, next_stage, &my_bars[ns], lane, policy))
-            inflight |= 1u << ns;
+          inflight |= issue_unit(a.k_comp, meta + nb * kMaxItemTiles, desc[nb].units, warp, next_stage, &my_bars[ns], lane,
+                                 policy)
+                      << (ns * kUnitTiles);
           prefetched = true;
         }
       }
       // wait for the current unit (nothing armed: all its pages are bad, and it is skipped)
-      const bool armed = (inflight >> sidx) & 1u;
-      if (armed) {
+      const uint32_t here = (inflight >> (sidx * kUnitTiles)) & kAll;
+      if (here) {
         if (*abort_flag || !mbar_wait(&my_bars[sidx], (phase >> sidx) & 1u)) {
           give_up();
           break;
         }
         phase ^= 1u << sidx;
-        inflight &= ~(1u << sidx);
+        inflight &= ~(kAll << (sidx * kUnitTiles));
 
         const uint8_t* st = my_stages + sidx * kStageQ4;
-        int ntok[kUnitTiles];       // tokens of each record that count (0: past the item, or a bad page)
+        const int pos0 = d.t0 + 16 * kUnitTiles * u;         // position of the unit's first token
+        // whether every token counts for every column; if not, ntok[i] tokens of record i do (none of
+        // a bad page's)
+        const bool full = here == kAll && pos0 + 16 * kUnitTiles <= (kMulti ? min(d.t1, causal_lim + 1) : d.t1);
+        int ntok[kUnitTiles];
 #pragma unroll
-        for (int i = 0; i < kUnitTiles; ++i) {
-          const int t = u * kUnitTiles + i;
-          ntok[i] = t < d.units && (m[t] & 3) != kKindInvalid ? min(16, d.t1 - (d.t0 + 16 * t)) : 0;
-        }
+        for (int i = 0; i < kUnitTiles; ++i) ntok[i] = (here >> i) & 1u ? min(16, d.t1 - (pos0 + 16 * i)) : 0;
 
         // ---- S^T (16 tokens x 8 kNT columns) = K (16 x 128) . Q^T, per record
         float x[kNT][kUnitTiles][4];
@@ -396,24 +426,17 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
             x[n][i][3] *= cs[n][1];
           }
         }
+        if (!full) {
 #pragma unroll
-        for (int i = 0; i < kUnitTiles; ++i) {
-          if (ntok[i] < 16) {
+          for (int i = 0; i < kUnitTiles; ++i) {
+            const int pos = pos0 + 16 * i + gi;                // this lane's first token; the second is pos + 8
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
-              if (gi >= ntok[i]) x[n][i][0] = x[n][i][1] = -CUDART_INF_F;
-              if (gi + 8 >= ntok[i]) x[n][i][2] = x[n][i][3] = -CUDART_INF_F;
-            }
-          }
-          if (kMulti) {
-            const int pos = d.t0 + 16 * (u * kUnitTiles + i) + gi;       // this lane's first row; the second is pos + 8
-            if (pos - gi + 15 > causal_lim) {
 #pragma unroll
-              for (int n = 0; n < kNT; ++n) {
-                if (pos > seen[n][0]) x[n][i][0] = -CUDART_INF_F;
-                if (pos > seen[n][1]) x[n][i][1] = -CUDART_INF_F;
-                if (pos + 8 > seen[n][0]) x[n][i][2] = -CUDART_INF_F;
-                if (pos + 8 > seen[n][1]) x[n][i][3] = -CUDART_INF_F;
+              for (int e = 0; e < 2; ++e) {
+                const int last = kMulti ? seen[n][e] : INT_MAX;
+                if (gi >= ntok[i] || pos > last) x[n][i][e] = -CUDART_INF_F;
+                if (gi + 8 >= ntok[i] || pos + 8 > last) x[n][i][e + 2] = -CUDART_INF_F;
               }
             }
           }
@@ -438,7 +461,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
               float v = top[n][e];
 #pragma unroll
               for (int dd = 4; dd < 32; dd <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, dd));
-              const float mn = fmaxf(mx[n][e], v - kPShift);      // finite: kNoScore at least
+              const float mn = fmaxf(mx[n][e], ceilf(v) - kPShift);      // finite: kNoScore at least
               al[e] = fast_exp2(mx[n][e] - mn);
               mx[n][e] = mn;
               l[n][e] *= al[e];
@@ -477,7 +500,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           // channel 16 gi + 2 mt, row gi + 8 the next one; k: tokens 2ti, 2ti+1, 2ti+8, 2ti+9.
           const uint8_t* rec = st + i * kQ4Record;
           uint32_t w = *reinterpret_cast<const uint32_t*>(rec + kQ4VScales + 16 * gi + 4 * ti) & 0x7F7F7F7Fu;
-          if (ntok[i] < 16) {       // what lies past the context counts as 0
+          if (!full) {              // what lies past the context counts as 0
             w &= (2 * ti < ntok[i] ? 0x000000FFu : 0u) | (2 * ti + 1 < ntok[i] ? 0x0000FF00u : 0u) |
                  (2 * ti + 8 < ntok[i] ? 0x00FF0000u : 0u) | (2 * ti + 9 < ntok[i] ? 0xFF000000u : 0u);
           }
@@ -566,22 +589,13 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           acc.z += f * v.z;
           acc.w += f * v.w;
         }
-        const float inv = lsum == 0.f ? 0.f : v_factor / lsum;           // a NaN sum stays a NaN
-        acc.x *= inv;
-        acc.y *= inv;
-        acc.z *= inv;
-        acc.w *= inv;
         const size_t bh = static_cast<size_t>(d.b) * a.hq + d.h0 + 8 * n + hh;
         if (d.single) {
-          const size_t row = query_row(d.b, d.h0 + 8 * n + hh, a.tokens, a.hq);
-          *reinterpret_cast<float4*>(a.out + row * ZF_HEAD_DIM + 4 * lane) = acc;
-          if (lane == 0) a.lse[row] = lsum == 0.f ? -CUDART_INF_F : (M + log2f(lsum)) * kLn2;
+          finish_row(a.out, a.lse, query_row(d.b, d.h0 + 8 * n + hh, a.tokens, a.hq), lane, acc, M, lsum, v_factor);
         } else {
           const size_t pidx = bh * a.max_chunks + d.c;
           *reinterpret_cast<float4*>(a.part_o + pidx * ZF_HEAD_DIM + 4 * lane) = acc;
-          // a NaN partial counts as +inf for the merge, whose weights and sum then are NaN
-          if (lane == 0)
-            a.part_lse[pidx] = lsum == 0.f ? -CUDART_INF_F : lsum == lsum ? M + log2f(lsum) : CUDART_INF_F;
+          if (lane == 0) reinterpret_cast<float2*>(a.part_lse)[pidx] = make_float2(M, lsum);
         }
       }
       consumers_sync<kWarps>();
@@ -591,7 +605,62 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   }
   // copies still in flight (only after a wait gave up) must land before the CTA exits
   for (int st = 0; st < kWarpStages; ++st)
-    if (inflight & (1u << st)) mbar_wait(&my_bars[st], (phase >> st) & 1u);
+    if ((inflight >> (st * kUnitTiles)) & kAll) mbar_wait(&my_bars[st], (phase >> st) & 1u);
+}
+
+// The merge: one warp per (request, query head, new token).  A partial holds its weighted sum of values as
+// it is, its maximum and its sum; the maxima are whole numbers, so the partials' factors are powers of
+// two and the merge adds no rounding but those of its sums (a log-sum-exp near 20, kept as one float,
+// would be off by 2^-20 in each weight).  Rows with one partial were finished by the attention
+// kernel.  The first 32 maxima and kMergePre partial outputs are loaded along with the partial count
+// (entries past the count hold anything and are not used).
+constexpr int kMergePre = 8;
+constexpr int kQ4MergeWarps = 2;
+__global__ void __launch_bounds__(kQ4MergeWarps * 32) q4_merge_kernel(const MergeArgs a, const float v_factor) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  allow_next_grid();
+  wait_prior_grid();
+  const int idx = blockIdx.x * kQ4MergeWarps + warp;
+  if (idx >= a.batch * a.hq) return;
+  const int b = idx / a.hq, h = idx - b * a.hq;
+  const int gq = h / a.group;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_lse) + static_cast<size_t>(idx) * a.max_chunks;
+  const float4* po = reinterpret_cast<const float4*>(a.part_o + static_cast<size_t>(idx) * a.max_chunks * ZF_HEAD_DIM) + lane;
+  const float2 first = lane < a.max_chunks ? ml[lane] : make_float2(kNoScore, 0.f);
+  float4 pre[kMergePre];
+#pragma unroll
+  for (int j = 0; j < kMergePre; ++j)
+    pre[j] = j < a.max_chunks ? po[static_cast<size_t>(j) * (ZF_HEAD_DIM / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+  const int nch = a.chunk_counts[(b * (a.hq / a.group) + gq) * a.slices + (h - gq * a.group) / a.hps];
+  if (nch == 1) return;
+  float M = lane < nch ? first.x : kNoScore;
+  for (int i = lane + 32; i < nch; i += 32) M = fmaxf(M, ml[i].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, d));
+  const float w0 = lane < nch ? fast_exp2(first.x - M) : 0.f;
+  float sum = lane < nch ? w0 * first.y : 0.f;
+  for (int i = lane + 32; i < nch; i += 32) sum += fast_exp2(ml[i].x - M) * ml[i].y;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float f, const float4& v) {
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  };
+#pragma unroll
+  for (int j = 0; j < kMergePre; ++j) {
+    const float f = __shfl_sync(0xFFFFFFFFu, w0, j);
+    if (j < nch) add(f, pre[j]);
+  }
+  for (int c0 = 0; c0 < nch; c0 += 32) {
+    const float w = c0 == 0 ? w0 : (c0 + lane < nch ? fast_exp2(ml[c0 + lane].x - M) : 0.f);
+    const int n = min(32, nch - c0);
+    for (int j = c0 == 0 ? kMergePre : 0; j < n; ++j)
+      add(__shfl_sync(0xFFFFFFFFu, w, j), po[static_cast<size_t>(c0 + j) * (ZF_HEAD_DIM / 4)]);
+  }
+  finish_row(a.out, a.lse, query_row(b, h, a.tokens, a.hq), lane, acc, M, sum, v_factor);
 }
 
 // 8-column tiles per pass: 1, 2 or 4 (the kernel reads a kv head's records once per 8, 16 or 32 columns).
@@ -599,7 +668,11 @@ int q4_col_tiles(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 
 template <int kNT>
 Plan q4_plan_nt(int batch, int hq, int hkv, int page_size, int max_pages, int sms) {
-  return make_plan(batch, hq, hkv, page_size, max_pages, sms, Q4Cfg<kNT>::kWarps, 8 * kNT);
+  Plan p = make_plan(batch, hq, hkv, page_size, max_pages, sms, Q4Cfg<kNT>::kWarps, 8 * kNT);
+  const size_t lse = p.part_lse_bytes;               // a partial keeps two floats (maximum and sum) there
+  p.part_lse_bytes = (static_cast<size_t>(batch) * hq * p.max_chunks * 8 + 255) & ~static_cast<size_t>(255);
+  p.ws_bytes += p.part_lse_bytes - lse;
+  return p;
 }
 
 Plan q4_plan(int batch, int hq, int hkv, int page_size, int max_pages, int sms) {
@@ -665,7 +738,9 @@ extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, 
   // the scores' factor, with the cache's scale and the scale decoding's 2^-8 in it, must be a float
   const float scale_log2 = softmax_scale * c->k_scale * (1.4426950408889634f * kQ4ScaleFactor);
   if (!(scale_log2 >= -1e37f && scale_log2 <= 1e37f)) return ZF_ERR_INVALID_ARGUMENT;
-  if (c->num_pages >= (1 << 26)) return ZF_ERR_UNSUPPORTED;       // record entries pack a page id into 26 bits
+  // the kernel numbers records with 32 bits
+  if (static_cast<unsigned long long>(c->num_pages) * c->num_kv_heads * (c->page_size / 16) >= kNoRecord)
+    return ZF_ERR_UNSUPPORTED;
   int sms = 0;
   if ((st = current_sm_count(&sms)) != ZF_OK) return st;
   const int32_t hq = num_q_heads * tokens;
@@ -693,12 +768,10 @@ extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, 
   a.slices = p.slices;
   a.page_size = c->page_size;
   a.num_pages = c->num_pages;
-  a.num_raw = c->num_pages;             // what resolve_tiles<false> bounds page ids by
   a.max_pages = max_pages;
   a.max_chunks = p.max_chunks;
   a.min_range_pages = p.min_range_pages;
   a.chunk_pages = p.chunk_pages;
-  a.comp_head_bytes = static_cast<int64_t>(c->page_size / 16) * kQ4Record;
   a.scale_log2 = scale_log2;
   a.wait_limit_ns = kWaitTimeoutNs;
   const float v_factor = c->v_scale * kQ4ScaleFactor;
@@ -723,5 +796,15 @@ extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, 
   m.max_chunks = p.max_chunks;
   m.tokens = tokens;
   m.hps = a.hps;
-  return launch_merge(m, multi, s);
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  const int rows = batch * hq;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((rows + kQ4MergeWarps - 1) / kQ4MergeWarps);
+  cfg.blockDim = dim3(kQ4MergeWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, q4_merge_kernel, m, v_factor) == cudaSuccess ? ZF_OK : ZF_ERR_CUDA;
 }

@@ -481,81 +481,118 @@ def decode_attn_static(cache: Cache, q, page_table, seq_lens, scale=None, out=No
 
 
 # ------------------------------------------------------------------ the 4-bit cache (zf_q4_*)
+def _tensor(t, name, dtypes, device, shape, write=False):
+    """`t` checked for dtype, device and exact shape; contiguous (a tensor written in place has to be)."""
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.device == device and t.shape == shape:
+        if t.is_contiguous():
+            return t
+        if not write:
+            return t.contiguous()
+        raise ValueError(f"{name} must be contiguous (it is written in place)")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name}: shape {list(t.shape)}, expected {list(shape)}")
+
+
+_I32, _F32 = (torch.int32,), (torch.float32,)
+
+
+def _launch_stream(stream, device) -> int:
+    """The stream to launch on, its own device being the current one (the kernels take that device's pointers)."""
+    if device.type != "cuda":
+        raise ValueError(f"the tensors are on {device}: a CUDA device is needed")
+    current = torch.cuda.current_device()
+    if device.index != current:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{current}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(current)
+    return stream.cuda_stream
+
+
 class Q4Cache:
     """One layer's 4-bit paged cache in device memory (layout and numbers: include/zf.h, zf_q4).
 
     records: [num_pages][Hkv][P/16][2304] uint8, given or allocated (zeros: every token reads as 0);
     status: one int32 device word.  k_scale / v_scale multiply the stored values (1 suits values up
-    to about 2688).
+    to about 2688).  Sizes, scales and tensors are fixed once made.
     """
 
     def __init__(self, num_pages, num_kv_heads, page_size, device="cuda", k_scale=1.0, v_scale=1.0, records=None):
-        self.num_pages, self.num_kv_heads, self.page_size = num_pages, num_kv_heads, page_size
-        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
         shape = (num_pages, num_kv_heads, page_size // 16, Q4_RECORD_BYTES)
         if records is None:
             records = torch.zeros(shape, dtype=torch.uint8, device=torch.device(device))
-        elif records.dtype != torch.uint8 or tuple(records.shape) != shape or not records.is_contiguous():
-            raise ValueError(f"records must be contiguous uint8 of shape {list(shape)}")
-        self.records = records
-        self.status = torch.zeros(1, dtype=torch.int32, device=records.device)
+        else:
+            _tensor(records, "records", (torch.uint8,), getattr(records, "device", None), shape, write=True)
+        self._sizes = (num_pages, num_kv_heads, page_size, float(k_scale), float(v_scale))
+        self._records, self._device = records, records.device
+        self._status = torch.zeros(1, dtype=torch.int32, device=records.device)
+        self._desc = ZfQ4CacheDesc(num_pages, num_kv_heads, HEAD_DIM, page_size, float(k_scale), float(v_scale),
+                                   _ptr(records), _ptr(self._status))
+        self._ref = ctypes.byref(self._desc)
 
-    @property
-    def device(self):
-        return self.status.device
+    num_pages = property(lambda self: self._sizes[0])
+    num_kv_heads = property(lambda self: self._sizes[1])
+    page_size = property(lambda self: self._sizes[2])
+    k_scale = property(lambda self: self._sizes[3])
+    v_scale = property(lambda self: self._sizes[4])
+    records = property(lambda self: self._records)
+    status = property(lambda self: self._status)
+    device = property(lambda self: self._device)
 
     def desc(self) -> ZfQ4CacheDesc:
-        return ZfQ4CacheDesc(self.num_pages, self.num_kv_heads, HEAD_DIM, self.page_size, self.k_scale, self.v_scale,
-                             _ptr(self.records), _ptr(self.status))
+        return self._desc
 
     def status_word(self) -> int:
-        return int(self.status.item())
+        return int(self._status.item())
 
     def stored_bytes(self) -> int:
-        return self.records.numel()
+        return self._records.numel()
+
+
+def _places(cache, page_ids, positions):
+    """Index lists of a call as int32 device tensors of one length."""
+    out = []
+    for name, x in (("page_ids", page_ids), ("positions", positions)):
+        if not (isinstance(x, torch.Tensor) and x.dtype == torch.int32 and x.device == cache._device):
+            x = torch.as_tensor(x, dtype=torch.int32, device=cache._device)
+        if x.dim() != 1:
+            raise ValueError(f"{name}: shape {list(x.shape)}, expected one dimension")
+        out.append(x if x.is_contiguous() else x.contiguous())
+    if out[0].shape != out[1].shape:
+        raise ValueError(f"positions: {out[1].numel()} entries for {out[0].numel()} tokens")
+    return out
 
 
 def q4_write_tokens(cache: Q4Cache, k_tok, v_tok, page_ids, positions, stream=None):
     """zf_q4_write_tokens: k_tok/v_tok [n][Hkv][128] int16 BF16 bits (or bfloat16) on the device; entry i
     is token positions[i] of page page_ids[i] (position -1: skipped).  Returns the index tensors (keep
     them alive until the stream has consumed them)."""
-    k_tok = _arg(k_tok, "k_tok", cache, _BITS16, (None, cache.num_kv_heads, HEAD_DIM))
-    v_tok = _arg(v_tok, "v_tok", cache, _BITS16, tuple(k_tok.shape))
-    n = int(k_tok.shape[0])
-    ids, pos = _places(cache, page_ids, positions, n)
-    _on_current(cache.device)
-    d = cache.desc()
-    _check("zf_q4_write_tokens", lib().zf_q4_write_tokens(ctypes.byref(d), _ptr(k_tok), _ptr(v_tok), _ptr(ids),
-                                                           _ptr(pos), n, _stream(stream)))
+    ids, pos = _places(cache, page_ids, positions)
+    n = ids.shape[0]
+    shape = (n, cache._sizes[1], HEAD_DIM)
+    k_tok = _tensor(k_tok, "k_tok", _BITS16, cache._device, shape)
+    v_tok = _tensor(v_tok, "v_tok", _BITS16, cache._device, shape)
+    s = _launch_stream(stream, cache._device)
+    code = lib().zf_q4_write_tokens(cache._ref, k_tok.data_ptr(), v_tok.data_ptr(), ids.data_ptr(), pos.data_ptr(), n, s)
+    if code:
+        _check("zf_q4_write_tokens", code)
     return ids, pos
 
 
 def q4_read_tokens(cache: Q4Cache, page_ids, positions, stream=None):
     """zf_q4_read_tokens: the values held at the listed places, (k, v) [n][Hkv][128] int16 BF16 bits."""
-    n = _count(page_ids)
-    ids, pos = _places(cache, page_ids, positions, n)
-    _on_current(cache.device)
-    k = torch.empty((n, cache.num_kv_heads, HEAD_DIM), dtype=torch.int16, device=cache.device)
-    v = torch.empty_like(k)
-    d = cache.desc()
-    _check("zf_q4_read_tokens", lib().zf_q4_read_tokens(ctypes.byref(d), _ptr(ids), _ptr(pos), n, _ptr(k), _ptr(v),
-                                                         _stream(stream)))
+    ids, pos = _places(cache, page_ids, positions)
+    n = ids.shape[0]
+    s = _launch_stream(stream, cache._device)
+    k, v = torch.empty((2, n, cache._sizes[1], HEAD_DIM), dtype=torch.int16, device=cache._device).unbind(0)
+    code = lib().zf_q4_read_tokens(cache._ref, ids.data_ptr(), pos.data_ptr(), n, k.data_ptr(), v.data_ptr(), s)
+    if code:
+        _check("zf_q4_read_tokens", code)
     return k, v
-
-
-def _on_current(device):
-    """The kernels run on the current CUDA device and take its pointers."""
-    if device.type != "cuda":
-        raise ValueError(f"the tensors are on {device}: a CUDA device is needed")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-
-
-def _places(cache, page_ids, positions, n):
-    for name, x in (("page_ids", page_ids), ("positions", positions)):
-        if _count(x) != n:
-            raise ValueError(f"{name}: {_count(x)} entries for {n} tokens")
-    return _dev_i32(page_ids, cache.device), _dev_i32(positions, cache.device)
 
 
 def q4_workspace_size(batch, tokens, num_q_heads, num_kv_heads, page_size, max_pages) -> int:
@@ -567,26 +604,28 @@ def q4_decode_attn(cache: Q4Cache, q, page_table, seq_lens, scale=None, out=None
     """zf_q4_decode_attn: decode attention over the 4-bit cache.  q [B][Hq][128], or [B][T][Hq][128] for T
     new tokens per request (token t attends to positions 0 .. seq_lens[b] - T + t), int16 BF16 bits or
     bfloat16.  Returns (out f32 of q's shape, lse f32 without the last dimension)."""
-    q = _arg(q, "q", cache, _BITS16)
-    if q.dim() not in (3, 4) or q.shape[-1] != HEAD_DIM:
-        raise ValueError(f"q: shape {list(q.shape)}, expected [*][*][{HEAD_DIM}] or [*][*][*][{HEAD_DIM}]")
-    shape = tuple(q.shape)
+    dev = cache._device
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    shape = q.shape
+    if len(shape) not in (3, 4) or shape[-1] != HEAD_DIM:
+        raise ValueError(f"q: shape {list(shape)}, expected [*][*][{HEAD_DIM}] or [*][*][*][{HEAD_DIM}]")
+    q = _tensor(q, "q", _BITS16, dev, shape)
     B, T, Hq = (shape[0], 1, shape[1]) if len(shape) == 3 else shape[:3]
     page_table, seq_lens = _attn_args(cache, q, page_table, seq_lens, B)
-    max_pages = int(page_table.shape[1])
-    scale = 1.0 / math.sqrt(HEAD_DIM) if scale is None else scale
-    dev = cache.device
-    out = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else _result(out, "out", cache, shape)
+    max_pages = page_table.shape[1]
+    out = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else \
+        _tensor(out, "out", _F32, dev, shape, write=True)
     lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if lse is None else \
-        _result(lse, "lse", cache, shape[:-1])
-    _on_current(dev)
+        _tensor(lse, "lse", _F32, dev, shape[:-1], write=True)
+    s = _launch_stream(stream, dev)
     if workspace is None:
-        workspace = new_workspace(q4_workspace_size(B, T, Hq, cache.num_kv_heads, cache.page_size, max_pages), dev)
-    d = cache.desc()
-    _check("zf_q4_decode_attn",
-           lib().zf_q4_decode_attn(ctypes.byref(d), _ptr(q), B, T, Hq, _ptr(page_table), max_pages, _ptr(seq_lens), scale,
-                                   _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                   _stream(stream)))
+        workspace = new_workspace(q4_workspace_size(B, T, Hq, cache._sizes[1], cache._sizes[2], max_pages), dev)
+    code = lib().zf_q4_decode_attn(cache._ref, q.data_ptr(), B, T, Hq, page_table.data_ptr(), max_pages,
+                                   seq_lens.data_ptr(), 1.0 / math.sqrt(HEAD_DIM) if scale is None else scale,
+                                   out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, s)
+    if code:
+        _check("zf_q4_decode_attn", code)
     return out, lse
 
 
@@ -604,21 +643,6 @@ class TokenMap(NamedTuple):
     seq_positions: torch.Tensor
 
 
-def _ints(t, name, like, shape, write=False):
-    """An int32 argument on the device of `like`, a tensor; written in place when `write`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {list(t.shape)}, expected {list(shape)}")
-    if write and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (it is written in place)")
-    return t.contiguous()
-
-
 def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_pos, page_size, max_tokens, out=None,
                status=None, stream=None) -> TokenMap:
     """zf_map_tokens: places for new_tokens[b] tokens of every request b, on the GPU.  page_table [B][max_pages]
@@ -627,42 +651,35 @@ def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_po
     free_pos may be the arguments themselves); status: an int32 device word."""
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a [batch][max_pages] tensor")
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a one-dimensional tensor")
     B, max_pages = page_table.shape
-    page_table = _ints(page_table, "page_table", page_table, (B, max_pages), write=True)
-    seq_lens = _ints(seq_lens, "seq_lens", page_table, (B,))
-    pages_held = _ints(pages_held, "pages_held", page_table, (B,))
-    new_tokens = _ints(new_tokens, "new_tokens", page_table, (B,))
-    free_pages = _ints(free_pages, "free_pages", page_table, (_count(free_pages),))
-    free_pos = _ints(free_pos, "free_pos", page_table, (1,))
-    max_tokens = int(max_tokens)
-    shapes = ((B,), (B,), (1,), (B + 1,), (max(max_tokens, 0),), (max(max_tokens, 0),), (max(max_tokens, 0),))
+    dev = page_table.device
+    page_table = _tensor(page_table, "page_table", _I32, dev, (B, max_pages), write=True)
+    seq_lens = _tensor(seq_lens, "seq_lens", _I32, dev, (B,))
+    pages_held = _tensor(pages_held, "pages_held", _I32, dev, (B,))
+    new_tokens = _tensor(new_tokens, "new_tokens", _I32, dev, (B,))
+    free_pages = _tensor(free_pages, "free_pages", _I32, dev, free_pages.shape)
+    free_pos = _tensor(free_pos, "free_pos", _I32, dev, (1,))
+    n = max(int(max_tokens), 0)
     if out is None:
-        out = TokenMap(*(torch.empty(s, dtype=torch.int32, device=page_table.device) for s in shapes))
+        pad = -n % 4                         # the lists start on 16-byte boundaries
+        p = torch.empty(3 * (n + pad) + 3 * B + 2, dtype=torch.int32, device=dev) \
+            .split((n, pad, n, pad, n, pad, B, B, B + 1, 1))
+        out = TokenMap(p[6], p[7], p[9], p[8], p[0], p[2], p[4])
     else:
-        out = TokenMap(*(_ints(t, f"out.{name}", page_table, s, write=True)
+        shapes = ((B,), (B,), (1,), (B + 1,), (n,), (n,), (n,))
+        out = TokenMap(*(_tensor(t, "out." + name, _I32, dev, s, write=True)
                          for t, name, s in zip(out, TokenMap._fields, shapes)))
-    if status is not None:
-        status = _ints(status, "status", page_table, (1,), write=True)
-    _on_current(page_table.device)
-    _check("zf_map_tokens",
-           lib().zf_map_tokens(B, int(page_size), max_pages, _ptr(seq_lens), _ptr(pages_held), _ptr(new_tokens),
-                               _ptr(page_table), _ptr(free_pages), _count(free_pages), _ptr(free_pos),
-                               _ptr(out.seq_lens), _ptr(out.pages_held), _ptr(out.free_pos), _ptr(out.token_start),
-                               _ptr(out.page_ids), _ptr(out.positions), _ptr(out.seq_positions), max_tokens,
-                               _ptr(status), _stream(stream)))
+    word = None if status is None else _tensor(status, "status", _I32, dev, (1,), write=True).data_ptr()
+    s = _launch_stream(stream, dev)
+    code = lib().zf_map_tokens(B, page_size, max_pages, seq_lens.data_ptr(), pages_held.data_ptr(), new_tokens.data_ptr(),
+                               page_table.data_ptr(), free_pages.data_ptr(), free_pages.shape[0], free_pos.data_ptr(),
+                               out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+                               out[4].data_ptr(), out[5].data_ptr(), out[6].data_ptr(), max_tokens, word, s)
+    if code:
+        _check("zf_map_tokens", code)
     return out
-
-
-def _floats(t, name, like, shape):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.float32:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.float32")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {list(t.shape)}, expected {list(shape)}")
-    return t.contiguous()
 
 
 def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_drafts=None, seq_lens=None,
@@ -677,28 +694,31 @@ def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_draft
     B, T = draft_tokens.shape
     if not isinstance(target_probs, torch.Tensor) or target_probs.dim() != 3:
         raise ValueError("target_probs must be a [batch][drafts + 1][vocab] tensor")
-    V = target_probs.shape[2]
-    draft_tokens = _ints(draft_tokens, "draft_tokens", draft_tokens, (B, T))
-    target_probs = _floats(target_probs, "target_probs", draft_tokens, (B, T + 1, V))
-    uniform = _floats(uniform, "uniform", draft_tokens, (B, T + 1))
+    V, dev = target_probs.shape[2], draft_tokens.device
+    draft_tokens = _tensor(draft_tokens, "draft_tokens", _I32, dev, (B, T))
+    target_probs = _tensor(target_probs, "target_probs", _F32, dev, (B, T + 1, V))
+    uniform = _tensor(uniform, "uniform", _F32, dev, (B, T + 1))
+    q = n = before = after = word = None
     if draft_probs is not None:
-        draft_probs = _floats(draft_probs, "draft_probs", draft_tokens, (B, T, V))
+        draft_probs = _tensor(draft_probs, "draft_probs", _F32, dev, (B, T, V))
+        q = draft_probs.data_ptr()
     if n_drafts is not None:
-        n_drafts = _ints(n_drafts, "n_drafts", draft_tokens, (B,))
+        n_drafts = _tensor(n_drafts, "n_drafts", _I32, dev, (B,))
+        n = n_drafts.data_ptr()
     if (seq_lens is None) != (new_seq_lens is None):
         raise ValueError("seq_lens and new_seq_lens go together")
     if seq_lens is not None:
-        new_seq_lens = _ints(new_seq_lens, "new_seq_lens", draft_tokens, (B,), write=True)
-        seq_lens = _ints(seq_lens, "seq_lens", draft_tokens, (B,))
+        seq_lens = _tensor(seq_lens, "seq_lens", _I32, dev, (B,))
+        before, after = seq_lens.data_ptr(), _tensor(new_seq_lens, "new_seq_lens", _I32, dev, (B,), write=True).data_ptr()
     if status is not None:
-        status = _ints(status, "status", draft_tokens, (1,), write=True)
-    _on_current(draft_tokens.device)
-    accepted = torch.empty(B, dtype=torch.int32, device=draft_tokens.device)
-    tokens = torch.empty((B, T + 1), dtype=torch.int32, device=draft_tokens.device)
-    _check("zf_verify_drafts",
-           lib().zf_verify_drafts(B, T, V, _ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(n_drafts),
-                                  _ptr(uniform), _ptr(accepted), _ptr(tokens), _ptr(seq_lens), _ptr(new_seq_lens),
-                                  _ptr(status), _stream(stream)))
+        word = _tensor(status, "status", _I32, dev, (1,), write=True).data_ptr()
+    s = _launch_stream(stream, dev)
+    accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    tokens = torch.empty((B, T + 1), dtype=torch.int32, device=dev)
+    code = lib().zf_verify_drafts(B, T, V, target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, uniform.data_ptr(),
+                                  accepted.data_ptr(), tokens.data_ptr(), before, after, word, s)
+    if code:
+        _check("zf_verify_drafts", code)
     return accepted, tokens
 
 

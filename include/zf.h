@@ -404,7 +404,7 @@ zf_status zf_decode_attn_static(const zf_cache* cache, const uint16_t* q, int32_
  *   [2176,2304)  V scales: token j, block c at 2176 + 16 c + 4 (j%8/2) + 2 (j/8) + j%2
  * ------------------------------------------------------------------------------------------ */
 typedef struct zf_q4_cache {
-  int32_t num_pages;      /* page ids are in [0, num_pages); below 2^26 for zf_q4_decode_attn */
+  int32_t num_pages;      /* page ids are in [0, num_pages) */
   int32_t num_kv_heads;
   int32_t head_dim;       /* must be 128 */
   int32_t page_size;      /* tokens per page, multiple of 16, <= ZF_MAX_PAGE_SIZE */
