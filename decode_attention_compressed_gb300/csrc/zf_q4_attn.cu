@@ -97,11 +97,16 @@ __device__ __forceinline__ bool consumers_any(bool v) {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8x8 transpose of 16-bit values (as transpose8x8, free to move between other instructions).
+__device__ __forceinline__ uint32_t flip8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -490,10 +495,10 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
               l[n][r & 1] += p[r];
               hi[r] = __uint_as_float(__float_as_uint(p[r]) & 0xFFFFE000u);
             }
-            bh[n][0] = transpose8x8(pack_f16x2(hi[0], hi[1]));
-            bh[n][1] = transpose8x8(pack_f16x2(hi[2], hi[3]));
-            bl[n][0] = transpose8x8(pack_f16x2(p[0] - hi[0], p[1] - hi[1]));
-            bl[n][1] = transpose8x8(pack_f16x2(p[2] - hi[2], p[3] - hi[3]));
+            bh[n][0] = flip8x8(pack_f16x2(hi[0], hi[1]));
+            bh[n][1] = flip8x8(pack_f16x2(hi[2], hi[3]));
+            bl[n][0] = flip8x8(pack_f16x2(p[0] - hi[0], p[1] - hi[1]));
+            bl[n][1] = flip8x8(pack_f16x2(p[2] - hi[2], p[3] - hi[3]));
           }
 
           // ---- O^T (128 channels x columns) += V^T (128 x 16 tokens) . P^T.  m-tile mt: row gi is
