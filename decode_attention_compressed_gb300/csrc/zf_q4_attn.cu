@@ -39,6 +39,7 @@ namespace {
 constexpr int kUnitTiles = 2;                            // records per stage
 constexpr int kStageQ4 = kUnitTiles * kQ4Record;         // 4608
 constexpr int kQ4QRowBytes = 320;                        // q row in shared memory (see q_at)
+constexpr int kItemTilesQ4 = 2048;                       // records (and pages) of the largest item
 constexpr float kPShift = 7.f;                           // weights are 2^7 times their usual size
 static_assert(kStageQ4 >= (8 * kOStride + 16) * 4, "a stage holds a warp's combine state of 8 columns");
 
@@ -65,7 +66,7 @@ __host__ __device__ inline Q4Smem q4_smem(int batch) {
   s.item_empty = at; at += 2 * 8;
   s.misc = at; at += 16 + 16 * 4;               // [0] abort flag, [16..] combine stage per warp
   s.desc = at; at += 2 * 64;
-  s.meta = at; at += 2 * kMaxItemTiles * 4;
+  s.meta = at; at += 2 * kItemTilesQ4 * 4;
   s.qbuf = at; at += 2 * C::kCols * kQ4QRowBytes;
   s.qscale = at; at += 2 * C::kCols * 4;
   s.bars = at; at += static_cast<size_t>(C::kWarps) * kWarpStages * 8;
@@ -109,6 +110,29 @@ __device__ __forceinline__ uint32_t flip8x8(uint32_t x) {
   return y;
 }
 
+// Two floats in a register pair, and the packed additions and fused multiply-adds on them.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -121,18 +145,21 @@ constexpr uint32_t kNoRecord = 0xFFFFFFFFu;
 __device__ __forceinline__ void resolve_records(const AttnArgs& a, const ItemDesc& d, uint32_t* rec, int lane) {
   const int tpp = a.page_size >> 4;
   const int32_t* row = a.page_table + static_cast<size_t>(d.b) * a.max_pages + d.pg0;
-  int pid[kPagesPerLane];
+  constexpr int kAhead = 8;            // page-table entries per lane read at once
+  for (int i0 = lane; i0 < d.npg; i0 += 32 * kAhead) {
+    int pid[kAhead];
 #pragma unroll
-  for (int k = 0; k < kPagesPerLane; ++k) pid[k] = lane + 32 * k < d.npg ? row[lane + 32 * k] : -1;
+    for (int k = 0; k < kAhead; ++k) pid[k] = i0 + 32 * k < d.npg ? row[i0 + 32 * k] : -1;
 #pragma unroll
-  for (int k = 0; k < kPagesPerLane; ++k) {
-    const int i = lane + 32 * k;
-    if (i >= d.npg) break;
-    const bool ok = pid[k] >= 0 && pid[k] < a.num_pages;
-    if (!ok) report(a.status, ZF_DEV_BAD_PAGE_ID);
-    const uint32_t first = (static_cast<uint32_t>(pid[k]) * a.hkv + d.g) * tpp;
-    for (int t = 0; t < tpp; ++t)
-      if (i * tpp + t < d.units) rec[i * tpp + t] = ok ? first + t : kNoRecord;
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + 32 * k;
+      if (i >= d.npg) break;
+      const bool ok = pid[k] >= 0 && pid[k] < a.num_pages;
+      if (!ok) report(a.status, ZF_DEV_BAD_PAGE_ID);
+      const uint32_t first = (static_cast<uint32_t>(pid[k]) * a.hkv + d.g) * tpp;
+      for (int t = 0; t < tpp; ++t)
+        if (i * tpp + t < d.units) rec[i * tpp + t] = ok ? first + t : kNoRecord;
+    }
   }
 }
 
@@ -156,12 +183,12 @@ __device__ __forceinline__ uint32_t issue_unit(const uint8_t* records, const uin
 // a power of two that brings its largest exponent to 11; returns the inverse factor.  Channel c =
 // 32 t + 8 j + e goes to byte 64 j + 16 t + 2 e: lane t's words of k-steps 2j, 2j+1 are 16 bytes,
 // and the rows' stride spreads a warp's reads over the banks.
-__device__ __forceinline__ float store_q_row(uint8_t* row, int lane, uint32_t w0, uint32_t w1) {
+__device__ __forceinline__ float store_q_row(uint8_t* row, int lane, uint32_t w0, uint32_t w1, bool negate) {
   const uint32_t m0 = w0 & 0x7FFF7FFFu, m1 = w1 & 0x7FFF7FFFu;
   const uint32_t big = max(max(m0 & 0xFFFFu, m0 >> 16), max(m1 & 0xFFFFu, m1 >> 16));
   const int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, big) >> 7);        // biased exponent
   const int k = min(138 - e, 126);
-  const float f = __int_as_float((127 + k) << 23);
+  const float f = __int_as_float(((127 + k) << 23) | (negate ? 0x80000000 : 0));
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t w = h ? w1 : w0;
@@ -187,8 +214,9 @@ __device__ __forceinline__ void stage_q(const AttnArgs& a, const ItemDesc& d, ui
     }
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const float inv = store_q_row(qb + (r0 + r) * kQ4QRowBytes, lane, v[r][0], v[r][1]);
-      if (lane == 0) qs[r0 + r] = inv * a.scale_log2;
+      const float inv = store_q_row(qb + (r0 + r) * kQ4QRowBytes, lane, v[r][0], v[r][1], a.scale_log2 < 0.f);
+      // positive, so that the largest raw score has the largest score, and -inf stays one
+      if (lane == 0) qs[r0 + r] = fmaxf(inv * fabsf(a.scale_log2), 1e-37f);
     }
   }
 }
@@ -238,7 +266,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   allow_next_grid();
   const uint64_t policy = l2_evict_first_policy();
   load_lengths<false, C::kThreads>(a, prefix, lens, tid);       // ends with a barrier (also for the barriers above)
-  const Ranges g = make_ranges(a, HS * prefix[a.batch]);
+  const Ranges g = make_ranges<kItemTilesQ4, kItemTilesQ4>(a, HS * prefix[a.batch]);
 
   if (warp == kWarps) {
     // ============================================================== metadata warp
@@ -256,7 +284,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         }
         return false;
       }
-      if (d.b >= 0) resolve_records(a, d, meta + buf * kMaxItemTiles, lane);
+      if (d.b >= 0) resolve_records(a, d, meta + buf * kItemTilesQ4, lane);
       __syncwarp();
       if (lane == 0) {
         desc[buf] = d;
@@ -306,7 +334,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
     // one decision for all consumer warps: stop at the end marker, or once any wait gave up
     if (consumers_any<kWarps>(aborted || desc[buf].b < 0)) break;
     const ItemDesc d = desc[buf];
-    const uint32_t* m = meta + buf * kMaxItemTiles;
+    const uint32_t* m = meta + buf * kItemTilesQ4;
     const int nu = (d.units + kUnitTiles - 1) / kUnitTiles;
     const uint8_t* qrow = qbuf + (buf * C::kCols + gi) * kQ4QRowBytes + 16 * ti;
 
@@ -351,7 +379,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           give_up();
           break;
         } else if (desc[nb].b >= 0 && warp < (desc[nb].units + kUnitTiles - 1) / kUnitTiles) {
-          inflight |= issue_unit(a.k_comp, meta + nb * kMaxItemTiles, desc[nb].units, warp, next_stage, &my_bars[ns], lane,
+          inflight |= issue_unit(a.k_comp, meta + nb * kItemTilesQ4, desc[nb].units, warp, next_stage, &my_bars[ns], lane,
                                  policy)
                       << (ns * kUnitTiles);
           prefetched = true;
@@ -421,16 +449,6 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
 
         // ---- online softmax, log2 domain.  lane: tokens gi, gi + 8 x columns 2ti, 2ti + 1 (per n)
         bool grow = false;
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-#pragma unroll
-          for (int i = 0; i < kUnitTiles; ++i) {
-            x[n][i][0] *= cs[n][0];
-            x[n][i][1] *= cs[n][1];
-            x[n][i][2] *= cs[n][0];
-            x[n][i][3] *= cs[n][1];
-          }
-        }
         if (!full) {
 #pragma unroll
           for (int i = 0; i < kUnitTiles; ++i) {
@@ -454,6 +472,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
             top[n][e] = fmaxf(x[n][0][e], x[n][0][e + 2]);
 #pragma unroll
             for (int i = 1; i < kUnitTiles; ++i) top[n][e] = fmaxf(top[n][e], fmaxf(x[n][i][e], x[n][i][e + 2]));
+            top[n][e] *= cs[n][e];
             grow |= top[n][e] > mx[n][e] + (kRescaleThreshold + kPShift);
           }
         }
@@ -488,17 +507,21 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           uint32_t bh[kNT][2], bl[kNT][2];
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
-            float p[4], hi[4];
+            // (a register pair holds the two columns of a token)
+            F2 p[2], hi[2], lo[2];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              p[r] = fast_exp2(x[n][i][r] - mx[n][r & 1]);
-              l[n][r & 1] += p[r];
-              hi[r] = __uint_as_float(__float_as_uint(p[r]) & 0xFFFFE000u);
+            for (int r = 0; r < 2; ++r) {
+              const F2 y = fma2(F2{x[n][i][2 * r], x[n][i][2 * r + 1]}, F2{cs[n][0], cs[n][1]}, F2{-mx[n][0], -mx[n][1]});
+              p[r] = F2{fast_exp2(y.x), fast_exp2(y.y)};
+              const F2 sum = add2(F2{l[n][0], l[n][1]}, p[r]);
+              l[n][0] = sum.x;
+              l[n][1] = sum.y;
+              hi[r] = F2{__uint_as_float(__float_as_uint(p[r].x) & 0xFFFFE000u),
+                         __uint_as_float(__float_as_uint(p[r].y) & 0xFFFFE000u)};
+              lo[r] = add2(p[r], F2{-hi[r].x, -hi[r].y});
+              bh[n][r] = flip8x8(pack_f16x2(hi[r].x, hi[r].y));
+              bl[n][r] = flip8x8(pack_f16x2(lo[r].x, lo[r].y));
             }
-            bh[n][0] = flip8x8(pack_f16x2(hi[0], hi[1]));
-            bh[n][1] = flip8x8(pack_f16x2(hi[2], hi[3]));
-            bl[n][0] = flip8x8(pack_f16x2(p[0] - hi[0], p[1] - hi[1]));
-            bl[n][1] = flip8x8(pack_f16x2(p[2] - hi[2], p[3] - hi[3]));
           }
 
           // ---- O^T (128 channels x columns) += V^T (128 x 16 tokens) . P^T.  m-tile mt: row gi is
@@ -673,7 +696,8 @@ int q4_col_tiles(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 
 template <int kNT>
 Plan q4_plan_nt(int batch, int hq, int hkv, int page_size, int max_pages, int sms) {
-  Plan p = make_plan(batch, hq, hkv, page_size, max_pages, sms, Q4Cfg<kNT>::kWarps, 8 * kNT);
+  Plan p = make_plan(batch, hq, hkv, page_size, max_pages, sms, Q4Cfg<kNT>::kWarps, 8 * kNT, kItemTilesQ4,
+                     kItemTilesQ4);
   const size_t lse = p.part_lse_bytes;               // a partial keeps two floats (maximum and sum) there
   p.part_lse_bytes = (static_cast<size_t>(batch) * hq * p.max_chunks * 8 + 255) & ~static_cast<size_t>(255);
   p.ws_bytes += p.part_lse_bytes - lse;
