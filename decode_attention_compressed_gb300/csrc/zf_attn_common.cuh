@@ -496,11 +496,11 @@ static Plan make_plan(int batch, int hq, int hkv, int page_size, int max_pages, 
 }
 
 // Raise a kernel's dynamic shared-memory limit once per (device, kernel); the limit only grows.
-// `which` (0-3) names the kernel among those of the calling file: each file that includes this
+// `which` (0-7) names the kernel among those of the calling file: each file that includes this
 // header keeps its own records, so two kernels of one file must not share a number.
 static zf_status ensure_smem_limit(const void* kernel, int which, size_t bytes) {
   static std::mutex mu;
-  static size_t done[64][4] = {};
+  static size_t done[64][8] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return ZF_ERR_CUDA;
   if (dev < 0 || dev >= 64) return ZF_ERR_UNSUPPORTED;

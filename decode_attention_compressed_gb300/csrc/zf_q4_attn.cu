@@ -199,7 +199,7 @@ __device__ __forceinline__ float store_q_row(uint8_t* row, int lane, uint32_t w0
   return __int_as_float((127 - k) << 23);
 }
 
-template <int kNT>
+template <int kNT, bool kFold>
 __device__ __forceinline__ void stage_q(const AttnArgs& a, const ItemDesc& d, uint8_t* qb, float* qs, int lane) {
   constexpr int kCols = Q4Cfg<kNT>::kCols;
 #pragma unroll
@@ -207,10 +207,11 @@ __device__ __forceinline__ void stage_q(const AttnArgs& a, const ItemDesc& d, ui
     uint32_t v[8][2];
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
-      const int qh = d.h0 + min(r0 + r, d.nh - 1);
+      const int c = kFold ? r & 3 : r0 + r;
+      const int qh = d.h0 + min(c, d.nh - 1);
       const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + query_row(d.b, qh, a.tokens, a.hq) * ZF_HEAD_DIM);
-      v[r][0] = r0 + r < d.nh ? src[lane] : 0u;
-      v[r][1] = r0 + r < d.nh ? src[lane + 32] : 0u;
+      v[r][0] = c < d.nh ? src[lane] : 0u;
+      v[r][1] = c < d.nh ? src[lane + 32] : 0u;
     }
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -232,7 +233,9 @@ __device__ __forceinline__ void finish_row(float* out, float* lse, size_t row, i
 }
 
 // kMulti: several new tokens per request (a causal mask on the last positions).
-template <int kNT, bool kMulti>
+// kFold (kNT = 1, at most 4 columns): columns 4 to 7 repeat 0 to 3, and in the second product the first
+// four carry the weights' high parts and the others the remainders, so that one MMA does the work of two.
+template <int kNT, bool kMulti, bool kFold>
 __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const AttnArgs a, const float v_factor) {
   using C = Q4Cfg<kNT>;
   constexpr int kWarps = C::kWarps;
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         mbar_arrive(&item_full[buf]);        // release: the records can be fetched
       }
       if (d.b >= 0) {
-        stage_q<kNT>(a, d, qbuf + buf * C::kCols * kQ4QRowBytes, qscale + buf * C::kCols, lane);
+        stage_q<kNT, kFold>(a, d, qbuf + buf * C::kCols * kQ4QRowBytes, qscale + buf * C::kCols, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[buf]);   // release: the q rows
       }
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
       for (int e = 0; e < 2; ++e) {
         mx[n][e] = kNoScore;
         l[n][e] = 0.f;
-        seen[n][e] = kMulti ? lens[d.b] - a.tokens + (d.h0 + 8 * n + 2 * ti + e) % a.tokens : 0;
+        seen[n][e] = kMulti ? lens[d.b] - a.tokens + (d.h0 + (kFold ? (2 * ti + e) & 3 : 8 * n + 2 * ti + e)) % a.tokens : 0;
       }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) o[n][mt][0] = o[n][mt][1] = o[n][mt][2] = o[n][mt][3] = 0.f;
@@ -519,8 +522,9 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
               hi[r] = F2{__uint_as_float(__float_as_uint(p[r].x) & 0xFFFFE000u),
                          __uint_as_float(__float_as_uint(p[r].y) & 0xFFFFE000u)};
               lo[r] = add2(p[r], F2{-hi[r].x, -hi[r].y});
+              if (kFold) hi[r] = ti < 2 ? hi[r] : lo[r];
               bh[n][r] = flip8x8(pack_f16x2(hi[r].x, hi[r].y));
-              bl[n][r] = flip8x8(pack_f16x2(lo[r].x, lo[r].y));
+              if (!kFold) bl[n][r] = flip8x8(pack_f16x2(lo[r].x, lo[r].y));
             }
           }
 
@@ -556,10 +560,12 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
               for (int e = 0; e < 4; ++e) mma_f16(o[n][4 * h + e], a0[e], a1[e], a2[e], a3[e], bh[n][0], bh[n][1]);
+            if (!kFold) {
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
 #pragma unroll
               for (int e = 0; e < 4; ++e) mma_f16(o[n][4 * h + e], a0[e], a1[e], a2[e], a3[e], bl[n][0], bl[n][1]);
+            }
           }
         }
       }
@@ -611,7 +617,11 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
               stages + (static_cast<size_t>(w) * kWarpStages + combine_stage[w]) * kStageQ4);
           const float f = fast_exp2(mw[w] - M);
           lsum += f * cwp[8 * kOStride + 8 + hh];
-          const float4 v = *reinterpret_cast<const float4*>(cwp + hh * kOStride + 4 * lane);
+          float4 v = *reinterpret_cast<const float4*>(cwp + hh * kOStride + 4 * lane);
+          if (kFold) {
+            const float4 r = *reinterpret_cast<const float4*>(cwp + (hh + 4) * kOStride + 4 * lane);
+            v = make_float4(v.x + r.x, v.y + r.y, v.z + r.z, v.w + r.w);
+          }
           acc.x += f * v.x;
           acc.y += f * v.y;
           acc.z += f * v.z;
@@ -712,10 +722,10 @@ Plan q4_plan(int batch, int hq, int hkv, int page_size, int max_pages, int sms) 
   }
 }
 
-template <int kNT, bool kMulti>
+template <int kNT, bool kMulti, bool kFold = false>
 zf_status launch_q4(const AttnArgs& a, float v_factor, int grid, int which, cudaStream_t s) {
   const size_t smem = q4_smem<kNT>(a.batch).total;
-  const zf_status st = ensure_smem_limit(reinterpret_cast<const void*>(attn_q4_kernel<kNT, kMulti>), which, smem);
+  const zf_status st = ensure_smem_limit(reinterpret_cast<const void*>(attn_q4_kernel<kNT, kMulti, kFold>), which, smem);
   if (st != ZF_OK) return st;
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -727,7 +737,7 @@ zf_status launch_q4(const AttnArgs& a, float v_factor, int grid, int which, cuda
   cfg.stream = s;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_q4_kernel<kNT, kMulti>, a, v_factor) == cudaSuccess ? ZF_OK : ZF_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, attn_q4_kernel<kNT, kMulti, kFold>, a, v_factor) == cudaSuccess ? ZF_OK : ZF_ERR_CUDA;
 }
 
 }  // namespace
@@ -807,7 +817,10 @@ extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, 
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool multi = tokens > 1;
-  if (nt == 1) st = multi ? launch_q4<1, true>(a, v_factor, p.grid, 0, s) : launch_q4<1, false>(a, v_factor, p.grid, 1, s);
+  if (a.group <= 4)
+    st = multi ? launch_q4<1, true, true>(a, v_factor, p.grid, 4, s) : launch_q4<1, false, true>(a, v_factor, p.grid, 5, s);
+  else if (nt == 1)
+    st = multi ? launch_q4<1, true>(a, v_factor, p.grid, 0, s) : launch_q4<1, false>(a, v_factor, p.grid, 1, s);
   else if (nt == 2) st = launch_q4<2, true>(a, v_factor, p.grid, 2, s);
   else st = launch_q4<4, true>(a, v_factor, p.grid, 3, s);
   if (st != ZF_OK) return st;
