@@ -513,6 +513,22 @@ def _launch_stream(stream, device) -> int:
     return stream.cuda_stream
 
 
+def _tables(page_table, seq_lens, device, B):
+    """page_table [>= B][*] and seq_lens [>= B], int32."""
+    for t, name, dims in ((page_table, "page_table", 2), (seq_lens, "seq_lens", 1)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != torch.int32:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+        if len(t.shape) != dims:
+            raise ValueError(f"{name}: shape {list(t.shape)}, expected {'[*][*]' if dims == 2 else '[*]'}")
+        if t.shape[0] < B:
+            raise ValueError(f"{name}: {t.shape[0]} rows, at least {B} needed")
+    return page_table.contiguous(), seq_lens.contiguous()
+
+
 class Q4Cache:
     """One layer's 4-bit paged cache in device memory (layout and numbers: include/zf.h, zf_q4).
 
@@ -588,7 +604,9 @@ def q4_read_tokens(cache: Q4Cache, page_ids, positions, stream=None):
     ids, pos = _places(cache, page_ids, positions)
     n = ids.shape[0]
     s = _launch_stream(stream, cache._device)
-    k, v = torch.empty((2, n, cache._sizes[1], HEAD_DIM), dtype=torch.int16, device=cache._device).unbind(0)
+    shape = (n, cache._sizes[1], HEAD_DIM)
+    k = torch.empty(shape, dtype=torch.int16, device=cache._device)
+    v = torch.empty(shape, dtype=torch.int16, device=cache._device)
     code = lib().zf_q4_read_tokens(cache._ref, ids.data_ptr(), pos.data_ptr(), n, k.data_ptr(), v.data_ptr(), s)
     if code:
         _check("zf_q4_read_tokens", code)
@@ -612,7 +630,7 @@ def q4_decode_attn(cache: Q4Cache, q, page_table, seq_lens, scale=None, out=None
         raise ValueError(f"q: shape {list(shape)}, expected [*][*][{HEAD_DIM}] or [*][*][*][{HEAD_DIM}]")
     q = _tensor(q, "q", _BITS16, dev, shape)
     B, T, Hq = (shape[0], 1, shape[1]) if len(shape) == 3 else shape[:3]
-    page_table, seq_lens = _attn_args(cache, q, page_table, seq_lens, B)
+    page_table, seq_lens = _tables(page_table, seq_lens, dev, B)
     max_pages = page_table.shape[1]
     out = torch.empty(shape, dtype=torch.float32, device=dev) if out is None else \
         _tensor(out, "out", _F32, dev, shape, write=True)
@@ -662,11 +680,16 @@ def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_po
     free_pages = _tensor(free_pages, "free_pages", _I32, dev, free_pages.shape)
     free_pos = _tensor(free_pos, "free_pos", _I32, dev, (1,))
     n = max(int(max_tokens), 0)
-    if out is None:
-        pad = -n % 4                         # the lists start on 16-byte boundaries
-        p = torch.empty(3 * (n + pad) + 3 * B + 2, dtype=torch.int32, device=dev) \
-            .split((n, pad, n, pad, n, pad, B, B, B + 1, 1))
-        out = TokenMap(p[6], p[7], p[9], p[8], p[0], p[2], p[4])
+    if out is None:        # one allocation; the lists start on 16-byte boundaries
+        pad = -n % 4
+        if pad:
+            ids, _, pos, _, seq, _, lens, held, start, free = torch.empty(
+                3 * (n + pad) + 3 * B + 2, dtype=torch.int32, device=dev) \
+                .split_with_sizes((n, pad, n, pad, n, pad, B, B, B + 1, 1))
+        else:
+            ids, pos, seq, lens, held, start, free = torch.empty(
+                3 * n + 3 * B + 2, dtype=torch.int32, device=dev).split_with_sizes((n, n, n, B, B, B + 1, 1))
+        out = TokenMap(lens, held, free, start, ids, pos, seq)
     else:
         shapes = ((B,), (B,), (1,), (B + 1,), (n,), (n,), (n,))
         out = TokenMap(*(_tensor(t, "out." + name, _I32, dev, s, write=True)
