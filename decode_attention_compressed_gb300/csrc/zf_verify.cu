@@ -8,15 +8,17 @@
 // Only the rows that the draw needs are read (one or two per request; the acceptance reads two numbers
 // per draft), so the call is bound by 4 or 8 bytes per vocabulary entry and request, and by its chain
 // of dependent steps when the batch is small.  A cluster of CTAs (up to 16) owns a request: each
-// warp sums a contiguous piece of the row, the sums of all warps are exchanged through distributed
-// shared memory, and the one CTA whose piece holds the drawn point narrows it down (its
-// warps re-read that warp's piece from L2, then one warp the piece of a piece).
+// warp sums a contiguous piece of the row in blocks, the pieces' sums are exchanged through
+// distributed shared memory, and the one warp whose piece holds the drawn point finds its block among the
+// sums it kept and the entry by reading that block once more, from L2.
 //
-// Sums: a thread adds its weights in float with the rounding errors carried along (Knuth's two-sum,
-// 48 bits), everything above that is double.  The result so does not depend on how the row is split,
-// short of a drawn point that falls within 2^-44 of the border between two tokens.  (Double
-// additions for every weight would bind the call: their rate is 1/64 of float's here.)
+// Sums are kept as pairs of floats (Knuth's two-sum; 48 bits, 44 and more of them right after the
+// additions made here), so the result does not depend on how a row is split, short of a drawn
+// point that close to the border between two tokens.  (Double additions would do too, but their rate is
+// 1/64 of float's on this GPU: with doubles only above the level of a thread, the call took 41.8 us
+// for 64 requests of 128000 entries.)
 #include <cuda_runtime.h>
+#include <math_constants.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -31,6 +33,7 @@ namespace {
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyMaxCluster = 16;
+constexpr int kMaxBlocks = 32;                     // blocks of a warp's piece
 
 struct VerifyArgs {
   const float* target;
@@ -50,11 +53,11 @@ __device__ __forceinline__ void v_cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Store a double into the shared memory of CTA `rank` of the cluster, at this CTA's address of `p`.
-__device__ __forceinline__ void dsmem_store(double* p, uint32_t rank, double v) {
+// Store a sum into the shared memory of CTA `rank` of the cluster, at this CTA's address of `p`.
+__device__ __forceinline__ void dsmem_store(float2* p, uint32_t rank, float hi, float lo) {
   uint32_t addr;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(v) : "memory");
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(hi), "f"(lo) : "memory");
 }
 
 // What is sampled from: p, or p - q where positive; `drop` names the draft whose q is 1 when there is no q row.
@@ -64,86 +67,198 @@ struct Row {
   int drop;
 };
 
-__device__ __forceinline__ float weight(const Row& r, int i, float p, float q) {
-  float w = r.q ? p - q : (i == r.drop ? p - 1.f : p);
-  return w > 0.f ? w : 0.f;
-}
-__device__ __forceinline__ float weight_at(const Row& r, int i) { return weight(r, i, r.p[i], r.q ? r.q[i] : 0.f); }
-
-struct Sum {
-  float s = 0.f, e = 0.f;
-  __device__ __forceinline__ void add(float w) {          // s + e gains w, the rounding error of s in e
-    const float t = __fadd_rn(s, w);
-    const float z = __fadd_rn(t, -s);
-    e = __fadd_rn(e, __fadd_rn(__fadd_rn(s, -__fadd_rn(t, -z)), __fadd_rn(w, -z)));
-    s = t;
-  }
-  __device__ __forceinline__ double value() const { return static_cast<double>(s) + static_cast<double>(e); }
+// An unevaluated sum of two floats, |lo| at most half a step of hi: 48 bits.
+struct DF {
+  float hi, lo;
 };
+__device__ __forceinline__ DF two_sum(float a, float b) {          // Knuth: a + b, exactly
+  const float s = __fadd_rn(a, b);
+  const float z = __fadd_rn(s, -a);
+  return {s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -z)), __fadd_rn(b, -z))};
+}
+__device__ __forceinline__ DF norm(float s, float e) {             // |s| >= |e|
+  const float h = __fadd_rn(s, e);
+  return {h, __fadd_rn(e, -__fadd_rn(h, -s))};
+}
+__device__ __forceinline__ DF add(DF a, DF b) {
+  const DF s = two_sum(a.hi, b.hi);
+  return norm(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ DF sub(DF a, DF b) { return add(a, {-b.hi, -b.lo}); }
+__device__ __forceinline__ bool above(DF a, DF b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+__device__ __forceinline__ DF shfl(DF v, int lane) {
+  return {__shfl_sync(0xFFFFFFFFu, v.hi, lane), __shfl_sync(0xFFFFFFFFu, v.lo, lane)};
+}
 
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ DF warp_sum(DF v) {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  for (int d = 16; d > 0; d >>= 1)
+    v = add(v, {__shfl_xor_sync(0xFFFFFFFFu, v.hi, d), __shfl_xor_sync(0xFFFFFFFFu, v.lo, d)});
+  return v;
+}
+// Sums over the lanes up to and including this one.
+__device__ __forceinline__ DF warp_scan(DF v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const DF x = {__shfl_up_sync(0xFFFFFFFFu, v.hi, d), __shfl_up_sync(0xFFFFFFFFu, v.lo, d)};
+    if (lane >= d) v = add(v, x);
+  }
   return v;
 }
 
-// Sum of the weights [lo, hi) by one warp.  kVec: rows are 16-byte aligned, lo and hi multiples of 4.
-template <bool kVec>
-__device__ __forceinline__ double piece_sum(const Row& r, int lo, int hi, int lane) {
-  Sum s;
+// A batch: the weights of kBatch consecutive entries from i0 (0 from hi on), kLane per lane, read
+// together.  kVec: rows are 16-byte aligned, i0 and hi multiples of 4; lane l then holds entries
+// i0 + 128 k + 4 l .. + 3 as w[4 k ..], else i0 + 32 k + l as w[k].
+constexpr int kLane = 16;
+constexpr int kBatch = 32 * kLane;
+template <bool kVec, bool kHasQ>
+__device__ __forceinline__ void load_batch(const Row& r, int i0, int hi, int lane, float (&w)[kLane]) {
+  float q[kLane];
   if (kVec) {
-#pragma unroll 4
-    for (int i = lo + 4 * lane; i < hi; i += 128) {
-      const float4 p = *reinterpret_cast<const float4*>(r.p + i);
-      const float4 q = r.q ? *reinterpret_cast<const float4*>(r.q + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      s.add(weight(r, i, p.x, q.x));
-      s.add(weight(r, i + 1, p.y, q.y));
-      s.add(weight(r, i + 2, p.z, q.z));
-      s.add(weight(r, i + 3, p.w, q.w));
+#pragma unroll
+    for (int k = 0; k < kLane / 4; ++k) {
+      const int i = i0 + 128 * k + 4 * lane;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (i < hi) {
+        x = *reinterpret_cast<const float4*>(r.p + i);
+        if (kHasQ) y = *reinterpret_cast<const float4*>(r.q + i);
+      }
+      w[4 * k] = x.x; w[4 * k + 1] = x.y; w[4 * k + 2] = x.z; w[4 * k + 3] = x.w;
+      q[4 * k] = y.x; q[4 * k + 1] = y.y; q[4 * k + 2] = y.z; q[4 * k + 3] = y.w;
     }
   } else {
-#pragma unroll 8
-    for (int i = lo + lane; i < hi; i += 32) s.add(weight_at(r, i));
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const int i = i0 + 32 * k + lane;
+      w[k] = i < hi ? r.p[i] : 0.f;
+      q[k] = kHasQ && i < hi ? r.q[i] : 0.f;
+    }
   }
-  return warp_sum(s.value());
+#pragma unroll
+  for (int k = 0; k < kLane; ++k) {
+    const int i = kVec ? i0 + 128 * (k / 4) + 4 * lane + k % 4 : i0 + 32 * k + lane;
+    const float x = kHasQ ? w[k] - q[k] : i == r.drop ? w[k] - 1.f : w[k];
+    w[k] = x > 0.f ? x : 0.f;
+  }
+}
+
+// Sum of the weights [lo, hi) by one warp.
+template <bool kVec, bool kHasQ>
+__device__ __forceinline__ DF block_sum(const Row& r, int lo, int hi, int lane) {
+  DF s[2] = {{0.f, 0.f}, {0.f, 0.f}};
+  for (int i = lo; i < hi; i += kBatch) {
+    float w[kLane];
+    load_batch<kVec, kHasQ>(r, i, hi, lane, w);
+#pragma unroll
+    for (int k = 0; k < kLane; ++k) {
+      const DF t = two_sum(s[k & 1].hi, w[k]);
+      s[k & 1] = {t.hi, __fadd_rn(s[k & 1].lo, t.lo)};
+    }
+  }
+  return warp_sum(add(norm(s[0].hi, s[0].lo), norm(s[1].hi, s[1].lo)));
+}
+
+// Sums of a piece's blocks of blen entries into blk; returns their sum.
+template <bool kVec, bool kHasQ>
+__device__ __forceinline__ DF piece_sum(const Row& r, int lo, int hi, int blen, float2* blk, int lane) {
+  DF sum = {0.f, 0.f};
+  for (int k = 0, i = lo; i < hi; ++k, i += blen) {
+    const DF s = block_sum<kVec, kHasQ>(r, i, min(hi, i + blen), lane);
+    if (lane == 0) blk[k] = make_float2(s.hi, s.lo);
+    sum = add(sum, s);
+  }
+  return sum;
+}
+
+// The first entry of [lo, hi) with a running sum (from run on) above x; the last positive one when there is
+// none.  One warp.
+template <bool kVec, bool kHasQ>
+__device__ __forceinline__ int scan_block(const Row& r, int lo, int hi, DF run, DF x, int lane) {
+  int last = -1;
+  for (int i0 = lo; i0 < hi; i0 += kBatch) {
+    float w[kLane];
+    load_batch<kVec, kHasQ>(r, i0, hi, lane, w);
+    constexpr int kRun = kVec ? 4 : 1;                 // consecutive entries of a lane
+#pragma unroll
+    for (int k = 0; k < kLane / kRun; ++k) {
+      DF own = {0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) own = add(own, {w[kRun * k + e], 0.f});
+      const DF in = warp_scan(own, lane);
+      DF at = add(run, sub(in, own));
+      int mine = -1, any = -1;                         // this lane's hit, and its last positive entry
+#pragma unroll
+      for (int e = 0; e < kRun; ++e) {
+        const float v = w[kRun * k + e];
+        at = add(at, {v, 0.f});
+        const int i = i0 + 32 * kRun * k + kRun * lane + e;
+        if (v > 0.f) {
+          any = i;
+          if (mine < 0 && above(at, x)) mine = i;
+        }
+      }
+      const uint32_t hit = __ballot_sync(0xFFFFFFFFu, mine >= 0), pos = __ballot_sync(0xFFFFFFFFu, any >= 0);
+      if (hit) return __shfl_sync(0xFFFFFFFFu, mine, __ffs(hit) - 1);
+      if (pos) last = __shfl_sync(0xFFFFFFFFu, any, 31 - __clz(pos));
+      run = add(run, shfl(in, 31));
+    }
+  }
+  return last;
 }
 
 // Length of each of `parts` equal pieces of n entries, a multiple of 4.
 __device__ __forceinline__ int piece_len(int n, int parts) { return ((n + parts - 1) / parts + 3) & ~3; }
 
-// Index of the first of n sums whose running total is above r (the last positive one when none is), and
-// the total before it; -1 when no sum is positive.  One warp; n <= 32 * kVerifyMaxCluster.
-__device__ __forceinline__ int find(const double* sums, int n, double r, double& before, int lane) {
-  double run = 0.0, last_before = 0.0;
-  int last = -1;
-  for (int b = 0; b < n; b += 32) {
-    const double v = b + lane < n ? sums[b + lane] : 0.0;
-    double in = v;
+// Index of the first of n sums whose running total is above u times the total (the last positive one when
+// none is); x: that point, before: the total before the sum found.  -1 when no sum is positive or the
+// total is not finite; zero: whether every sum is 0.  One warp, n <= 32 * kPer; given_x: x is given instead.
+template <int kPer>
+__device__ __forceinline__ int find(const float2* sums, int n, float u, bool given_x, DF& x, DF& before, bool& zero,
+                                    int lane) {
+  const int per = (n + 31) / 32;
+  DF v[kPer], own = {0.f, 0.f};
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const double x = __shfl_up_sync(0xFFFFFFFFu, in, d);
-      if (lane >= d) in += x;
-    }
-    const uint32_t hit = __ballot_sync(0xFFFFFFFFu, v > 0.0 && run + in > r);
-    const uint32_t pos = __ballot_sync(0xFFFFFFFFu, v > 0.0);
-    const uint32_t pick = hit ? hit & (0u - hit) : pos;      // the first hit, or the last positive
-    if (pick) {
-      const int at = 31 - __clz(pick);
-      last = b + at;
-      last_before = run + __shfl_sync(0xFFFFFFFFu, in - v, at);
-      if (hit) break;
-    }
-    run += __shfl_sync(0xFFFFFFFFu, in, 31);
+  for (int k = 0; k < kPer; ++k) {
+    const int i = lane * per + k;
+    const float2 s = k < per && i < n ? sums[i] : make_float2(0.f, 0.f);
+    v[k] = {s.x, s.y};
+    own = add(own, v[k]);
   }
-  before = last_before;
-  return last;
+  const DF in = warp_scan(own, lane), total = shfl(in, 31);
+  zero = total.hi == 0.f;
+  if (!(total.hi > 0.f && total.hi < CUDART_INF_F)) return -1;
+  if (!given_x) {
+    const float p = __fmul_rn(u, total.hi);
+    x = norm(p, __fmaf_rn(u, total.lo, __fmaf_rn(u, total.hi, -p)));
+  }
+  DF at = sub(in, own), at_mine = at, at_any = at;
+  int mine = -1, any = -1;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) {
+    const DF next = add(at, v[k]);
+    if (v[k].hi > 0.f) {
+      any = lane * per + k;
+      at_any = at;
+      if (mine < 0 && above(next, x)) {
+        mine = any;
+        at_mine = at;
+      }
+    }
+    at = next;
+  }
+  const uint32_t hit = __ballot_sync(0xFFFFFFFFu, mine >= 0), pos = __ballot_sync(0xFFFFFFFFu, any >= 0);
+  const int src = hit ? __ffs(hit) - 1 : 31 - __clz(pos);          // (a positive total has a positive sum)
+  before = hit ? shfl(at_mine, src) : shfl(at_any, src);
+  return __shfl_sync(0xFFFFFFFFu, hit ? mine : any, src);
 }
 
 // Grid: one cluster per request.
 template <bool kVec>
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a) {
-  __shared__ double sums[kVerifyMaxCluster * kVerifyWarps];   // of every warp of the cluster
-  __shared__ double part[kVerifyWarps];
+  __shared__ float2 sums[kVerifyMaxCluster * kVerifyWarps];   // of every warp of the cluster
+  __shared__ float2 blocks[kVerifyWarps][kMaxBlocks];         // of this CTA's pieces
+  __shared__ int sh_piece, sh_zero;
+  __shared__ DF sh_x, sh_before;
   __shared__ int sh_acc, sh_n;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank, ranks;
@@ -201,73 +316,54 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
 
   // ---- sums of all warps' pieces
   const int len = piece_len(V, ranks * kVerifyWarps);
+  const int blen = max((len + kMaxBlocks * kBatch - 1) / (kMaxBlocks * kBatch), 1) * kBatch;
   const int mine = static_cast<int>(rank) * kVerifyWarps + warp;
-  int token = -1;
-  double W = 0.0;
+  const int lo = min(V, mine * len), hi = min(V, lo + len);
+  const float u = a.uniform[static_cast<size_t>(b) * (T + 1) + T];
   for (int attempt = 0; attempt < 2; ++attempt) {
-    const int lo = min(V, mine * len), hi = min(V, lo + len);
-    const double s = piece_sum<kVec>(row, lo, hi, lane);
-    if (lane < static_cast<int>(ranks)) dsmem_store(&sums[mine], lane, s);
+    const DF s = row.q ? piece_sum<kVec, true>(row, lo, hi, blen, blocks[warp], lane)
+                       : piece_sum<kVec, false>(row, lo, hi, blen, blocks[warp], lane);
+    if (lane < static_cast<int>(ranks)) dsmem_store(&sums[mine], lane, s.hi, s.lo);
     v_cluster_sync();
-    W = 0.0;                                            // every warp adds them in the same order
-    for (int i = lane; i < static_cast<int>(ranks) * kVerifyWarps; i += 32) W += sums[i];
-    W = warp_sum(W);
-    if (W != 0.0 || (!row.q && row.drop < 0)) break;    // uniform over the cluster
+    if (warp == 0) {                                    // the same in every CTA of the cluster
+      DF x, before = {0.f, 0.f};
+      bool zero;
+      const int piece = find<kVerifyMaxCluster * kVerifyWarps / 32>(sums, ranks * kVerifyWarps, u, false, x, before, zero, lane);
+      if (lane == 0) {
+        sh_piece = piece;
+        sh_zero = zero;
+        sh_x = x;
+        sh_before = before;
+      }
+    }
+    __syncthreads();
+    if (!sh_zero || (!row.q && row.drop < 0)) break;    // uniform over the cluster
     row.q = nullptr;                                    // p nowhere above q: sample from p itself
     row.drop = -1;
     v_cluster_sync();                                   // the sums have been read everywhere
   }
-  const bool good = W > 0.0 && W < 1e300;               // finite (float sums reach 2^152 at most)
-  const double r = static_cast<double>(a.uniform[static_cast<size_t>(b) * (T + 1) + T]) * W;
-  double before = 0.0;
-  const int piece = good ? find(sums, ranks * kVerifyWarps, r, before, lane) : -1;
-  const bool owner = piece >= 0 ? piece / kVerifyWarps == static_cast<int>(rank) : rank == 0;
-  if (owner) {                                          // uniform over the CTA
+  const int piece = sh_piece;
+  if (piece >= 0 ? piece == mine : mine == 0) {         // one warp of the cluster
+    int token = -1;
     if (piece >= 0) {
-      // ---- the piece, cut once more over this CTA's warps
-      const int lo = min(V, piece * len), hi = min(V, lo + len);
-      const int sub = piece_len(hi - lo, kVerifyWarps);
-      const int slo = min(hi, lo + warp * sub), shi = min(hi, slo + sub);
-      const double s = piece_sum<kVec>(row, slo, shi, lane);
-      if (lane == 0) part[warp] = s;
-      __syncthreads();
-      if (warp == 0) {
-        double inner = 0.0;
-        const int w = find(part, kVerifyWarps, r - before, inner, lane);
-        // ---- and entry by entry: 32 at a time
-        const int flo = min(hi, lo + max(w, 0) * sub), fhi = min(hi, flo + sub);
-        double run = before + inner;
-        int last = -1;
-        for (int i0 = flo; i0 < fhi; i0 += 32) {
-          const double v = i0 + lane < fhi ? static_cast<double>(weight_at(row, i0 + lane)) : 0.0;
-          double in = v;
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const double x = __shfl_up_sync(0xFFFFFFFFu, in, d);
-            if (lane >= d) in += x;
-          }
-          const uint32_t hit = __ballot_sync(0xFFFFFFFFu, v > 0.0 && run + in > r);
-          const uint32_t pos = __ballot_sync(0xFFFFFFFFu, v > 0.0);
-          if (hit) {
-            last = i0 + __ffs(hit) - 1;
-            break;
-          }
-          if (pos) last = i0 + 31 - __clz(pos);
-          run += __shfl_sync(0xFFFFFFFFu, in, 31);
-        }
-        token = last;
-      }
-    } else if (tid == 0) {
+      // ---- the block of the piece, then the entry in it (read again, from L2)
+      DF x = sh_x, inner = {0.f, 0.f};
+      DF rest = sub(x, sh_before);
+      bool zero;
+      const int k = find<kMaxBlocks / 32>(blocks[warp], (hi - lo + blen - 1) / blen, 0.f, true, rest, inner, zero, lane);
+      const int blo = lo + max(k, 0) * blen, bhi = min(hi, blo + blen);
+      const DF run = add(sh_before, inner);
+      token = row.q ? scan_block<kVec, true>(row, blo, bhi, run, x, lane)
+                    : scan_block<kVec, false>(row, blo, bhi, run, x, lane);
+    } else if (lane == 0) {
       report(a.status, ZF_DEV_BAD_PROBS);
     }
-    if (warp == 0) {
-      for (int t = lane; t <= T; t += 32)
-        a.tokens[static_cast<size_t>(b) * (T + 1) + t] =
-            t < acc ? a.tokens_in[static_cast<size_t>(b) * T + t] : t == acc ? token : -1;
-      if (lane == 0) {
-        a.accepted[b] = acc;
-        if (a.out_lens) a.out_lens[b] = a.seq_lens[b] - (n - acc);
-      }
+    for (int t = lane; t <= T; t += 32)
+      a.tokens[static_cast<size_t>(b) * (T + 1) + t] =
+          t < acc ? a.tokens_in[static_cast<size_t>(b) * T + t] : t == acc ? token : -1;
+    if (lane == 0) {
+      a.accepted[b] = acc;
+      if (a.out_lens) a.out_lens[b] = a.seq_lens[b] - (n - acc);
     }
   }
   // no CTA reads another's shared memory after the last barrier (the sums were pushed), so none has to wait
