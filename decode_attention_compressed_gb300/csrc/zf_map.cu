@@ -6,11 +6,12 @@
 // entry is about to get), index p % P.
 //
 // A decode step is bound by latency (one launch, two dependent round trips), a batch of prompts by
-// the 12 bytes it writes per token.  One launch either way: a single cluster of 1, 8 or 16 CTAs, every
-// one of which scans the whole batch (three loads per request) into its shared memory; the cluster
-// barrier after that scan is what lets the outputs be the same arrays as the inputs.  The CTAs then
-// share out the table entries (a warp per request) and the list entries (four per thread: one
-// binary search and one division for each four, 16-byte stores).
+// the 12 bytes it writes per token.  The first kernel is a single cluster of 1 or 8 CTAs, every one of
+// which scans the whole batch (three loads per request) into its shared memory; the cluster barrier
+// after that scan is what lets the outputs be the same arrays as the inputs.  The CTAs then share out
+// the table entries and, for short lists, the list entries.  Long lists get a
+// second, grid-wide kernel that works from the outputs of the first.  Either way a thread makes four
+// entries at a time: one binary search over the list starts, one division, 16-byte stores.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -43,7 +44,72 @@ struct MapArgs {
   int32_t* seq_positions;
   int32_t* status;
   int32_t batch, page_size, max_pages, num_free, max_tokens;
+  int32_t lists;               // whether the first kernel writes the list entries
 };
+
+// The largest b with start[b] <= i.
+__device__ __forceinline__ int request_of(const int32_t* start, int batch, int i) {
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= i) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// List entries 4 c .. 4 c + 3: len(b) is request b's length before the call, page(b, j) its page j.
+template <typename Len, typename Page>
+__device__ __forceinline__ void write_entries(const MapArgs& a, const int32_t* start, int total, int c, Len&& len,
+                                              Page&& page_of) {
+  const int P = a.page_size, i0 = c * 4;
+  int pid[4], pos[4], seq[4];
+  int b = i0 < total ? request_of(start, a.batch, i0) : 0;
+  int page = 0, in = -1, page_id = -1;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = i0 + e;
+    if (i >= total) {
+      pid[e] = pos[e] = seq[e] = -1;
+      continue;
+    }
+    bool moved = e == 0, fresh = false;         // to another request; to another page
+    while (start[b + 1] <= i) {
+      ++b;
+      moved = true;
+    }
+    const int p = len(b) + (i - start[b]);
+    if (moved) {
+      page = p / P;
+      in = p - page * P;
+      fresh = true;
+    } else if (++in == P) {
+      in = 0;
+      ++page;
+      fresh = true;
+    }
+    if (fresh) page_id = page_of(b, page);
+    pid[e] = page_id;
+    pos[e] = in;
+    seq[e] = p;
+  }
+  if (i0 + 4 <= a.max_tokens) {
+    *reinterpret_cast<int4*>(a.page_ids + i0) = make_int4(pid[0], pid[1], pid[2], pid[3]);
+    *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    *reinterpret_cast<int4*>(a.seq_positions + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (i0 + e < a.max_tokens) {
+        a.page_ids[i0 + e] = pid[e];
+        a.positions[i0 + e] = pos[e];
+        a.seq_positions[i0 + e] = seq[e];
+      }
+    }
+  }
+}
+__device__ __forceinline__ int entry_chunks(const MapArgs& a) {
+  return static_cast<int>((static_cast<long long>(a.max_tokens) + 3) >> 2);
+}
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -114,8 +180,9 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(const MapArgs a) {
   }
   __syncthreads();
   long long off_new = 0, off_extra = 0, total_new = 0, total_extra = 0;
-#pragma unroll 8
-  for (int w = 0; w < kMapThreads / 32; ++w) {
+  const int used = ((a.batch + max(per, 1) - 1) / max(per, 1) + 31) / 32;      // warps that hold requests
+#pragma unroll 4
+  for (int w = 0; w < used; ++w) {
     const long long x = warp_new[w], y = warp_extra[w];
     if (w < warp) {
       off_new += x;
@@ -160,78 +227,43 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(const MapArgs a) {
   }
   const int total = start[a.batch];
 
-  // ---- list entries, four per thread.  A page past those held is read from the free list, not from
-  // the table, whose new entries are being written below at the same time.
-  const int chunks = static_cast<int>((static_cast<long long>(a.max_tokens) + 3) >> 2);
-  for (int c = rank * kMapThreads + tid; c < chunks; c += ranks * kMapThreads) {
-    const int i0 = c * 4;
-    int pid[4], pos[4], seq[4];
-    int b = 0;
-    if (i0 < total) {                    // largest b with start[b] <= i0 (so start[b + 1] > i0)
-      int lo = 0, hi = a.batch;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= i0) lo = mid; else hi = mid;
-      }
-      b = lo;
-    }
-    int page = 0, in = -1, page_id = -1;
-    bool fresh = true;                   // the page id has to be fetched
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + e;
-      if (i >= total) {
-        pid[e] = pos[e] = seq[e] = -1;
-        continue;
-      }
-      bool moved = e == 0;
-      while (start[b + 1] <= i) {
-        ++b;
-        moved = true;
-      }
-      const int p = len[b] + (i - start[b]);
-      if (moved) {
-        page = p / P;
-        in = p - page * P;
-        fresh = true;
-      } else if (++in == P) {
-        in = 0;
-        ++page;
-        fresh = true;
-      }
-      if (fresh) {
-        page_id = page < held[b] ? a.page_table[static_cast<size_t>(b) * a.max_pages + page]
-                                 : a.free_pages[base[b] + page - held[b]];
-        fresh = false;
-      }
-      pid[e] = page_id;
-      pos[e] = in;
-      seq[e] = p;
-    }
-    if (i0 + 4 <= a.max_tokens) {
-      *reinterpret_cast<int4*>(a.page_ids + i0) = make_int4(pid[0], pid[1], pid[2], pid[3]);
-      *reinterpret_cast<int4*>(a.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
-      *reinterpret_cast<int4*>(a.seq_positions + i0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (i0 + e < a.max_tokens) {
-          a.page_ids[i0 + e] = pid[e];
-          a.positions[i0 + e] = pos[e];
-          a.seq_positions[i0 + e] = seq[e];
-        }
-      }
-    }
+  // ---- list entries.  A page past those held is read from the free list, not from the table, whose
+  // new entries are being written below at the same time.
+  if (a.lists) {
+    const int chunks = entry_chunks(a);
+    for (int c = rank * kMapThreads + tid; c < chunks; c += ranks * kMapThreads)
+      write_entries(a, start, total, c, [&](int b) { return len[b]; },
+                    [&](int b, int j) {
+                      return j < held[b] ? a.page_table[static_cast<size_t>(b) * a.max_pages + j]
+                                         : a.free_pages[base[b] + j - held[b]];
+                    });
   }
 
-  // ---- new table entries: a warp per request
-  if (fits && total_extra > 0) {
-    for (int b = rank * (kMapThreads / 32) + warp; b < a.batch; b += ranks * (kMapThreads / 32)) {
-      const int end = b + 1 < a.batch ? base[b + 1] : pos0 + static_cast<int>(total_extra);
-      int32_t* row = a.page_table + static_cast<size_t>(b) * a.max_pages + held[b];
-      for (int j = base[b] + lane; j < end; j += 32) row[j - base[b]] = a.free_pages[j];
+  // ---- new table entries: one thread each, whatever requests they belong to
+  if (fits) {
+    const long long end = pos0 + total_extra;
+    for (long long k = static_cast<long long>(pos0) + rank * kMapThreads + tid; k < end; k += ranks * kMapThreads) {
+      const int j = static_cast<int>(k);
+      const int b = request_of(base, a.batch, j);
+      a.page_table[static_cast<size_t>(b) * a.max_pages + held[b] + (j - base[b])] = a.free_pages[j];
     }
   }
+}
+
+// List entries of a long list, from what the first kernel wrote.
+constexpr int kListThreads = 256;
+__global__ void __launch_bounds__(kListThreads) list_kernel(const MapArgs a) {
+  extern __shared__ int32_t start[];               // [batch + 1]
+  allow_next_grid();
+  wait_prior_grid();
+  for (int i = threadIdx.x; i <= a.batch; i += kListThreads) start[i] = a.token_start[i];
+  __syncthreads();
+  const int total = start[a.batch], chunks = entry_chunks(a);
+  for (long long c = static_cast<long long>(blockIdx.x) * kListThreads + threadIdx.x; c < chunks;
+       c += static_cast<long long>(gridDim.x) * kListThreads)
+    write_entries(a, start, total, static_cast<int>(c),
+                  [&](int b) { return a.out_lens[b] - (start[b + 1] - start[b]); },
+                  [&](int b, int j) { return a.page_table[static_cast<size_t>(b) * a.max_pages + j]; });
 }
 
 }  // namespace
@@ -282,8 +314,11 @@ extern "C" zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max
   a.max_pages = max_pages;
   a.num_free = num_free;
   a.max_tokens = max_tokens;
-  // One CTA handles 4096 list entries in one pass; longer lists are shared out over a cluster.
-  const int ctas = max_tokens <= 4096 ? 1 : max_tokens <= 65536 ? 8 : 16;
+  // Lists of up to kShortList entries are written by the first kernel, by one CTA up to 4096 entries
+  // (one pass of its threads), else by a cluster of 8.
+  constexpr int kShortList = 32768;
+  const int ctas = max_tokens <= 4096 ? 1 : 8;
+  a.lists = max_tokens <= kShortList ? 1 : 0;
   const size_t smem = (static_cast<size_t>(batch) * 4 + 1) * 4;
   static std::mutex mu;
   static bool ready[64] = {};
@@ -294,8 +329,7 @@ extern "C" zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
       const int most = (ZF_MAX_BATCH * 4 + 1) * 4;
-      if (cudaFuncSetAttribute(map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess ||
-          cudaFuncSetAttribute(map_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      if (cudaFuncSetAttribute(map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess)
         return ZF_ERR_CUDA;
       ready[dev] = true;
     }
@@ -314,5 +348,12 @@ extern "C" zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, map_kernel, a) == cudaSuccess ? ZF_OK : ZF_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, map_kernel, a) != cudaSuccess) return ZF_ERR_CUDA;
+  if (a.lists) return ZF_OK;
+  const long long blocks = ((static_cast<long long>(max_tokens) + 3) / 4 + kListThreads - 1) / kListThreads;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < 1216 ? blocks : 1216));       // 152 SMs x 8 resident CTAs
+  cfg.blockDim = dim3(kListThreads);
+  cfg.dynamicSmemBytes = (static_cast<size_t>(batch) + 1) * 4;
+  cfg.numAttrs = 1;                                                               // no cluster
+  return cudaLaunchKernelEx(&cfg, list_kernel, a) == cudaSuccess ? ZF_OK : ZF_ERR_CUDA;
 }

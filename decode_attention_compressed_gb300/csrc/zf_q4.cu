@@ -8,9 +8,9 @@
 // (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
 //
 // Bound: bytes (512 in, 144 out per token and kv head; a decode step's few tokens: launch latency).
-// One thread owns one block of K or of V: it reads 32 contiguous bytes, needs no exchange with
-// other lanes and writes 8 code bytes and one scale byte; 8 consecutive threads cover a 64-byte
-// code row.
+// One thread owns one block of K and the same block of V: it reads 32 contiguous bytes of each, needs
+// no exchange with other lanes and writes 8 code bytes and one scale byte of each; 8 consecutive
+// threads cover the 64-byte code rows of a token and kv head.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -18,7 +18,7 @@
 
 namespace zf {
 
-constexpr int kQ4Threads = 256;
+constexpr int kQ4Threads = 128;
 
 struct Q4Args {
   uint8_t* records;
@@ -46,41 +46,58 @@ __device__ __forceinline__ uint8_t* q4_record(const Q4Args& a, int i, int h, int
   return a.records + ((static_cast<size_t>(pid) * a.hkv + h) * (a.page_size >> 4) + (pos >> 4)) * kQ4Record;
 }
 
-// Thread index -> (entry, head, K or V, block): [n][hkv][2][8].
-__global__ void __launch_bounds__(kQ4Threads) q4_write_kernel(const Q4Args a) {
-  allow_next_grid();
-  wait_prior_grid();
-  const long long g = static_cast<long long>(blockIdx.x) * kQ4Threads + threadIdx.x;
-  const int block = static_cast<int>(g & 7);
-  const bool is_v = (g >> 3) & 1;
-  const long long row = g >> 4;                       // entry * hkv + head
-  if (row >= static_cast<long long>(a.n) * a.hkv) return;
-  const int i = static_cast<int>(row / a.hkv), h = static_cast<int>(row - static_cast<long long>(i) * a.hkv);
-  int tok = 0;
-  uint8_t* rec = q4_record(a, i, h, tok, h == 0 && (g & 15) == 0);
-  if (!rec) return;
-  const uint4* src = reinterpret_cast<const uint4*>((is_v ? a.v : a.k) + row * ZF_HEAD_DIM + block * 16);
-  const uint4 lo = src[0], hi = src[1];
-  const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-  const float inv = is_v ? a.v_inv : a.k_inv;
-  float t[16];
-  float amax = 0.f;
-  bool odd = false;                                   // a NaN or an infinity among the values
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t bits = (j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16;
-    odd |= (bits & 0x7F800000u) == 0x7F800000u;
-    float x = __uint_as_float(bits) * inv;
-    x = x != x ? 0.f : x;
-    t[j] = fminf(fmaxf(x, -65536.f), 65536.f);        // beyond 6 * 448: saturates either way
-    amax = fmaxf(amax, fabsf(t[j]));
+// Thread index -> (entry, head, block): [n][hkv][8].
+struct Q4Place {
+  uint8_t* rec;
+  size_t src;               // first value of the block in a [n][hkv][128] array
+  int tok, block;
+  bool in;                  // within the call
+};
+__device__ __forceinline__ Q4Place q4_place(const Q4Args& a) {
+  const size_t g = static_cast<size_t>(blockIdx.x) * kQ4Threads + threadIdx.x;
+  const uint32_t row = static_cast<uint32_t>(g >> 3);           // entry * hkv + head, below 2^31
+  Q4Place p;
+  p.block = static_cast<int>(g & 7);
+  p.src = g * 16;
+  p.tok = 0;
+  p.in = (g >> 3) < static_cast<size_t>(a.n) * a.hkv;
+  p.rec = nullptr;
+  if (p.in) {
+    const int i = static_cast<int>(row / static_cast<uint32_t>(a.hkv));
+    const int h = static_cast<int>(row - static_cast<uint32_t>(i) * a.hkv);
+    p.rec = q4_record(a, i, h, p.tok, h == 0 && p.block == 0);
   }
-  if (odd) report(a.status, ZF_DEV_NOT_FINITE);
+  return p;
+}
+
+// One block of 16 BF16 values (as eight words) -> codes and scale byte; odd: a NaN or an infinity among
+// them.  The largest magnitude is found on the bit patterns, two at a time; a block with something that is
+// not finite, or beyond every code, is cleaned up first.
+__device__ __forceinline__ uint2 q4_quantise(const uint32_t (&w)[8], float inv, uint32_t& sbyte, bool& odd) {
+  float t[16];
+  uint32_t big2 = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    big2 = __vmaxu2(big2, w[j] & 0x7FFF7FFFu);
+    t[2 * j] = bf16lo_to_f32(w[j]) * inv;
+    t[2 * j + 1] = bf16hi_to_f32(w[j]) * inv;
+  }
+  const uint32_t big = max(big2 & 0xFFFFu, big2 >> 16);
+  float amax = __uint_as_float(big << 16) * inv;      // rounding keeps the order: this is max |t|
+  if (!(amax <= 65536.f)) {                           // 6 * 448 and less are the values that codes reach
+    odd |= big >= 0x7F80u;
+    amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      t[j] = t[j] != t[j] ? 0.f : fminf(fmaxf(t[j], -65536.f), 65536.f);       // saturates either way
+      amax = fmaxf(amax, fabsf(t[j]));
+    }
+  }
   // scale: e4m3 of max / 6, at least its smallest positive number
   uint16_t pair;
   const float want = amax > 0.f ? fmaxf(__fdiv_rn(amax, 6.f), 0.001953125f) : 0.f;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(pair) : "f"(0.f), "f"(want));
-  const uint32_t sbyte = pair & 0xFFu;
+  sbyte = pair & 0xFFu;
   const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sbyte << 7))) * kQ4ScaleFactor;
   const float r = sbyte ? __frcp_rn(s) : 0.f;
   uint32_t codes[2];
@@ -95,9 +112,31 @@ __global__ void __launch_bounds__(kQ4Threads) q4_write_kernel(const Q4Args a) {
     }
     codes[half] = q4_encode8(q);
   }
-  *reinterpret_cast<uint2*>(rec + (is_v ? q4_v_code_at(tok, block) : q4_k_code_at(tok, block))) =
-      make_uint2(codes[0], codes[1]);
-  rec[is_v ? q4_v_scale_at(tok, block) : q4_k_scale_at(tok, block)] = static_cast<uint8_t>(sbyte);
+  return make_uint2(codes[0], codes[1]);
+}
+
+__global__ void __launch_bounds__(kQ4Threads) q4_write_kernel(const Q4Args a) {
+  allow_next_grid();
+  wait_prior_grid();
+  const Q4Place p = q4_place(a);
+  if (!p.rec) return;
+  uint32_t w[2][8];
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const uint4* src = reinterpret_cast<const uint4*>((v ? a.v : a.k) + p.src);
+    const uint4 lo = src[0], hi = src[1];
+    w[v][0] = lo.x; w[v][1] = lo.y; w[v][2] = lo.z; w[v][3] = lo.w;
+    w[v][4] = hi.x; w[v][5] = hi.y; w[v][6] = hi.z; w[v][7] = hi.w;
+  }
+  bool odd = false;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    uint32_t sbyte;
+    const uint2 codes = q4_quantise(w[v], v ? a.v_inv : a.k_inv, sbyte, odd);
+    *reinterpret_cast<uint2*>(p.rec + (v ? q4_v_code_at(p.tok, p.block) : q4_k_code_at(p.tok, p.block))) = codes;
+    p.rec[v ? q4_v_scale_at(p.tok, p.block) : q4_k_scale_at(p.tok, p.block)] = static_cast<uint8_t>(sbyte);
+  }
+  if (odd) report(a.status, ZF_DEV_NOT_FINITE);
 }
 
 // Values of the listed tokens as BF16: code * s * cache scale, rounded once (exact when the cache
@@ -105,35 +144,37 @@ __global__ void __launch_bounds__(kQ4Threads) q4_write_kernel(const Q4Args a) {
 __global__ void __launch_bounds__(kQ4Threads) q4_read_kernel(const Q4Args a) {
   allow_next_grid();
   wait_prior_grid();
-  const long long g = static_cast<long long>(blockIdx.x) * kQ4Threads + threadIdx.x;
-  const int block = static_cast<int>(g & 7);
-  const bool is_v = (g >> 3) & 1;
-  const long long row = g >> 4;
-  if (row >= static_cast<long long>(a.n) * a.hkv) return;
-  const int i = static_cast<int>(row / a.hkv), h = static_cast<int>(row - static_cast<long long>(i) * a.hkv);
-  int tok = 0;
-  const uint8_t* rec = q4_record(a, i, h, tok, h == 0 && (g & 15) == 0);
-  uint32_t out[8] = {};
-  if (rec) {
-    const uint2 codes = *reinterpret_cast<const uint2*>(rec + (is_v ? q4_v_code_at(tok, block) : q4_k_code_at(tok, block)));
-    const uint32_t sbyte = rec[is_v ? q4_v_scale_at(tok, block) : q4_k_scale_at(tok, block)] & 0x7Fu;
+  const Q4Place p = q4_place(a);
+  if (!p.in) return;
+  uint2 codes[2] = {};
+  uint32_t sbyte[2] = {0u, 0u};
+  if (p.rec) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      codes[v] = *reinterpret_cast<const uint2*>(p.rec + (v ? q4_v_code_at(p.tok, p.block) : q4_k_code_at(p.tok, p.block)));
+      sbyte[v] = p.rec[v ? q4_v_scale_at(p.tok, p.block) : q4_k_scale_at(p.tok, p.block)] & 0x7Fu;
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
     // code * s is exact in float (two and four significant bits)
-    const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sbyte << 7))) * kQ4ScaleFactor;
-    const float g_scale = is_v ? a.v_scale : a.k_scale;
+    const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(sbyte[v] << 7))) * kQ4ScaleFactor;
+    const float g_scale = v ? a.v_scale : a.k_scale;
+    uint32_t out[8];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      uint32_t p[4];
-      q4_decode4(half ? codes.y : codes.x, p);
+      uint32_t h[4];
+      q4_decode4(half ? codes[v].y : codes[v].x, h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
+        const float2 c = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
         out[4 * half + j] = pack_bf16x2(c.x * s * g_scale, c.y * s * g_scale);
       }
     }
+    uint4* dst = reinterpret_cast<uint4*>((v ? a.v_out : a.k_out) + p.src);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
   }
-  uint4* dst = reinterpret_cast<uint4*>((is_v ? a.v_out : a.k_out) + row * ZF_HEAD_DIM + block * 16);
-  dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-  dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 static zf_status q4_tokens(const zf_q4_cache* c, const void* k, const void* v, const int32_t* page_ids,
@@ -145,9 +186,9 @@ static zf_status q4_tokens(const zf_q4_cache* c, const void* k, const void* v, c
   if (!k || !v || !page_ids || !positions || !aligned16(k) || !aligned16(v) ||
       (reinterpret_cast<uintptr_t>(page_ids) & 3u) || (reinterpret_cast<uintptr_t>(positions) & 3u))
     return ZF_ERR_INVALID_ARGUMENT;
-  const long long threads = static_cast<long long>(n) * c->num_kv_heads * 16;
-  const long long blocks = (threads + kQ4Threads - 1) / kQ4Threads;
-  if (blocks > 0x7FFFFFFFll) return ZF_ERR_UNSUPPORTED;
+  const long long rows = static_cast<long long>(n) * c->num_kv_heads;
+  if (rows > 0x7FFFFFFFll) return ZF_ERR_UNSUPPORTED;
+  const long long blocks = (rows * 8 + kQ4Threads - 1) / kQ4Threads;
   Q4Args a{};
   a.records = c->records;
   a.status = c->status;

@@ -107,11 +107,11 @@ __device__ __forceinline__ DF warp_scan(DF v, int lane) {
 }
 
 // A batch: the weights of kBatch consecutive entries from i0 (0 from hi on), kLane per lane, read
-// together.  kVec: rows are 16-byte aligned, i0 and hi multiples of 4; lane l then holds entries
-// i0 + 128 k + 4 l .. + 3 as w[4 k ..], else i0 + 32 k + l as w[k].
+// together.  kVec: rows are 16-byte aligned, i0 and hi multiples of 4.  kRuns (and kVec): lane l holds
+// entries i0 + 128 k + 4 l .. + 3 as w[4 k ..], else i0 + 32 k + l as w[k].
 constexpr int kLane = 16;
 constexpr int kBatch = 32 * kLane;
-template <bool kVec, bool kHasQ>
+template <bool kVec, bool kHasQ, bool kRuns = kVec>
 __device__ __forceinline__ void load_batch(const Row& r, int i0, int hi, int lane, float (&w)[kLane]) {
   float q[kLane];
   if (kVec) {
@@ -129,14 +129,14 @@ __device__ __forceinline__ void load_batch(const Row& r, int i0, int hi, int lan
   } else {
 #pragma unroll
     for (int k = 0; k < kLane; ++k) {
-      const int i = i0 + 32 * k + lane;
+      const int i = kRuns ? i0 + 128 * (k / 4) + 4 * lane + k % 4 : i0 + 32 * k + lane;
       w[k] = i < hi ? r.p[i] : 0.f;
       q[k] = kHasQ && i < hi ? r.q[i] : 0.f;
     }
   }
 #pragma unroll
   for (int k = 0; k < kLane; ++k) {
-    const int i = kVec ? i0 + 128 * (k / 4) + 4 * lane + k % 4 : i0 + 32 * k + lane;
+    const int i = kRuns ? i0 + 128 * (k / 4) + 4 * lane + k % 4 : i0 + 32 * k + lane;
     const float x = kHasQ ? w[k] - q[k] : i == r.drop ? w[k] - 1.f : w[k];
     w[k] = x > 0.f ? x : 0.f;
   }
@@ -177,8 +177,8 @@ __device__ __forceinline__ int scan_block(const Row& r, int lo, int hi, DF run, 
   int last = -1;
   for (int i0 = lo; i0 < hi; i0 += kBatch) {
     float w[kLane];
-    load_batch<kVec, kHasQ>(r, i0, hi, lane, w);
-    constexpr int kRun = kVec ? 4 : 1;                 // consecutive entries of a lane
+    load_batch<kVec, kHasQ, true>(r, i0, hi, lane, w);
+    constexpr int kRun = 4;                            // consecutive entries of a lane: a quarter of the scans
 #pragma unroll
     for (int k = 0; k < kLane / kRun; ++k) {
       DF own = {0.f, 0.f};
@@ -254,7 +254,7 @@ __device__ __forceinline__ int find(const float2* sums, int n, float u, bool giv
 
 // Grid: one cluster per request.
 template <bool kVec>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyArgs a) {
   __shared__ float2 sums[kVerifyMaxCluster * kVerifyWarps];   // of every warp of the cluster
   __shared__ float2 blocks[kVerifyWarps][kMaxBlocks];         // of this CTA's pieces
   __shared__ int sh_piece, sh_zero;
@@ -272,30 +272,39 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
 
   // ---- accepted drafts (warp 0 of every CTA; T <= 64: two per lane)
   if (warp == 0) {
+    // the drafts and their random numbers are read along with the count: two round trips in all
+    static_assert(ZF_MAX_TOKENS <= 64, "two drafts per lane");
+    int x[2];
+    float v[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int t = lane + 32 * k;
+      x[k] = t < T ? a.tokens_in[static_cast<size_t>(b) * T + t] : -1;
+      v[k] = t < T ? a.uniform[static_cast<size_t>(b) * (T + 1) + t] : 0.f;
+    }
     int n = a.n_drafts ? a.n_drafts[b] : T;
     if (n < 0 || n > T) {
       if (rank == 0 && lane == 0) report(a.status, ZF_DEV_BAD_DRAFT);
       n = min(max(n, 0), T);
     }
+    float p[2], q[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int t = lane + 32 * k;
+      const bool in = t < T && x[k] >= 0 && x[k] < V;
+      p[k] = in ? a.target[(static_cast<size_t>(b) * (T + 1) + t) * V + x[k]] : 0.f;
+      q[k] = in && a.draft ? a.draft[(static_cast<size_t>(b) * T + t) * V + x[k]] : 1.f;
+    }
     int acc = n;
-    for (int t0 = 0; t0 < n; t0 += 32) {
-      const int t = t0 + lane;
-      bool ok = true;
-      if (t < n) {
-        const int x = a.tokens_in[static_cast<size_t>(b) * T + t];
-        if (x < 0 || x >= V) {
-          ok = false;
-          if (rank == 0) report(a.status, ZF_DEV_BAD_DRAFT);
-        } else {
-          const float p = a.target[(static_cast<size_t>(b) * (T + 1) + t) * V + x];
-          const float q = a.draft ? a.draft[(static_cast<size_t>(b) * T + t) * V + x] : 1.f;
-          ok = __fmul_rn(a.uniform[static_cast<size_t>(b) * (T + 1) + t], q) < p;
-        }
-      }
-      const uint32_t refused = __ballot_sync(0xFFFFFFFFu, !ok);
-      if (refused) {
-        acc = t0 + __ffs(refused) - 1;
-        break;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int t = lane + 32 * k;
+      const bool bad = x[k] < 0 || x[k] >= V;
+      const uint32_t refused = __ballot_sync(0xFFFFFFFFu, t < n && (bad || !(__fmul_rn(v[k], q[k]) < p[k])));
+      // (a draft behind the first refused one is not looked at)
+      if (acc == n && refused) {
+        acc = 32 * k + __ffs(refused) - 1;
+        if (rank == 0 && t == acc && bad) report(a.status, ZF_DEV_BAD_DRAFT);
       }
     }
     if (lane == 0) {
