@@ -103,6 +103,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same into a fresh accumulator.
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 8x8 transpose of 16-bit values (as transpose8x8, free to move between other instructions).
 __device__ __forceinline__ uint32_t flip8x8(uint32_t x) {
   uint32_t y;
@@ -131,6 +139,16 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
+}
+
+// d += s, rounded to nearest (the matrix instructions cut their sums off instead: their accumulators are
+// kept short and added here).
+__device__ __forceinline__ void add4(float (&d)[4], const float (&s)[4]) {
+  const F2 a = add2(F2{d[0], d[1]}, F2{s[0], s[1]}), b = add2(F2{d[2], d[3]}, F2{s[2], s[3]});
+  d[0] = a.x;
+  d[1] = a.y;
+  d[2] = b.x;
+  d[3] = b.y;
 }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
@@ -408,11 +426,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         for (int i = 0; i < kUnitTiles; ++i) ntok[i] = (here >> i) & 1u ? min(16, d.t1 - (pos0 + 16 * i)) : 0;
 
         // ---- S^T (16 tokens x 8 kNT columns) = K (16 x 128) . Q^T, per record
-        float x[kNT][kUnitTiles][4];
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int i = 0; i < kUnitTiles; ++i) x[n][i][0] = x[n][i][1] = x[n][i][2] = x[n][i][3] = 0.f;
+        float x[kNT][kUnitTiles][4], y[kNT][kUnitTiles][4];     // (two halves of the channels)
         uint4 kc[kUnitTiles][2];
         uint32_t ks[kUnitTiles][4];      // scale pairs: (row gi, row gi + 8) x (block 2ti, 2ti + 1)
 #pragma unroll
@@ -444,11 +458,17 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
             }
 #pragma unroll
             for (int n = 0; n < kNT; ++n) {
-              mma_f16(x[n][i], ka[0], kb[0], ka[1], kb[1], q[n].x, q[n].y);
-              mma_f16(x[n][i], ka[2], kb[2], ka[3], kb[3], q[n].z, q[n].w);
+              float(&s)[4] = j < 2 ? x[n][i] : y[n][i];
+              if (j % 2 == 0) mma_f16_zero(s, ka[0], kb[0], ka[1], kb[1], q[n].x, q[n].y);
+              else mma_f16(s, ka[0], kb[0], ka[1], kb[1], q[n].x, q[n].y);
+              mma_f16(s, ka[2], kb[2], ka[3], kb[3], q[n].z, q[n].w);
             }
           }
         }
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int i = 0; i < kUnitTiles; ++i) add4(x[n][i], y[n][i]);
 
         // ---- online softmax, log2 domain.  lane: tokens gi, gi + 8 x columns 2ti, 2ti + 1 (per n)
         bool grow = false;
@@ -503,68 +523,84 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           }
         }
 
+        // P^T as the B operand (k = token, n = column): fp16 high part (the float's first 11 bits) and
+        // fp16 remainder (a register pair holds the two columns of a token)
+        uint32_t bh[kNT][kUnitTiles][2], bl[kNT][kUnitTiles][2];
 #pragma unroll
-        for (int i = 0; i < kUnitTiles; ++i) {
-          // P^T as the B operand (k = token, n = column): fp16 high part (the float's first 11 bits)
-          // and fp16 remainder
-          uint32_t bh[kNT][2], bl[kNT][2];
+        for (int n = 0; n < kNT; ++n) {
 #pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            // (a register pair holds the two columns of a token)
-            F2 p[2], hi[2], lo[2];
+          for (int i = 0; i < kUnitTiles; ++i) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const F2 y = fma2(F2{x[n][i][2 * r], x[n][i][2 * r + 1]}, F2{cs[n][0], cs[n][1]}, F2{-mx[n][0], -mx[n][1]});
-              p[r] = F2{fast_exp2(y.x), fast_exp2(y.y)};
-              const F2 sum = add2(F2{l[n][0], l[n][1]}, p[r]);
+              const F2 z = fma2(F2{x[n][i][2 * r], x[n][i][2 * r + 1]}, F2{cs[n][0], cs[n][1]}, F2{-mx[n][0], -mx[n][1]});
+              const F2 p = F2{fast_exp2(z.x), fast_exp2(z.y)};
+              const F2 sum = add2(F2{l[n][0], l[n][1]}, p);
               l[n][0] = sum.x;
               l[n][1] = sum.y;
-              hi[r] = F2{__uint_as_float(__float_as_uint(p[r].x) & 0xFFFFE000u),
-                         __uint_as_float(__float_as_uint(p[r].y) & 0xFFFFE000u)};
-              lo[r] = add2(p[r], F2{-hi[r].x, -hi[r].y});
-              if (kFold) hi[r] = ti < 2 ? hi[r] : lo[r];
-              bh[n][r] = flip8x8(pack_f16x2(hi[r].x, hi[r].y));
-              if (!kFold) bl[n][r] = flip8x8(pack_f16x2(lo[r].x, lo[r].y));
+              F2 hi = F2{__uint_as_float(__float_as_uint(p.x) & 0xFFFFE000u),
+                         __uint_as_float(__float_as_uint(p.y) & 0xFFFFE000u)};
+              const F2 lo = add2(p, F2{-hi.x, -hi.y});
+              if (kFold) hi = ti < 2 ? hi : lo;
+              bh[n][i][r] = flip8x8(pack_f16x2(hi.x, hi.y));
+              if (!kFold) bl[n][i][r] = flip8x8(pack_f16x2(lo.x, lo.y));
             }
           }
+        }
 
-          // ---- O^T (128 channels x columns) += V^T (128 x 16 tokens) . P^T.  m-tile mt: row gi is
-          // channel 16 gi + 2 mt, row gi + 8 the next one; k: tokens 2ti, 2ti+1, 2ti+8, 2ti+9.
+        // ---- O^T (128 channels x columns) += V^T (128 x 16 tokens) . P^T.  m-tile mt: row gi is
+        // channel 16 gi + 2 mt, row gi + 8 the next one; k: tokens 2ti, 2ti+1, 2ti+8, 2ti+9.
+        uint32_t vs[kUnitTiles][2];
+        uint2 vw[kUnitTiles][4];
+#pragma unroll
+        for (int i = 0; i < kUnitTiles; ++i) {
           const uint8_t* rec = st + i * kQ4Record;
           uint32_t w = *reinterpret_cast<const uint32_t*>(rec + kQ4VScales + 16 * gi + 4 * ti) & 0x7F7F7F7Fu;
           if (!full) {              // what lies past the context counts as 0
             w &= (2 * ti < ntok[i] ? 0x000000FFu : 0u) | (2 * ti + 1 < ntok[i] ? 0x0000FF00u : 0u) |
                  (2 * ti + 8 < ntok[i] ? 0x00FF0000u : 0u) | (2 * ti + 9 < ntok[i] ? 0xFF000000u : 0u);
           }
-          const uint32_t s0 = __byte_perm(w, 0u, 0x4140u) << 7, s1 = __byte_perm(w, 0u, 0x4342u) << 7;
-          const uint2 va = *reinterpret_cast<const uint2*>(rec + v_lane);
-          const uint2 vb = *reinterpret_cast<const uint2*>(rec + v_lane + 64);
-          const uint2 vc = *reinterpret_cast<const uint2*>(rec + v_lane + 512);
-          const uint2 vd = *reinterpret_cast<const uint2*>(rec + v_lane + 576);
+          vs[i][0] = __byte_perm(w, 0u, 0x4140u) << 7;
+          vs[i][1] = __byte_perm(w, 0u, 0x4342u) << 7;
+          vw[i][0] = *reinterpret_cast<const uint2*>(rec + v_lane);
+          vw[i][1] = *reinterpret_cast<const uint2*>(rec + v_lane + 64);
+          vw[i][2] = *reinterpret_cast<const uint2*>(rec + v_lane + 512);
+          vw[i][3] = *reinterpret_cast<const uint2*>(rec + v_lane + 576);
+        }
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t wa = h ? va.y : va.x, wb = h ? vb.y : vb.x, wc = h ? vc.y : vc.x, wd = h ? vd.y : vd.x;
-            uint32_t a0[4], a1[4], a2[4], a3[4];
-            q4_decode4((wa & 0x0F0F0F0Fu) | ((wb << 4) & 0xF0F0F0F0u), a0);
-            q4_decode4(((wa >> 4) & 0x0F0F0F0Fu) | (wb & 0xF0F0F0F0u), a1);
-            q4_decode4((wc & 0x0F0F0F0Fu) | ((wd << 4) & 0xF0F0F0F0u), a2);
-            q4_decode4(((wc >> 4) & 0x0F0F0F0Fu) | (wd & 0xF0F0F0F0u), a3);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t v[kUnitTiles][4][4];       // [record][register of the operand][m-tile]
+#pragma unroll
+          for (int i = 0; i < kUnitTiles; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = h ? vw[i][k].y : vw[i][k].x;
+            q4_decode4((w[0] & 0x0F0F0F0Fu) | ((w[1] << 4) & 0xF0F0F0F0u), v[i][0]);
+            q4_decode4(((w[0] >> 4) & 0x0F0F0F0Fu) | (w[1] & 0xF0F0F0F0u), v[i][1]);
+            q4_decode4((w[2] & 0x0F0F0F0Fu) | ((w[3] << 4) & 0xF0F0F0F0u), v[i][2]);
+            q4_decode4(((w[2] >> 4) & 0x0F0F0F0Fu) | (w[3] & 0xF0F0F0F0u), v[i][3]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              a0[e] = mul_f16x2(a0[e], s0);
-              a1[e] = mul_f16x2(a1[e], s0);
-              a2[e] = mul_f16x2(a2[e], s1);
-              a3[e] = mul_f16x2(a3[e], s1);
+              v[i][0][e] = mul_f16x2(v[i][0][e], vs[i][0]);
+              v[i][1][e] = mul_f16x2(v[i][1][e], vs[i][0]);
+              v[i][2][e] = mul_f16x2(v[i][2][e], vs[i][1]);
+              v[i][3][e] = mul_f16x2(v[i][3][e], vs[i][1]);
             }
+          }
 #pragma unroll
-            for (int n = 0; n < kNT; ++n)
+          for (int n = 0; n < kNT; ++n) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mma_f16(o[n][4 * h + e], a0[e], a1[e], a2[e], a3[e], bh[n][0], bh[n][1]);
-            if (!kFold) {
+            for (int e = 0; e < 4; ++e) {
+              float s[4];
+              mma_f16_zero(s, v[0][0][e], v[0][1][e], v[0][2][e], v[0][3][e], bh[n][0][0], bh[n][0][1]);
 #pragma unroll
-            for (int n = 0; n < kNT; ++n)
+              for (int i = 1; i < kUnitTiles; ++i)
+                mma_f16(s, v[i][0][e], v[i][1][e], v[i][2][e], v[i][3][e], bh[n][i][0], bh[n][i][1]);
+              if (!kFold) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mma_f16(o[n][4 * h + e], a0[e], a1[e], a2[e], a3[e], bl[n][0], bl[n][1]);
+                for (int i = 0; i < kUnitTiles; ++i)
+                  mma_f16(s, v[i][0][e], v[i][1][e], v[i][2][e], v[i][3][e], bl[n][i][0], bl[n][i][1]);
+              }
+              add4(o[n][4 * h + e], s);
             }
           }
         }
