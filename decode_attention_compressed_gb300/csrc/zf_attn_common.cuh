@@ -331,12 +331,10 @@ __device__ __forceinline__ int load_lengths(const AttnArgs& a, int* prefix, int*
   return mine;
 }
 
-// kItemTiles, kItemPages: the largest item (an attention kernel's metadata buffers).
-template <int kItemTiles = kMaxItemTiles, int kItemPages = kMaxItemPages>
 __device__ __forceinline__ Ranges make_ranges(const AttnArgs& a, int total) {
   Ranges g;
   g.W = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), a.min_range_pages);
-  g.pmax = min(kItemTiles / (a.page_size / ZF_BLOCK_TOKENS), kItemPages);
+  g.pmax = min(kMaxItemTiles / (a.page_size / ZF_BLOCK_TOKENS), kMaxItemPages);
   g.ppc = (g.W + g.pmax - 1) / g.pmax;
   return g;
 }
@@ -425,16 +423,15 @@ struct MergeArgs {
 //  * fixed chunks of cp pages, items dealt round-robin: for short contexts, where the per-item cost
 //    dominates and chunks that never straddle a request boundary save items.
 // hps: query heads per head slice (the columns one kernel pass gives a kv head's tiles).
-// item_tiles, item_pages: the kernel's largest item (as in make_ranges).
 static Plan make_plan(int batch, int hq, int hkv, int page_size, int max_pages, int num_sms, int warps,
-                      int hps = kHeadsPerSlice, int item_tiles = kMaxItemTiles, int item_pages = kMaxItemPages) {
+                      int hps = kHeadsPerSlice) {
   Plan p;
   const int group = hq / hkv;
   p.slices = (group + hps - 1) / hps;
   const long long pairs = static_cast<long long>(batch) * hkv * p.slices;
   const long long total_max = pairs * max_pages;     // pages when every request is full length
   const int tpp = page_size / ZF_BLOCK_TOKENS;
-  const int pmax = item_tiles / tpp < item_pages ? item_tiles / tpp : item_pages;
+  const int pmax = kMaxItemTiles / tpp < kMaxItemPages ? kMaxItemTiles / tpp : kMaxItemPages;
   const int grid_b = static_cast<int>(total_max < num_sms ? (total_max > 0 ? total_max : 1) : num_sms);
   const long long balanced = (total_max + grid_b - 1) / grid_b;
   auto rounds = [&](long long tiles) { return (tiles + warps - 1) / warps; };
