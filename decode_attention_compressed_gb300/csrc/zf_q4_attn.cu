@@ -46,6 +46,7 @@ namespace {
 constexpr int kUnitTiles = 2;                            // records per stage
 constexpr int kStageQ4 = kUnitTiles * kQ4Record;         // 4608
 constexpr int kQ4QRowBytes = 320;                        // q row in shared memory (see store_q_row)
+constexpr int kFewPartials = 20;
 constexpr float kPShift = 7.f;                           // weights are 2^7 times their usual size
 
 // Warps per CTA by the number of 8-column tiles of a pass (kNT), from the registers they need (128, 168
@@ -198,6 +199,16 @@ __device__ __forceinline__ void stage_q(const Q4AttnArgs& a, int b, int h0, int 
   }
 }
 
+// Records per range: an equal share of the total, but enough that a pair's partials stay few (the square of
+// the length times kFewPartials at least the mean records of a pair; one request of 8192 tokens, 8 kv
+// heads: 26.0 us with the equal share of 2 records and up to 256 partials, 10.7 with 6 and 86); an even
+// number, so that units are whole.
+__host__ __device__ inline int range_length(long long total, int ranges, int mean) {
+  int W = static_cast<int>((total + 2LL * ranges - 1) / (2LL * ranges)) * 2;
+  while (W > 0 && static_cast<long long>(W) * W * kFewPartials < mean) W += 2;
+  return W;
+}
+
 // A warp's place in its range: the next record is `tile` of pair (b, r) (r: kv head * slices + slice), whose
 // request has n of them; `left` records remain.  page, in: the record's page and place in it.
 struct Cursor {
@@ -320,8 +331,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   const int HS = a.hkv * a.slices, tpp = a.page_size >> 4;
   const long long total = static_cast<long long>(HS) * prefix[a.batch];
   const int ranges = gridDim.x * kWarps;
-  // an even number of records per range, so that units are whole
-  const int W = static_cast<int>((total + 2LL * ranges - 1) / (2LL * ranges)) * 2;
+  const int W = range_length(total, ranges, prefix[a.batch] / a.batch);
   if (blockIdx.x == 0) {                                 // for the merge
     for (int b = tid; b <= a.batch; b += C::kThreads) a.prefix[b] = prefix[b];
     if (tid == 0) a.prefix[a.batch + 1] = W;
@@ -643,8 +653,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   }
 }
 
-// The merge: one CTA per (request, query head, new token), its warps taking turns at the partials.  A
-// partial holds its weighted sum of values as it is, its maximum and its sum; the maxima are whole
+// The merge: kPerRow warps per (request, query head, new token) take turns at its partials.  A partial holds its weighted sum of values as it is, its maximum and its sum; the maxima are whole
 // numbers, so the partials' factors are powers of two and the merge adds no rounding but those of its
 // sums (a log-sum-exp near 20, kept as one float, would be off by 2^-20 in each weight).  Rows whose
 // pair lies in one range were finished by the attention kernel.
@@ -657,40 +666,50 @@ struct Q4MergeArgs {
   int32_t batch, hq, group, slices, tokens, cols;
   float v_factor;
 };
-constexpr int kQ4MergeWarps = 4;
-constexpr int kMergePre = 4;                     // partials a warp reads at once
-__global__ void __launch_bounds__(kQ4MergeWarps * 32) q4_merge_kernel(const Q4MergeArgs a) {
-  __shared__ float4 sh_o[kQ4MergeWarps][32];
-  __shared__ float2 sh_ml[kQ4MergeWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int idx = blockIdx.x;
-  const int b = idx / a.hq, h = idx - b * a.hq;
+constexpr int kMergePre = 8;                     // partials a warp reads at once
+constexpr int kMergeOne = 16, kMergeFour = 48;    // up to so many partials: one or four warps per row
+template <int kPerRow>
+constexpr int kMergeRows = kPerRow < 4 ? 4 / kPerRow : 1;          // rows per CTA
+template <int kPerRow>
+__global__ void __launch_bounds__(kMergeRows<kPerRow> * kPerRow * 32) q4_merge_kernel(const Q4MergeArgs a) {
+  constexpr int kRows = kMergeRows<kPerRow>;
+  __shared__ float4 sh_o[kRows * kPerRow][32];
+  __shared__ float2 sh_ml[kRows * kPerRow];
+  const int lane = threadIdx.x & 31;
+  const int all = threadIdx.x >> 5, warp = all % kPerRow, base = all - warp;      // warp: among the row's
+  const int idx = blockIdx.x * kRows + all / kPerRow;
+  const bool in = idx < a.batch * a.hq;
+  const int b = in ? idx / a.hq : 0, h = in ? idx - b * a.hq : 0;
   const int g = h / a.group, hg = h - g * a.group;
   const int s = hg / a.cols, col = hg - s * a.cols;
   allow_next_grid();
   wait_prior_grid();
   const int p0 = a.prefix[b], n = a.prefix[b + 1] - p0, W = a.prefix[a.batch + 1];
   const size_t row = query_row(b, h, a.tokens, a.hq);
-  if (n == 0) {                                  // an empty request
+  if (in && n == 0) {                            // an empty request
     if (warp == 0) *reinterpret_cast<float4*>(a.out + row * ZF_HEAD_DIM + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (threadIdx.x == 0) a.lse[row] = -CUDART_INF_F;
-    return;
+    if (warp == 0 && lane == 0) a.lse[row] = -CUDART_INF_F;
   }
   const int HS = a.hq / a.group * a.slices;
   const long long S = static_cast<long long>(HS) * p0 + static_cast<long long>(g * a.slices + s) * n;
-  const int k0 = static_cast<int>(S / W), k1 = static_cast<int>((S + n - 1) / W);
-  if (k0 == k1) return;
+  int k0 = 0, k1 = 0;
+  if (in && n > 0) {
+    k0 = static_cast<int>(S / W);
+    k1 = static_cast<int>((S + n - 1) / W);
+  }
+  if (k0 == k1 && kRows == 1) return;            // (the warps of other rows of the CTA meet at a barrier below)
+  const bool live = k0 != k1;
   // range k's partial of this pair: its first, unless the pair began within range k0
   const int first = S == static_cast<long long>(k0) * W ? 0 : 1;
   auto at = [&](int k) { return (static_cast<size_t>(k) * 2 + (k == k0 ? first : 0)) * a.cols + col; };
   float M = kNoScore, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k = k0 + warp; k <= k1; k += kQ4MergeWarps * kMergePre) {
+  for (int k = k0 + warp; live && k <= k1; k += kPerRow * kMergePre) {
     float2 ml[kMergePre];
     float4 v[kMergePre];
 #pragma unroll
     for (int j = 0; j < kMergePre; ++j) {
-      const int kk = k + j * kQ4MergeWarps;
+      const int kk = k + j * kPerRow;
       ml[j] = make_float2(kNoScore, 0.f);
       v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (kk <= k1) {
@@ -715,24 +734,27 @@ __global__ void __launch_bounds__(kQ4MergeWarps * 32) q4_merge_kernel(const Q4Me
       acc.w += f * v[j].w;
     }
   }
-  sh_o[warp][lane] = acc;
-  if (lane == 0) sh_ml[warp] = make_float2(M, sum);
-  __syncthreads();
-  if (warp != 0) return;
+  if (kPerRow > 1) {
+    sh_o[all][lane] = acc;
+    if (lane == 0) sh_ml[all] = make_float2(M, sum);
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-  for (int w = 1; w < kQ4MergeWarps; ++w) M = fmaxf(M, sh_ml[w].x);
-  sum = 0.f;
-  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 1; w < kPerRow; ++w) M = fmaxf(M, sh_ml[base + w].x);
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int w = 0; w < kQ4MergeWarps; ++w) {
-    const float f = fast_exp2(sh_ml[w].x - M);
-    sum += f * sh_ml[w].y;
-    const float4 v = sh_o[w][lane];
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
+    for (int w = 0; w < kPerRow; ++w) {
+      const float f = fast_exp2(sh_ml[base + w].x - M);
+      sum += f * sh_ml[base + w].y;
+      const float4 v = sh_o[base + w][lane];
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
   }
+  if (!live) return;
   const float inv = sum == 0.f ? 0.f : a.v_factor / sum;           // a NaN sum stays a NaN
   *reinterpret_cast<float4*>(a.out + row * ZF_HEAD_DIM + 4 * lane) =
       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
@@ -875,5 +897,11 @@ extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, 
   m.tokens = tokens;
   m.cols = 8 * p.nt;
   m.v_factor = a.v_factor;
-  return launch_pdl(q4_merge_kernel, batch * hq, kQ4MergeWarps * 32, 0, s, m);
+  // warps per row by the partials that a pair of the largest length has (one warp reads kMergePre at once)
+  const int rows = batch * hq, most = max_pages * (c->page_size / 16);
+  const long long total = static_cast<long long>(batch) * c->num_kv_heads * p.slices * most;
+  const int parts = most / range_length(total, p.grid * q4_warps(p.nt), most) + 1;
+  if (parts <= kMergeOne) return launch_pdl(q4_merge_kernel<1>, (rows + 3) / 4, 128, 0, s, m);
+  if (parts <= kMergeFour) return launch_pdl(q4_merge_kernel<4>, rows, 128, 0, s, m);
+  return launch_pdl(q4_merge_kernel<16>, rows, 512, 0, s, m);
 }
