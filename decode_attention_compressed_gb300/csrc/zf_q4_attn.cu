@@ -11,7 +11,7 @@
 //
 // Work split.  The 16-token records of all (request, kv head, column slice) pairs, laid end to end, are
 // cut into one equal contiguous range per warp of the grid (one CTA per SM).  A warp goes through its
-// range on its own: it walks the pairs, reads page ids 32 at a time, stages its pair's query rows,
+// range on its own: it walks the pairs, works out 32 records' addresses at a time, stages its pair's query rows,
 // streams units of two records into two private shared-memory stages (one 2304-byte bulk copy per
 // record, the next unit's under way while it works on this one) and, where a pair ends or its range
 // does, writes the result (a pair that lies within the range) or a partial: its weighted sum of
@@ -209,75 +209,73 @@ __host__ __device__ inline int range_length(long long total, int ranges, int mea
   return W;
 }
 
-// A warp's place in its range: the next record is `tile` of pair (b, r) (r: kv head * slices + slice), whose
-// request has n of them; `left` records remain.  page, in: the record's page and place in it.
-struct Cursor {
-  int b, r, tile, n, left, page, in;
+// What a warp still has to fetch.  Records are taken in batches of up to 32 of one pair, whose addresses the
+// lanes work out once (lane i: record i); units are handed out from the batch.
+struct Feed {
+  int b, r, tile, n, left;       // the next batch: record `tile` of pair (b, r) (r: kv head * slices + slice) with n; left in the range
+  int bb, br, bt, count, pos;    // the batch: its pair, first record and length; the next unit's first record in it
+  uint32_t good;                 // bit i: record i's page id is good
+  bool starts, ends, closes;     // the batch begins its pair (or the range); it ends its pair; it ends its pair or the range
+  const uint8_t* addr;
 };
 
 // Up to kUnitTiles consecutive records of one pair.
 struct Unit {
-  int b, r, tile, count;
-  bool last;               // the pair or the range ends with it
-  uint32_t have;           // bit i: record i's copy was started (its page id is good)
-};
-
-// Page ids base .. base + 31 of request b, one per lane.
-struct Pages {
-  int b, base, id;
+  int b, r, tile;
+  uint32_t have;                 // bit i: record i's copy was started (its page id is good)
+  bool start, ends, last;        // the pair (or range) begins with it; the pair ends with it; the pair or the range does
 };
 
 __device__ __forceinline__ int tiles_of(const int* prefix, int b) { return prefix[b + 1] - prefix[b]; }
 
-// Take the cursor's next unit and start its copies into `stage`.
-__device__ __forceinline__ Unit next_unit(const Q4AttnArgs& a, const int* prefix, int HS, int tpp, Cursor& c, Pages& pg,
+__device__ __forceinline__ void next_batch(const Q4AttnArgs& a, const int* prefix, int HS, int tpp, Feed& f, int lane) {
+  f.starts = f.tile == 0 || f.count == 0;
+  f.bb = f.b;
+  f.br = f.r;
+  f.bt = f.tile;
+  f.count = min(min(32, f.n - f.tile), f.left);
+  f.pos = 0;
+  const int t = f.tile + lane, page = t / tpp, in = t - page * tpp;
+  const int id = lane < f.count ? a.page_table[static_cast<size_t>(f.b) * a.max_pages + page] : -1;
+  const bool ok = id >= 0 && id < a.num_pages;
+  if (lane < f.count && !ok) report(a.status, ZF_DEV_BAD_PAGE_ID);
+  f.good = __ballot_sync(0xFFFFFFFFu, ok);
+  const int g = a.slices == 1 ? f.r : f.r / a.slices;
+  f.addr = a.records + ((static_cast<size_t>(ok ? id : 0) * a.hkv + g) * tpp + in) * kQ4Record;
+  f.tile += f.count;
+  f.left -= f.count;
+  f.ends = f.tile == f.n;
+  f.closes = f.ends || f.left == 0;
+  if (f.ends && f.left > 0) {                            // the next pair with records
+    f.tile = 0;
+    if (++f.r == HS) {
+      f.r = 0;
+      do ++f.b; while (tiles_of(prefix, f.b) == 0);
+      f.n = tiles_of(prefix, f.b);
+    }
+  }
+}
+
+// Take the next unit and start its copies into `stage`.
+__device__ __forceinline__ Unit next_unit(const Q4AttnArgs& a, const int* prefix, int HS, int tpp, Feed& f,
                                           uint8_t* stage, uint64_t* bar, int lane, uint64_t policy) {
+  static_assert(kUnitTiles == 2, "a lane pair holds a unit");
+  if (f.pos >= f.count) next_batch(a, prefix, HS, tpp, f, lane);
   Unit u;
-  u.b = c.b;
-  u.r = c.r;
-  u.tile = c.tile;
-  u.count = min(min(kUnitTiles, c.n - c.tile), c.left);
-  static_assert(kUnitTiles == 2, "a unit lies on at most two pages");
-  const bool turn = c.in + 1 == tpp;                     // its second record starts the next page
-  if (pg.b != c.b || c.page < pg.base || c.page + (turn ? 1 : 0) >= pg.base + 32) {
-    const int i = c.page + lane;
-    pg.b = c.b;
-    pg.base = c.page;
-    pg.id = i < a.max_pages ? a.page_table[static_cast<size_t>(c.b) * a.max_pages + i] : -1;
-  }
-  // lane i: record i
-  const int mine = lane == 1 && turn ? c.page + 1 : c.page;
-  const int id = __shfl_sync(0xFFFFFFFFu, pg.id, mine - pg.base);
-  const bool ok = lane < u.count && id >= 0 && id < a.num_pages;
-  if (lane < u.count && !ok) report(a.status, ZF_DEV_BAD_PAGE_ID);
-  u.have = __ballot_sync(0xFFFFFFFFu, ok);
+  u.b = f.bb;
+  u.r = f.br;
+  u.tile = f.bt + f.pos;
+  u.have = (f.good >> f.pos) & 3u;
+  u.start = f.starts && f.pos == 0;
   if (u.have != 0) {
-    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(u.have) * kQ4Record);
+    if (lane == f.pos) mbar_arrive_expect_tx(bar, __popc(u.have) * kQ4Record);
     __syncwarp();
-    if (ok) {
-      const int in = lane == 0 ? c.in : turn ? 0 : c.in + 1;
-      const int g = a.slices == 1 ? c.r : c.r / a.slices;
-      const size_t rec = (static_cast<size_t>(id) * a.hkv + g) * tpp + in;
-      bulk_copy_g2s(stage + lane * kQ4Record, a.records + rec * kQ4Record, kQ4Record, bar, policy);
-    }
+    if ((lane & ~1) == f.pos && (f.good >> lane) & 1u)
+      bulk_copy_g2s(stage + (lane & 1) * kQ4Record, f.addr, kQ4Record, bar, policy);
   }
-  // advance
-  c.tile += u.count;
-  c.left -= u.count;
-  c.in += u.count;
-  if (c.in >= tpp) {
-    c.page += tpp == 1 ? u.count : 1;
-    c.in -= tpp == 1 ? u.count : tpp;
-  }
-  u.last = c.tile == c.n || c.left == 0;
-  if (c.tile == c.n && c.left > 0) {                     // the next pair with records
-    c.tile = c.page = c.in = 0;
-    if (++c.r == HS) {
-      c.r = 0;
-      do ++c.b; while (tiles_of(prefix, c.b) == 0);
-      c.n = tiles_of(prefix, c.b);
-    }
-  }
+  f.pos += kUnitTiles;
+  u.last = f.closes && f.pos >= f.count;
+  u.ends = f.ends && f.pos >= f.count;
   return u;
 }
 
@@ -341,28 +339,28 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   const long long lo = static_cast<long long>(range) * W;
   if (lo >= total) return;
 
-  Cursor c;
+  Feed f;
   {
     int l = 0, h = a.batch;                              // the request holding record lo: the largest b with
     while (h - l > 1) {                                  // HS * prefix[b] <= lo that has records
       const int mid = (l + h) >> 1;
       if (static_cast<long long>(HS) * prefix[mid] <= lo) l = mid; else h = mid;
     }
-    c.b = l;
-    c.n = tiles_of(prefix, l);
+    f.b = l;
+    f.n = tiles_of(prefix, l);
     const long long in = lo - static_cast<long long>(HS) * prefix[l];
-    c.r = static_cast<int>(in / c.n);
-    c.tile = static_cast<int>(in - static_cast<long long>(c.r) * c.n);
-    c.left = static_cast<int>(min(static_cast<long long>(W), total - lo));
-    c.page = c.tile / tpp;
-    c.in = c.tile - c.page * tpp;
+    f.r = static_cast<int>(in / f.n);
+    f.tile = static_cast<int>(in - static_cast<long long>(f.r) * f.n);
+    f.left = static_cast<int>(min(static_cast<long long>(W), total - lo));
+    f.count = f.pos = 0;
   }
-  Pages pg{-1, 0, -1};
   const uint64_t policy = l2_evict_first_policy();
   const int gi = lane >> 2, ti = lane & 3;
   const int v_lane = kQ4VCodes + 128 * ti + 8 * (gi ^ ((ti & 1) << 2));     // V codes of tokens 2ti (+1, +8, +9)
   const uint8_t* qrow = qbuf + gi * kQ4QRowBytes + 16 * ti;
   constexpr uint32_t kAll = (1u << kUnitTiles) - 1;
+  const float fold_c = ti < 2 ? 0.f : 1.f;
+  const uint32_t fold_s = ti < 2 ? 0u : 0x80000000u;
 
   float mx[kNT][2], l[kNT][2], cs[kNT][2];      // running maximum (rounded up) less kPShift, sum, score factor; columns 2ti, 2ti+1
   int seen[kNT][2];                             // kMulti: last position those columns see
@@ -370,18 +368,18 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   int len = 0, causal_lim = 0, h0 = 0, nh = 0;
   int slot = 0;                                 // partial of the range the current pair would write
   bool whole = false;                           // the current pair began with its first record
-  bool start = true;                            // the next unit begins a pair
+  int cb = 0;                                   // its request
   uint32_t phase = 0;                           // bit s: parity of the next wait on stage s
   int sidx = 0;
-  Unit u = next_unit(a, prefix, HS, tpp, c, pg, stages, &bars[0], lane, policy);
+  Unit u = next_unit(a, prefix, HS, tpp, f, stages, &bars[0], lane, policy);
   while (true) {
-    const bool more = c.left > 0;
+    const bool more = f.left > 0 || f.pos < f.count;
     Unit next{};
     if (more)
-      next = next_unit(a, prefix, HS, tpp, c, pg, stages + (sidx ^ 1) * kStageQ4, &bars[sidx ^ 1], lane, policy);
-    if (start) {
-      start = false;
+      next = next_unit(a, prefix, HS, tpp, f, stages + (sidx ^ 1) * kStageQ4, &bars[sidx ^ 1], lane, policy);
+    if (u.start) {
       whole = u.tile == 0;
+      cb = u.b;
       len = min(max(a.seq_lens[u.b], 0), max_len);
       const int g = a.slices == 1 ? u.r : u.r / a.slices;
       const int s = u.r - g * a.slices;
@@ -418,7 +416,11 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
       const bool full = u.have == kAll && pos0 + 16 * kUnitTiles <= (kMulti ? min(len, causal_lim + 1) : len);
       int ntok[kUnitTiles];
 #pragma unroll
-      for (int i = 0; i < kUnitTiles; ++i) ntok[i] = (u.have >> i) & 1u ? min(16, len - (pos0 + 16 * i)) : 0;
+      for (int i = 0; i < kUnitTiles; ++i) ntok[i] = 16;
+      if (!full) {
+#pragma unroll
+        for (int i = 0; i < kUnitTiles; ++i) ntok[i] = (u.have >> i) & 1u ? min(16, len - (pos0 + 16 * i)) : 0;
+      }
 
       // ---- S^T (16 tokens x 8 kNT columns) = K (16 x 128) . Q^T, per record
       float x[kNT][kUnitTiles][4];
@@ -527,10 +529,14 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
             const F2 sum = add2(F2{l[n][0], l[n][1]}, p);
             l[n][0] = sum.x;
             l[n][1] = sum.y;
-            F2 hi = F2{__uint_as_float(__float_as_uint(p.x) & 0xFFFFE000u),
-                       __uint_as_float(__float_as_uint(p.y) & 0xFFFFE000u)};
-            const F2 lo = add2(p, F2{-hi.x, -hi.y});
-            if (kFold) hi = ti < 2 ? hi : lo;
+            uint32_t hx = __float_as_uint(p.x) & 0xFFFFE000u, hy = __float_as_uint(p.y) & 0xFFFFE000u;
+            F2 hi, lo;
+            if (kFold) {          // lanes ti < 2: the high part (0 p + h); the others: the remainder (1 p - h)
+              hi = fma2(p, F2{fold_c, fold_c}, F2{__uint_as_float(hx ^ fold_s), __uint_as_float(hy ^ fold_s)});
+            } else {
+              hi = F2{__uint_as_float(hx), __uint_as_float(hy)};
+              lo = add2(p, F2{-hi.x, -hi.y});
+            }
             bh[n][i][r] = flip8x8(pack_f16x2(hi.x, hi.y));
             if (!kFold) bl[n][i][r] = flip8x8(pack_f16x2(lo.x, lo.y));
           }
@@ -598,7 +604,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
     if (u.last) {
       // ---- the pair, or the range, ends: its result or a partial.  A lane holds 16 consecutive channels
       // of two columns (of one, when columns are folded: the halves of a column's sum meet first).
-      const bool done = whole && u.tile + u.count == tiles_of(prefix, u.b);
+      const bool done = whole && u.ends;
       const size_t part = (static_cast<size_t>(range) * 2 + slot) * C::kCols;
       slot = 1;
 #pragma unroll
@@ -609,7 +615,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           float* dst;
           float f = 1.f;
           if (done) {
-            const size_t row = query_row(u.b, h0 + col, a.tokens, a.hq);
+            const size_t row = query_row(cb, h0 + col, a.tokens, a.hq);
             dst = a.out + row * ZF_HEAD_DIM;
             f = s == 0.f ? 0.f : a.v_factor / s;           // a sum of 0: nothing was seen; a NaN sum stays a NaN
             if (gi == 0) a.lse[row] = s == 0.f ? -CUDART_INF_F : (m + log2f(s)) * kLn2;
@@ -644,7 +650,6 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           put(8 * n + 2 * ti + 1, mx[n][1], l[n][1], x[1]);
         }
       }
-      start = true;
     }
     __syncwarp();                // the stage, and at a pair's end the query rows, may be overwritten
     if (!more) break;
