@@ -187,8 +187,8 @@ __device__ __forceinline__ void stage_q(const Q4AttnArgs& a, int b, int h0, int 
       const int c = kFold ? r & 3 : r0 + r;
       const int qh = h0 + min(c, nh - 1);
       const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + query_row(b, qh, a.tokens, a.hq) * ZF_HEAD_DIM);
-      v[r][0] = c < nh ? src[lane] : 0u;
-      v[r][1] = c < nh ? src[lane + 32] : 0u;
+      v[r][0] = c < nh ? __ldg(src + lane) : 0u;            // (read-only: every row's loads may go first)
+      v[r][1] = c < nh ? __ldg(src + lane + 32) : 0u;
     }
 #pragma unroll
     for (int r = 0; r < 8; ++r) {
@@ -362,8 +362,8 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   const float fold_c = ti < 2 ? 0.f : 1.f;
   const uint32_t fold_s = ti < 2 ? 0u : 0x80000000u;
 
-  float mx[kNT][2], l[kNT][2], cs[kNT][2];      // running maximum (rounded up) less kPShift, sum, score factor; columns 2ti, 2ti+1
-  int seen[kNT][2];                             // kMulti: last position those columns see
+  float mx[kNT][2], l[kNT][2];                  // running maximum (rounded up) less kPShift, sum; columns 2ti, 2ti+1
+  float cs[kNT][2];                             // score factor (with several tiles read per unit, to spare registers)
   float o[kNT][8][4];
   int len = 0, causal_lim = 0, h0 = 0, nh = 0;
   int slot = 0;                                 // partial of the range the current pair would write
@@ -394,8 +394,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         for (int e = 0; e < 2; ++e) {
           mx[n][e] = kNoScore;
           l[n][e] = 0.f;
-          cs[n][e] = qscale[8 * n + 2 * ti + e];
-          seen[n][e] = kMulti ? causal_lim + (h0 + (kFold ? (2 * ti + e) & 3 : 8 * n + 2 * ti + e)) % a.tokens : 0;
+          if (kNT == 1) cs[n][e] = qscale[2 * ti + e];
         }
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) o[n][mt][0] = o[n][mt][1] = o[n][mt][2] = o[n][mt][3] = 0.f;
@@ -472,12 +471,20 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           for (int n = 0; n < kNT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int last = kMulti ? seen[n][e] : INT_MAX;
+              // (kMulti) the last position that column sees
+              const int last =
+                  kMulti ? causal_lim + (h0 + (kFold ? (2 * ti + e) & 3 : 8 * n + 2 * ti + e)) % a.tokens : INT_MAX;
               if (gi >= ntok[i] || pos > last) x[n][i][e] = -CUDART_INF_F;
               if (gi + 8 >= ntok[i] || pos + 8 > last) x[n][i][e + 2] = -CUDART_INF_F;
             }
           }
         }
+      }
+      if (kNT > 1) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) cs[n][e] = qscale[8 * n + 2 * ti + e];
       }
       float top[kNT][2];
 #pragma unroll

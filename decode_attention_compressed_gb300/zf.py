@@ -685,10 +685,10 @@ def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_po
         if pad:
             ids, _, pos, _, seq, _, lens, held, start, free = torch.empty(
                 3 * (n + pad) + 3 * B + 2, dtype=torch.int32, device=dev) \
-                .split_with_sizes((n, pad, n, pad, n, pad, B, B, B + 1, 1))
+                .unsafe_split_with_sizes((n, pad, n, pad, n, pad, B, B, B + 1, 1))
         else:
             ids, pos, seq, lens, held, start, free = torch.empty(
-                3 * n + 3 * B + 2, dtype=torch.int32, device=dev).split_with_sizes((n, n, n, B, B, B + 1, 1))
+                3 * n + 3 * B + 2, dtype=torch.int32, device=dev).unsafe_split_with_sizes((n, n, n, B, B, B + 1, 1))
         out = TokenMap(lens, held, free, start, ids, pos, seq)
     else:
         shapes = ((B,), (B,), (1,), (B + 1,), (n,), (n,), (n,))
