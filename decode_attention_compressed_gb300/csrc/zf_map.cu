@@ -277,7 +277,8 @@ extern "C" zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max
                                    int32_t* new_seq_lens, int32_t* new_pages_held, int32_t* new_free_pos,
                                    int32_t* token_start, int32_t* page_ids, int32_t* positions,
                                    int32_t* seq_positions, int32_t max_tokens, int32_t* status, void* stream) {
-  if (batch < 0 || batch > ZF_MAX_BATCH || max_pages < 1 || num_free < 0 || max_tokens < 0)
+  if (batch < 0 || batch > ZF_MAX_BATCH || max_pages < 1 || num_free < 0 || max_tokens < 0 ||
+      max_tokens > (1 << 30))
     return ZF_ERR_INVALID_ARGUMENT;
   if (page_size < ZF_BLOCK_TOKENS || page_size % ZF_BLOCK_TOKENS) return ZF_ERR_INVALID_ARGUMENT;
   if (page_size > ZF_MAX_PAGE_SIZE) return ZF_ERR_UNSUPPORTED;

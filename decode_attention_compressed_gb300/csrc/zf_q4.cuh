@@ -69,9 +69,9 @@ inline zf_status check_q4_cache(const zf_q4_cache* c) {
   if (c->page_size > ZF_MAX_PAGE_SIZE) return ZF_ERR_UNSUPPORTED;
   if (c->num_kv_heads < 1 || c->num_pages < 0) return ZF_ERR_INVALID_ARGUMENT;
   if (c->num_pages > 0 && (!c->records || !aligned16(c->records))) return ZF_ERR_INVALID_ARGUMENT;
-  // positive normal numbers with a normal reciprocal
+  // positive, and far enough from the ends of float for their reciprocals and the stored values
   for (const float s : {c->k_scale, c->v_scale})
-    if (!(s >= 1e-37f && s <= 1e37f)) return ZF_ERR_INVALID_ARGUMENT;
+    if (!(s >= 1e-30f && s <= 1e30f)) return ZF_ERR_INVALID_ARGUMENT;
   if (c->status && (reinterpret_cast<uintptr_t>(c->status) & 3u)) return ZF_ERR_INVALID_ARGUMENT;
   return ZF_OK;
 }

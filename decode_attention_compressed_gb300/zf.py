@@ -7,6 +7,7 @@ loaded on first use and a missing library raises: there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import NamedTuple
@@ -501,16 +502,26 @@ def _tensor(t, name, dtypes, device, shape, write=False):
 _I32, _F32 = (torch.int32,), (torch.float32,)
 
 
-def _launch_stream(stream, device) -> int:
-    """The stream to launch on, its own device being the current one (the kernels take that device's pointers)."""
+def _on_stream(call):
+    """A call given stream= runs with that stream current, so that what it allocates or copies is
+    ordered with its kernels."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, **kw)
+    return wrapped
+
+
+def _launch_stream(device) -> int:
+    """The current stream; the tensors' device has to be the current one (the kernels take its pointers)."""
     if device.type != "cuda":
         raise ValueError(f"the tensors are on {device}: a CUDA device is needed")
     current = torch.cuda.current_device()
     if device.index != current:
         raise ValueError(f"the tensors are on {device}, the current device is cuda:{current}")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(current)
-    return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(current)
 
 
 def _tables(page_table, seq_lens, device, B):
@@ -529,6 +540,7 @@ def _tables(page_table, seq_lens, device, B):
     return page_table.contiguous(), seq_lens.contiguous()
 
 
+# (The calls below also take stream=, a torch.cuda.Stream to run on.)
 class Q4Cache:
     """One layer's 4-bit paged cache in device memory (layout and numbers: include/zf.h, zf_q4).
 
@@ -583,7 +595,8 @@ def _places(cache, page_ids, positions):
     return out
 
 
-def q4_write_tokens(cache: Q4Cache, k_tok, v_tok, page_ids, positions, stream=None):
+@_on_stream
+def q4_write_tokens(cache: Q4Cache, k_tok, v_tok, page_ids, positions):
     """zf_q4_write_tokens: k_tok/v_tok [n][Hkv][128] int16 BF16 bits (or bfloat16) on the device; entry i
     is token positions[i] of page page_ids[i] (position -1: skipped).  Returns the index tensors (keep
     them alive until the stream has consumed them)."""
@@ -592,18 +605,19 @@ def q4_write_tokens(cache: Q4Cache, k_tok, v_tok, page_ids, positions, stream=No
     shape = (n, cache._sizes[1], HEAD_DIM)
     k_tok = _tensor(k_tok, "k_tok", _BITS16, cache._device, shape)
     v_tok = _tensor(v_tok, "v_tok", _BITS16, cache._device, shape)
-    s = _launch_stream(stream, cache._device)
+    s = _launch_stream(cache._device)
     code = lib().zf_q4_write_tokens(cache._ref, k_tok.data_ptr(), v_tok.data_ptr(), ids.data_ptr(), pos.data_ptr(), n, s)
     if code:
         _check("zf_q4_write_tokens", code)
     return ids, pos
 
 
-def q4_read_tokens(cache: Q4Cache, page_ids, positions, stream=None):
+@_on_stream
+def q4_read_tokens(cache: Q4Cache, page_ids, positions):
     """zf_q4_read_tokens: the values held at the listed places, (k, v) [n][Hkv][128] int16 BF16 bits."""
     ids, pos = _places(cache, page_ids, positions)
     n = ids.shape[0]
-    s = _launch_stream(stream, cache._device)
+    s = _launch_stream(cache._device)
     shape = (n, cache._sizes[1], HEAD_DIM)
     k = torch.empty(shape, dtype=torch.int16, device=cache._device)
     v = torch.empty(shape, dtype=torch.int16, device=cache._device)
@@ -617,8 +631,8 @@ def q4_workspace_size(batch, tokens, num_q_heads, num_kv_heads, page_size, max_p
     return int(lib().zf_q4_decode_attn_workspace_size(batch, tokens, num_q_heads, num_kv_heads, page_size, max_pages))
 
 
-def q4_decode_attn(cache: Q4Cache, q, page_table, seq_lens, scale=None, out=None, lse=None, workspace=None,
-                   stream=None):
+@_on_stream
+def q4_decode_attn(cache: Q4Cache, q, page_table, seq_lens, scale=None, out=None, lse=None, workspace=None):
     """zf_q4_decode_attn: decode attention over the 4-bit cache.  q [B][Hq][128], or [B][T][Hq][128] for T
     new tokens per request (token t attends to positions 0 .. seq_lens[b] - T + t), int16 BF16 bits or
     bfloat16.  Returns (out f32 of q's shape, lse f32 without the last dimension)."""
@@ -636,7 +650,10 @@ def q4_decode_attn(cache: Q4Cache, q, page_table, seq_lens, scale=None, out=None
         _tensor(out, "out", _F32, dev, shape, write=True)
     lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if lse is None else \
         _tensor(lse, "lse", _F32, dev, shape[:-1], write=True)
-    s = _launch_stream(stream, dev)
+    if workspace is not None:
+        workspace = _tensor(workspace, "workspace", (getattr(workspace, "dtype", None),), dev,
+                            getattr(workspace, "shape", None), write=True)
+    s = _launch_stream(dev)
     if workspace is None:
         workspace = new_workspace(q4_workspace_size(B, T, Hq, cache._sizes[1], cache._sizes[2], max_pages), dev)
     code = lib().zf_q4_decode_attn(cache._ref, q.data_ptr(), B, T, Hq, page_table.data_ptr(), max_pages,
@@ -661,8 +678,9 @@ class TokenMap(NamedTuple):
     seq_positions: torch.Tensor
 
 
+@_on_stream
 def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_pos, page_size, max_tokens, out=None,
-               status=None, stream=None) -> TokenMap:
+               status=None) -> TokenMap:
     """zf_map_tokens: places for new_tokens[b] tokens of every request b, on the GPU.  page_table [B][max_pages]
     is extended in place with pages free_pages[free_pos ..]; seq_lens, pages_held, new_tokens [B], free_pages
     [F], free_pos [1], all int32 on the device.  out: a TokenMap to write into (its seq_lens, pages_held and
@@ -695,7 +713,7 @@ def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_po
         out = TokenMap(*(_tensor(t, "out." + name, _I32, dev, s, write=True)
                          for t, name, s in zip(out, TokenMap._fields, shapes)))
     word = None if status is None else _tensor(status, "status", _I32, dev, (1,), write=True).data_ptr()
-    s = _launch_stream(stream, dev)
+    s = _launch_stream(dev)
     code = lib().zf_map_tokens(B, page_size, max_pages, seq_lens.data_ptr(), pages_held.data_ptr(), new_tokens.data_ptr(),
                                page_table.data_ptr(), free_pages.data_ptr(), free_pages.shape[0], free_pos.data_ptr(),
                                out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
@@ -705,8 +723,9 @@ def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_po
     return out
 
 
+@_on_stream
 def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_drafts=None, seq_lens=None,
-                  new_seq_lens=None, status=None, stream=None):
+                  new_seq_lens=None, status=None):
     """zf_verify_drafts: target_probs [B][T+1][V] float32, draft_tokens [B][T] int32, uniform [B][T+1] float32 in
     [0, 1), draft_probs [B][T][V] float32 (None: the drafts were not sampled), n_drafts [B] int32 (None: T
     each).  Returns (accepted [B], tokens [B][T+1]) int32: the accepted drafts, one sampled token, then -1.
@@ -735,7 +754,7 @@ def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_draft
         before, after = seq_lens.data_ptr(), _tensor(new_seq_lens, "new_seq_lens", _I32, dev, (B,), write=True).data_ptr()
     if status is not None:
         word = _tensor(status, "status", _I32, dev, (1,), write=True).data_ptr()
-    s = _launch_stream(stream, dev)
+    s = _launch_stream(dev)
     accepted = torch.empty(B, dtype=torch.int32, device=dev)
     tokens = torch.empty((B, T + 1), dtype=torch.int32, device=dev)
     code = lib().zf_verify_drafts(B, T, V, target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, uniform.data_ptr(),

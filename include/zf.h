@@ -408,7 +408,7 @@ typedef struct zf_q4_cache {
   int32_t num_kv_heads;
   int32_t head_dim;       /* must be 128 */
   int32_t page_size;      /* tokens per page, multiple of 16, <= ZF_MAX_PAGE_SIZE */
-  float k_scale;          /* in [1e-37, 1e37]; 1 suits values up to about 2688 */
+  float k_scale;          /* in [1e-30, 1e30]; 1 suits values up to about 2688 */
   float v_scale;
   uint8_t* records;       /* [num_pages][num_kv_heads][page_size/16][ZF_Q4_RECORD_BYTES] */
   int32_t* status;        /* optional device word; ZF_DEV_* bits are OR-ed in; NULL = not reported */
@@ -478,8 +478,8 @@ zf_status zf_q4_decode_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t
  *   treated as if it had no new tokens, and ZF_DEV_CAPACITY is set.  A request with a negative length or
  *   count, more pages than max_pages_per_req, or more tokens than its pages hold gets no tokens and
  *   sets ZF_DEV_BAD_SEQ_LEN.
- *   status: optional device word.  batch <= ZF_MAX_BATCH; max_pages_per_req * page_size < 2^31.  One
- *   kernel, launched with programmatic stream serialisation.
+ *   status: optional device word.  batch <= ZF_MAX_BATCH; max_pages_per_req * page_size < 2^31;
+ *   max_tokens <= 2^30.  One kernel (two for long lists), launched with programmatic stream serialisation.
  */
 zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max_pages_per_req, const int32_t* seq_lens,
                         const int32_t* pages_held, const int32_t* new_tokens, int32_t* page_table,
@@ -502,14 +502,15 @@ zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max_pages_per_
  *   counts the accepted ones before the first that is not.  With a = accepted[b], one more token is sampled: from
  *   the weights max(p_a - q_a, 0) (float) when a draft was refused (from p_a when they are all 0), from
  *   p_n when none was: the first i whose running sum of weights is above uniform[T] * (their sum),
- *   sums being kept to at least 44 bits; the last i with a positive weight when there is none.
+ *   sums being kept to about 44 bits; the last i with a positive weight when there is none.
  *   Weights that are NaN count as 0.
  *   tokens: [batch][T+1]: the accepted drafts, the sampled token, then -1.
  *   seq_lens, new_seq_lens: optional (both or neither; may be the same array): new_seq_lens[b] =
- *                 seq_lens[b] - (n - a), the length without the refused drafts' places.
- *   A draft token outside [0, vocab) is refused (the sample then excludes nothing) and an n_drafts outside
- *   [0, T] is clamped, both setting ZF_DEV_BAD_DRAFT; a row whose weights have no positive finite sum
- *   gives token -1 and sets ZF_DEV_BAD_PROBS.  status: optional device word.
+ *                 seq_lens[b] - (n - a), the length without the refused drafts' places (the request's
+ *                 last ones).
+ *   A draft token outside [0, vocab) is refused (with draft_probs NULL nothing is then taken off p_a) and
+ *   an n_drafts outside [0, T] is clamped, both setting ZF_DEV_BAD_DRAFT; a row whose weights have no
+ *   positive finite sum gives token -1 and sets ZF_DEV_BAD_PROBS.  status: optional device word.
  *   batch <= ZF_MAX_BATCH, 1 <= T <= ZF_MAX_TOKENS, vocab <= ZF_MAX_VOCAB.  One kernel, launched with
  *   programmatic stream serialisation; results do not depend on how the work is split.
  */

@@ -165,7 +165,7 @@ def check(out, lse, ref, ref_lse, bound, vmax, lse_tol):
     off = np.abs(out - ref).max(-1)
     assert (off <= bound * vmax)[~empty].all(), (off / np.maximum(bound * vmax, 1e-300)).max()
     if (~empty).any():
-        d = np.abs(lse - ref_lse)[~empty]
+        d = np.abs(lse[~empty] - ref_lse[~empty])
         assert (d <= lse_tol[~empty] + 2.0 ** -22 * np.abs(ref_lse[~empty])).all(), d.max()
 
 
@@ -276,3 +276,92 @@ def test_another_stream_and_a_captured_graph(zf):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+
+
+def test_stream_argument_orders_the_whole_call(zf):
+    """stream=: inputs that have to be converted, outputs and workspace live on that stream, behind a slow writer."""
+    lens = [300, 77]
+    c, o, table, sl = build(zf, lens, 2, 16, 15)
+    k, v = tokens(6, 2, 99)
+    ids, pos = [int(table[0, 0])] * 6, list(range(6))
+    q = bits(torch.randn(2, 1, 8, 128, generator=torch.Generator().manual_seed(8)))
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        kd = torch.zeros(6, 128, 2, dtype=torch.int16, device="cuda")
+        torch.cuda._sleep(20_000_000)
+        kd.copy_(k.transpose(1, 2))                       # a strided source, written late on s
+        vd = v.cuda()
+    zf.q4_write_tokens(c, kd.transpose(1, 2), vd, ids, pos, stream=s)
+    kr, vr = zf.q4_read_tokens(c, ids, pos, stream=s)
+    with torch.cuda.stream(s):
+        qd, td, sd = q.cuda(), table.cuda(), sl.cuda()
+    out, lse = zf.q4_decode_attn(c, qd, td, sd, stream=s)
+    s.synchronize()
+    w = S.Q4Cache(c.num_pages, 2, 16)
+    w.records[...] = o.records
+    w.write(H.np_bits(k), H.np_bits(v), ids, pos)
+    assert (c.records.cpu().numpy() == w.records).all()
+    assert (S.bf16_to_f64(H.np_bits(kr[3, 1])) == w.token(ids[3], 1, pos[3])[0]).all()
+    ref, ref_lse, bound = S.attention(w, H.np_bits(q), table.numpy(), lens, 1 / math.sqrt(128))
+    check(out, lse, ref, ref_lse, bound, 6.0, bound)
+
+
+def test_two_calls_at_once(zf):
+    """Calls on two streams with workspaces of their own."""
+    runs = []
+    for seed, lens in ((16, [900, 40]), (17, [33, 700, 5])):
+        c, o, table, sl = build(zf, lens, 2, 16, seed)
+        q = bits(torch.randn(len(lens), 2, 8, 128, generator=torch.Generator().manual_seed(seed)))
+        runs.append((c, q.cuda(), table.cuda(), sl.cuda()))
+    want = [zf.q4_decode_attn(*r) for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in runs]
+    got = []
+    for _ in range(5):
+        got += [(i, zf.q4_decode_attn(*r, stream=s)) for i, (r, s) in enumerate(zip(runs, streams))]
+    torch.cuda.synchronize()
+    for i, (out, lse) in got:
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_cache_beyond_4_gib(zf):
+    """Records whose byte offsets pass 32 bits: written, read back and attended on a cache's last pages."""
+    page, hkv, lens = 128, 8, [200, 130]
+    pages = 31000
+    c = zf.Q4Cache(pages, hkv, page)
+    assert c.stored_bytes() > 1 << 32
+    small = S.Q4Cache(4, hkv, page)
+    at = [pages - 1, 5, pages - 2, pages // 2]               # page i of the small cache
+    ids = [0] * 128 + [1] * 72 + [2] * 128 + [3] * 2
+    pos = list(range(128)) + list(range(72)) + list(range(128)) + [0, 1]
+    k, v = tokens(len(ids), hkv, 18)
+    big = [at[i] for i in ids]
+    zf.q4_write_tokens(c, k.cuda(), v.cuda(), big, pos)
+    small.write(H.np_bits(k), H.np_bits(v), ids, pos)
+    for i, p in enumerate(at):
+        assert (c.records[p].cpu().numpy() == small.records[i]).all()
+    kr, _ = zf.q4_read_tokens(c, big, pos)
+    assert (S.bf16_to_f64(H.np_bits(kr[0, 7])) == small.token(0, 7, 0)[0]).all()
+    q = bits(torch.randn(2, 8, 128, generator=torch.Generator().manual_seed(19)))
+    out, lse = zf.q4_decode_attn(c, q.cuda(), i32([at[:2], at[2:]]).cuda(), i32(lens).cuda())
+    ref, ref_lse, bound = S.attention(small, H.np_bits(q)[:, None], np.array([[0, 1], [2, 3]]), lens, 1 / math.sqrt(128))
+    check(out[:, None], lse[:, None], ref, ref_lse, bound, 6.0, bound)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def test_many_requests_and_an_empty_batch(zf):
+    """4096 requests of zero to three records (ranges that end inside pairs, pairs without records), and none."""
+    rng = np.random.default_rng(20)
+    lens = rng.integers(0, 40, 4096).tolist()
+    c, o, table, sl = build(zf, lens, 1, 16, 21)
+    q = bits(torch.randn(4096, 1, 2, 128, generator=torch.Generator().manual_seed(22)))
+    out, lse = zf.q4_decode_attn(c, q.cuda(), table.cuda(), sl.cuda())
+    pick = rng.permutation(4096)[:300]
+    ref, ref_lse, bound = S.attention(o, H.np_bits(q)[pick], table.numpy()[pick], [lens[i] for i in pick], 1 / math.sqrt(128))
+    check(out[pick.tolist()], lse[pick.tolist()], ref, ref_lse, bound, 6.0, bound)
+    o0, l0 = zf.q4_decode_attn(c, q[:0].cuda(), table.cuda(), sl.cuda())
+    assert o0.shape == (0, 1, 2, 128) and l0.shape == (0, 1, 2)

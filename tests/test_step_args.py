@@ -24,7 +24,7 @@ def _desc(zf, **kw):
 BAD_CACHES = [(dict(head_dim=64), -1), (dict(page_size=8), -1), (dict(page_size=40), -1), (dict(page_size=144), -2),
               (dict(num_kv_heads=0), -1), (dict(num_pages=-1), -1), (dict(records=None), -1), (dict(records=0x1008), -1),
               (dict(k_scale=0.0), -1), (dict(k_scale=-1.0), -1), (dict(v_scale=float("nan")), -1),
-              (dict(v_scale=float("inf")), -1), (dict(k_scale=1e-38), -1), (dict(status=0x1002), -1)]
+              (dict(v_scale=float("inf")), -1), (dict(k_scale=1e-31), -1), (dict(v_scale=1e31), -1), (dict(status=0x1002), -1)]
 
 
 @pytest.mark.parametrize("entry", ["zf_q4_write_tokens", "zf_q4_read_tokens"])
@@ -61,7 +61,7 @@ def test_attention_refuses(zf):
                dict(lens=0x60003), dict(scale=float("nan")), dict(scale=float("inf")), dict(scale=1e38),
                dict(max_pages=1 << 24)):
         assert call(d, **kw) == -1, kw
-    assert call(_desc(zf, k_scale=1e37), scale=10.0) == -1                  # the scores' factor is no float
+    assert call(_desc(zf, k_scale=1e30), scale=1e10) == -1                  # the scores' factor is no float
     assert call(_desc(zf, page_size=128, num_kv_heads=1), batch=4096, hq=1, max_pages=(1 << 16) + 1) == -2    # 2^31 records
     assert call(d, batch=0) == 0
     size = zf.lib().zf_q4_decode_attn_workspace_size
@@ -83,7 +83,7 @@ def test_map_refuses(zf):
             args[names.index(k)] = v
         return f(*args)
     for kw in (dict(batch=-1), dict(batch=4097), dict(page_size=0), dict(page_size=24), dict(max_pages=0),
-               dict(max_pages=1 << 27), dict(num_free=-1), dict(max_tokens=-1), dict(ids=0x4004), dict(positions=0x5008),
+               dict(max_pages=1 << 27), dict(num_free=-1), dict(max_tokens=-1), dict(max_tokens=(1 << 30) + 1), dict(ids=0x4004), dict(positions=0x5008),
                dict(seq=0x6002), dict(status=0x7001), dict(free=0x3002)):
         assert call(**kw) == -1, kw
     for name in ("lens", "held", "new", "table", "free", "pos", "out_lens", "out_held", "out_pos", "start", "ids",
@@ -139,6 +139,8 @@ def test_binding_checks_tokens_and_attention(zf):
              ((q, table, lens), dict(out=torch.zeros(3, 8, 64)), "out: shape"),
              ((q, table, lens), dict(out=torch.zeros(3, 128, 8).transpose(1, 2)), "out must be contiguous"),
              ((q, table, lens), dict(lse=torch.zeros(3, 8, dtype=torch.float64)), "lse: dtype"),
+             ((q, table, lens), dict(workspace=torch.zeros(8, 8).t()), "workspace must be contiguous"),
+             ((q, table, lens), dict(workspace=torch.zeros(8, device="meta")), "workspace is on meta"),
              ((q, table, lens), {}, "a CUDA device")]
     for args, kw, msg in cases:
         with pytest.raises(ValueError, match=msg):
