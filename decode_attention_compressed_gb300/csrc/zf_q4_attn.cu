@@ -46,7 +46,8 @@ namespace {
 constexpr int kUnitTiles = 2;                            // records per stage
 constexpr int kStageQ4 = kUnitTiles * kQ4Record;         // 4608
 constexpr int kQ4QRowBytes = 320;                        // q row in shared memory (see store_q_row)
-constexpr int kFewPartials = 20;
+constexpr int kFewPartials = 20;                         // see range_length
+constexpr float kUnseen = -3e38f;                        // a maximum before any visible score: finite, below them all
 constexpr float kPShift = 7.f;                           // weights are 2^7 times their usual size
 
 // Warps per CTA by the number of 8-column tiles of a pass (kNT), from the registers they need (128, 168
@@ -133,6 +134,16 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   asm("{\n\t.reg .b64 a, b, d;\n\t"
       "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
       "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(r.x), "=f"(r.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   const uint32_t fold_s = ti < 2 ? 0u : 0x80000000u;
 
   float mx[kNT][2], l[kNT][2];                  // running maximum (rounded up) less kPShift, sum; columns 2ti, 2ti+1
-  float cs[kNT][2];                             // score factor (with several tiles read per unit, to spare registers)
+  float cs[kNT][2];                             // kNT = 1: score factor (read per unit otherwise, to spare registers)
   float o[kNT][8][4];
   int len = 0, causal_lim = 0, h0 = 0, nh = 0;
   int slot = 0;                                 // partial of the range the current pair would write
@@ -392,7 +403,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
       for (int n = 0; n < kNT; ++n) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[n][e] = kNoScore;
+          mx[n][e] = kUnseen;
           l[n][e] = 0.f;
           if (kNT == 1) cs[n][e] = qscale[2 * ti + e];
         }
@@ -403,7 +414,8 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
     if (u.have) {
       if (!mbar_wait(&bars[sidx], (phase >> sidx) & 1u)) {
         if (lane == 0) report(a.status, ZF_DEV_TIMEOUT);
-        // the next unit's copies must land before the CTA exits
+        // copies still in flight must land before the CTA exits
+        mbar_wait(&bars[sidx], (phase >> sidx) & 1u);
         if (next.have) mbar_wait(&bars[sidx ^ 1], (phase >> (sidx ^ 1)) & 1u);
         return;
       }
@@ -461,8 +473,23 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         }
       }
 
-      // ---- online softmax, log2 domain.  lane: tokens gi, gi + 8 x columns 2ti, 2ti + 1 (per n)
+      // ---- online softmax, log2 domain.  lane: tokens gi, gi + 8 x columns 2ti, 2ti + 1 (per n).  (Scores are
+      // rounded before the maximum comes off: a fused difference would miss the maximum, one of the
+      // rounded scores, where floats lie further apart than exponents.)
       bool grow = false;
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        const F2 f = kNT == 1 ? F2{cs[n][0], cs[n][1]} : F2{qscale[8 * n + 2 * ti], qscale[8 * n + 2 * ti + 1]};
+#pragma unroll
+        for (int i = 0; i < kUnitTiles; ++i) {
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const F2 y = mul2(F2{x[n][i][r], x[n][i][r + 1]}, f);
+            x[n][i][r] = y.x;
+            x[n][i][r + 1] = y.y;
+          }
+        }
+      }
       if (!full) {
 #pragma unroll
         for (int i = 0; i < kUnitTiles; ++i) {
@@ -480,12 +507,6 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           }
         }
       }
-      if (kNT > 1) {
-#pragma unroll
-        for (int n = 0; n < kNT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) cs[n][e] = qscale[8 * n + 2 * ti + e];
-      }
       float top[kNT][2];
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
@@ -494,8 +515,8 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           top[n][e] = fmaxf(x[n][0][e], x[n][0][e + 2]);
 #pragma unroll
           for (int i = 1; i < kUnitTiles; ++i) top[n][e] = fmaxf(top[n][e], fmaxf(x[n][i][e], x[n][i][e + 2]));
-          top[n][e] *= cs[n][e];
-          grow |= top[n][e] > mx[n][e] + (kRescaleThreshold + kPShift);
+          // (rounded down: the weights fit fp16 however far apart floats lie at the maximum)
+          grow |= top[n][e] > __fadd_rd(mx[n][e], kRescaleThreshold + kPShift);
         }
       }
       if (__any_sync(0xFFFFFFFFu, grow)) {
@@ -507,7 +528,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
             float v = top[n][e];
 #pragma unroll
             for (int dd = 4; dd < 32; dd <<= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, dd));
-            const float mn = fmaxf(mx[n][e], ceilf(v) - kPShift);      // finite: kNoScore at least
+            const float mn = fmaxf(mx[n][e], ceilf(v) - kPShift);      // finite: kUnseen at least
             al[e] = fast_exp2(mx[n][e] - mn);
             mx[n][e] = mn;
             l[n][e] *= al[e];
@@ -531,7 +552,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         for (int i = 0; i < kUnitTiles; ++i) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const F2 z = fma2(F2{x[n][i][2 * r], x[n][i][2 * r + 1]}, F2{cs[n][0], cs[n][1]}, F2{-mx[n][0], -mx[n][1]});
+            const F2 z = add2(F2{x[n][i][2 * r], x[n][i][2 * r + 1]}, F2{-mx[n][0], -mx[n][1]});
             const F2 p = F2{fast_exp2(z.x), fast_exp2(z.y)};
             const F2 sum = add2(F2{l[n][0], l[n][1]}, p);
             l[n][0] = sum.x;
@@ -714,7 +735,7 @@ __global__ void __launch_bounds__(kMergeRows<kPerRow> * kPerRow * 32) q4_merge_k
   // range k's partial of this pair: its first, unless the pair began within range k0
   const int first = S == static_cast<long long>(k0) * W ? 0 : 1;
   auto at = [&](int k) { return (static_cast<size_t>(k) * 2 + (k == k0 ? first : 0)) * a.cols + col; };
-  float M = kNoScore, sum = 0.f;
+  float M = kUnseen, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = k0 + warp; live && k <= k1; k += kPerRow * kMergePre) {
     float2 ml[kMergePre];
@@ -722,7 +743,7 @@ __global__ void __launch_bounds__(kMergeRows<kPerRow> * kPerRow * 32) q4_merge_k
 #pragma unroll
     for (int j = 0; j < kMergePre; ++j) {
       const int kk = k + j * kPerRow;
-      ml[j] = make_float2(kNoScore, 0.f);
+      ml[j] = make_float2(kUnseen, 0.f);
       v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (kk <= k1) {
         ml[j] = a.part_ml[at(kk)];
@@ -774,6 +795,9 @@ __global__ void __launch_bounds__(kMergeRows<kPerRow> * kPerRow * 32) q4_merge_k
 }
 
 // 8-column tiles per pass: 1, 2 or 4 (the kernel reads a kv head's records once per 8, 16 or 32 columns).
+// Wider passes decode each record once for more columns.  Measured at 32 requests of 8192 tokens, 28/4
+// heads: two new tokens (14 columns) 58.0 us in one pass of two tiles, 70.7 in two of one; four (28
+// columns) 98.1 in one pass of four, 100.2 in two of two, 127.3 in four of one.
 int q4_col_tiles(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
 int q4_warps(int nt) { return nt == 1 ? Q4Cfg<1>::kWarps : nt == 2 ? Q4Cfg<2>::kWarps : Q4Cfg<4>::kWarps; }
 

@@ -215,6 +215,27 @@ def test_query_magnitudes(zf):
     check(out[:, :, keep], lse[:, :, keep], ref, ref_lse, bound, 6.0, bound)
 
 
+@pytest.mark.parametrize("power", [20, 40, 90])
+def test_scores_beyond_float_steps_of_one(zf, power):
+    """Scores so large that neighbouring floats lie further apart than any exponent: the largest score takes
+    all the weight, over one unit, several units and several ranges."""
+    for lens in ([31], [700], [5000]):
+        c, o, table, sl = build(zf, lens, 1, 16, 30 + power)
+        q = torch.randn(1, 1, 8, 128, generator=torch.Generator().manual_seed(9)) * 2.0 ** power
+        kv = [o.token(int(table[0, p // 16]), 0, p % 16) for p in range(lens[0])]
+        k, v = np.array([x[0] for x in kv]), np.array([x[1] for x in kv])
+        q = bits(q)
+        out, lse = zf.q4_decode_attn(c, q.cuda(), table.cuda(), sl.cuda(), 1.0)
+        s = k @ S.bf16_to_f64(H.np_bits(q[0, 0])).T
+        order = np.sort(s, 0)
+        clear = order[-1] - order[-2] > 1e-4 * np.abs(s).max(0)           # above any rounding of the scores
+        assert clear.any() and torch.isfinite(out).all() and torch.isfinite(lse).all()
+        got = out[0, 0].cpu().numpy()
+        for g in np.nonzero(clear)[0]:
+            # one weight of 1: the value itself, up to the split's and the division's rounding
+            assert (np.abs(got[g] - v[s[:, g].argmax()]) <= 2.0 ** -21 * np.abs(v).max()).all()
+
+
 def test_nan_row_with_partials(zf):
     """A NaN query row over a context that is split: the merge keeps the NaN, the other rows their values."""
     c, o, table, sl = build(zf, [5000], 1, 16, 8)
