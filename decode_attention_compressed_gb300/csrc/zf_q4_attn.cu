@@ -794,11 +794,18 @@ __global__ void __launch_bounds__(kMergeRows<kPerRow> * kPerRow * 32) q4_merge_k
   if (lane == 0) a.lse[row] = sum == 0.f ? -CUDART_INF_F : (M + log2f(sum)) * kLn2;
 }
 
-// 8-column tiles per pass: 1, 2 or 4 (the kernel reads a kv head's records once per 8, 16 or 32 columns).
-// Wider passes decode each record once for more columns.  Measured at 32 requests of 8192 tokens, 28/4
-// heads: two new tokens (14 columns) 58.0 us in one pass of two tiles, 70.7 in two of one; four (28
-// columns) 98.1 in one pass of four, 100.2 in two of two, 127.3 in four of one.
-int q4_col_tiles(int cols) { return cols <= 8 ? 1 : cols <= 16 ? 2 : 4; }
+// Passes over a kv head's records (slices) and 8-column tiles per pass (1 to 4): as few passes as hold the
+// columns, of equal width.  Wider passes decode each record once for more columns.  Measured at 32 requests
+// of 8192 tokens: 28/4 heads, two new tokens (14 columns) 58.0 us in one pass of two tiles, 70.7 in two of
+// one; three (21) 76.8 in one of three, 96.5 in one of four, 99.3 in two of two; four (28) 97.9 in one of
+// four, 100.0 in two of two, 127.3 in four of one.  32/8 heads, five new tokens (20) 137.1 in one of three,
+// 169.7 in one of four.
+int q4_slices(int cols) { return (cols + 31) / 32; }
+int q4_col_tiles(int cols) {
+  const int tiles = (cols + 7) / 8, slices = q4_slices(cols);
+  return (tiles + slices - 1) / slices;
+}
+static_assert(Q4Cfg<3>::kWarps == Q4Cfg<4>::kWarps);
 int q4_warps(int nt) { return nt == 1 ? Q4Cfg<1>::kWarps : nt == 2 ? Q4Cfg<2>::kWarps : Q4Cfg<4>::kWarps; }
 
 // Grid and workspace: two partials per range, whatever the lengths; the prefix sums of the records.
@@ -811,7 +818,7 @@ Q4Plan q4_plan(int batch, int hq, int hkv, int page_size, int max_pages, int sms
   Q4Plan p;
   const int group = hq / hkv;
   p.nt = q4_col_tiles(group);
-  p.slices = (group + 8 * p.nt - 1) / (8 * p.nt);
+  p.slices = q4_slices(group);
   const long long most = static_cast<long long>(batch) * hkv * p.slices * max_pages * (page_size / 16);
   const long long units = (most + kUnitTiles - 1) / kUnitTiles;
   p.grid = static_cast<int>(units < sms ? (units > 0 ? units : 1) : sms);
@@ -917,6 +924,7 @@ extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, 
   if (a.group <= 4) st = multi ? launch_q4<1, true, true>(a, p.grid, 4, s) : launch_q4<1, false, true>(a, p.grid, 5, s);
   else if (p.nt == 1) st = multi ? launch_q4<1, true>(a, p.grid, 0, s) : launch_q4<1, false>(a, p.grid, 1, s);
   else if (p.nt == 2) st = launch_q4<2, true>(a, p.grid, 2, s);
+  else if (p.nt == 3) st = launch_q4<3, true>(a, p.grid, 6, s);
   else st = launch_q4<4, true>(a, p.grid, 3, s);
   if (st != ZF_OK) return st;
 

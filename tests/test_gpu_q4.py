@@ -129,10 +129,14 @@ CASES = [
     ([97, 3, 0, 130], 1, 8, 2, 16),          # 16 columns
     ([70, 129], 2, 5, 2, 32),                # 10 columns of 16
     ([257, 2], 1, 7, 4, 128),                # 28 columns of 32
-    ([150, 40], 1, 8, 5, 16),                # 40 columns: two passes of 32
+    ([150, 40], 1, 8, 5, 16),                # 40 columns: two passes of 24
     ([65], 1, 3, 8, 16),                     # 24 columns
     ([90], 1, 1, 64, 16),                    # 64 new tokens
     ([900, 1200], 2, 4, 1, 16),              # several partials per request
+    ([900, 0, 1203], 2, 4, 5, 16),           # 20 columns of 24, the same
+    ([131, 18], 1, 11, 3, 16),               # 33 columns: two passes of 24
+    ([100, 9], 1, 9, 9, 48),                 # 81 columns: three passes of 32
+    ([600, 40], 1, 16, 4, 16),               # 64 columns: two passes of 32
 ]
 
 
