@@ -822,7 +822,9 @@ Q4Plan q4_plan(int batch, int hq, int hkv, int page_size, int max_pages, int sms
   const long long most = static_cast<long long>(batch) * hkv * p.slices * max_pages * (page_size / 16);
   const long long units = (most + kUnitTiles - 1) / kUnitTiles;
   p.grid = static_cast<int>(units < sms ? (units > 0 ? units : 1) : sms);
-  const size_t parts = static_cast<size_t>(p.grid) * q4_warps(p.nt) * 2 * 8 * p.nt;
+  // (several passes count as passes of 32, so that more tokens never need a smaller workspace)
+  const int width = p.slices > 1 ? 4 : p.nt;
+  const size_t parts = static_cast<size_t>(p.grid) * q4_warps(p.nt) * 2 * 8 * width;
   p.o_bytes = parts * ZF_HEAD_DIM * 4;
   p.ml_bytes = parts * 8;
   p.prefix_bytes = ((static_cast<size_t>(batch) + 2) * 4 + 255) & ~static_cast<size_t>(255);

@@ -433,7 +433,8 @@ zf_status zf_q4_write_tokens(const zf_q4_cache* cache, const uint16_t* k_tok, co
 zf_status zf_q4_read_tokens(const zf_q4_cache* cache, const int32_t* page_ids, const int32_t* positions,
                             int32_t n, uint16_t* k_out, uint16_t* v_out, void* stream);
 
-/* Workspace bytes zf_q4_decode_attn needs for these sizes on the current device.  0 on invalid sizes. */
+/* Workspace bytes zf_q4_decode_attn needs for these sizes on the current device.  0 on invalid sizes.
+ * A larger batch, tokens or max_pages never needs fewer: the sizes of the largest call serve all. */
 size_t zf_q4_decode_attn_workspace_size(int32_t batch, int32_t tokens, int32_t num_q_heads,
                                         int32_t num_kv_heads, int32_t page_size,
                                         int32_t max_pages_per_req);

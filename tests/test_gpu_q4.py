@@ -189,6 +189,25 @@ def test_attention_matches_the_oracle(zf, lens, hkv, group, T, page):
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+def test_the_largest_calls_workspace_serves_smaller_ones(zf):
+    for hq, hkv in [(32, 8), (28, 4), (11, 1)]:
+        def size(batch, T, pages):
+            return zf.q4_workspace_size(batch, T, hq, hkv, 16, pages)
+        by_tokens = [size(8, T, 64) for T in range(1, 33)]
+        assert by_tokens[0] > 0 and by_tokens == sorted(by_tokens)
+        by_batch = [size(b, 5, 3) for b in range(1, 40)]
+        assert by_batch == sorted(by_batch)
+        by_pages = [size(2, 3, p) for p in range(1, 40)]
+        assert by_pages == sorted(by_pages)
+    c, _, table, sl = build(zf, [40, 75], 1, 16, 3)
+    q = bits(torch.randn(2, 3, 11, 128, generator=torch.Generator().manual_seed(6))).cuda()
+    ws = torch.empty(zf.q4_workspace_size(2, 9, 11, 1, 16, table.shape[1]), dtype=torch.uint8, device="cuda")
+    for T in (1, 2, 3):
+        want = zf.q4_decode_attn(c, q[:, :T].contiguous(), table.cuda(), sl.cuda())
+        got = zf.q4_decode_attn(c, q[:, :T].contiguous(), table.cuda(), sl.cuda(), workspace=ws)
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
 @pytest.mark.parametrize("k_scale,v_scale,scale", [(0.25, 3.0, 0.05), (1.0, 1.0, -0.08), (1.0, 1.0, 0.0)])
 def test_cache_scales_and_softmax_scales(zf, k_scale, v_scale, scale):
     c, o, table, sl = build(zf, [77, 20], 2, 16, 3, k_scale, v_scale)
