@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kMapThreads) map_kernel(const MapArgs a) {
                       static_cast<long long>(L) + n <= cap;
       if (ok) {
         nw[k] = n;
-        ex[k] = max(0, (L + n + P - 1) / P - h);
+        ex[k] = max(0, static_cast<int>((static_cast<uint32_t>(L) + n + P - 1u) / P) - h);    // (L + n may be near 2^31)
         sum_new += nw[k];
         sum_extra += ex[k];
       } else if (rank == 0) {

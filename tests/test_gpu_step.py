@@ -104,6 +104,20 @@ def test_map_bad_requests_get_nothing(zf):
     same_map(*run_map(zf, table, lens, held, new, free, 0, 16, 100), want)
 
 
+def test_map_near_the_largest_length(zf):
+    page = 48
+    max_pages = (2 ** 31 - 1) // page                       # the next page's end is past 2^31
+    table = torch.zeros((1, max_pages), dtype=torch.int32, device="cuda")
+    L = (max_pages - 1) * page
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    m = zf.map_tokens(table, i32([L]).cuda(), i32([max_pages - 1]).cuda(), i32([40]).cuda(), i32([9, 5]).cuda(),
+                      i32([1]).cuda(), page, 42, status=status)
+    assert m.seq_lens.tolist() == [L + 40] and m.pages_held.tolist() == [max_pages] and m.free_pos.tolist() == [2]
+    assert m.page_ids.tolist() == [5] * 40 + [-1] * 2 and m.positions.tolist() == list(range(40)) + [-1] * 2
+    assert m.seq_positions.tolist() == list(range(L, L + 40)) + [-1] * 2
+    assert table[0, -1].item() == 5 and table[0, :-1].abs().sum().item() == 0 and int(status) == 0
+
+
 def test_map_of_nothing(zf):
     same_map(*run_map(zf, np.full((3, 2), 1), [0, 5, 32], [0, 1, 2], [0, 0, 0], [4], 0, 16, 0),
              S.map_tokens([[1, 1]] * 3, [0, 5, 32], [0, 1, 2], [0, 0, 0], [4], 0, 16, 0))
