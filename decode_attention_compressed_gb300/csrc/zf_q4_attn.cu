@@ -76,8 +76,16 @@ struct Q4AttnArgs {
   float v_factor;
 };
 
+// What a warp keeps of the query columns of its current pair.
+template <int kNT>
+struct Q4Columns {
+  float scale[8 * kNT];          // score factor
+  int at[8 * kNT];               // row within the request's query rows
+  int token[8 * kNT];            // new token
+};
+
 struct Q4Smem {
-  size_t stages, qbuf, qscale, bars, prefix, total;
+  size_t stages, qbuf, cols, bars, prefix, total;
 };
 
 template <int kNT>
@@ -87,7 +95,7 @@ __host__ __device__ inline Q4Smem q4_smem(int batch) {
   size_t at = 0;
   s.stages = at; at += static_cast<size_t>(C::kWarps) * kWarpStages * kStageQ4;
   s.qbuf = at; at += static_cast<size_t>(C::kWarps) * C::kCols * kQ4QRowBytes;
-  s.qscale = at; at += static_cast<size_t>(C::kWarps) * C::kCols * 4;
+  s.cols = at; at += C::kWarps * sizeof(Q4Columns<kNT>);
   s.bars = at; at += static_cast<size_t>(C::kWarps) * kWarpStages * 8;
   s.prefix = at; at += static_cast<size_t>(batch + 1) * 4;
   s.total = (at + 127) & ~static_cast<size_t>(127);
@@ -166,46 +174,83 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// One q row of 128 BF16 values (lane holds words lane and lane + 32) into shared memory as fp16 times
-// a power of two that brings its largest exponent to 11; returns the inverse factor.  Channel c =
-// 32 t + 8 j + e goes to byte 64 j + 16 t + 2 e: lane t's words of k-steps 2j, 2j+1 are 16 bytes,
-// and the rows' stride spreads a warp's reads over the banks.
-__device__ __forceinline__ float store_q_row(uint8_t* row, int lane, uint32_t w0, uint32_t w1, bool negate) {
-  const uint32_t m0 = w0 & 0x7FFF7FFFu, m1 = w1 & 0x7FFF7FFFu;
-  const uint32_t big = max(max(m0 & 0xFFFFu, m0 >> 16), max(m1 & 0xFFFFu, m1 >> 16));
-  const int e = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, big) >> 7);        // biased exponent
-  const int k = min(138 - e, 126);
-  const float f = __int_as_float(((127 + k) << 23) | (negate ? 0x80000000 : 0));
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t w = h ? w1 : w0;
-    const int c = 2 * (lane + 32 * h);
-    const int t = c >> 5, j = (c >> 3) & 3, r = c & 7;
-    *reinterpret_cast<uint32_t*>(row + 64 * j + 16 * t + 2 * r) = pack_f16x2(bf16lo_to_f32(w) * f, bf16hi_to_f32(w) * f);
-  }
-  return __int_as_float((127 - k) << 23);
-}
-
-// The query rows of a pair (query heads h0 .. h0 + nh - 1 of request b), by one warp; rows past nh are zero.
+// The query rows of a pair (query heads h0 .. h0 + nh - 1 of request b), by one warp, into shared memory as fp16:
+// each row times a power of two that brings its largest exponent to 11; its factor takes that back.  Rows
+// past nh are zero.  Channel c = 32 t + 8 j + e goes to byte 64 j + 16 t + 2 e: lane t's words of k-steps
+// 2j, 2j+1 are 16 bytes, and the rows' stride spreads a warp's reads over the banks.  A warp takes four rows one
+// by one (one maximum over the lanes each), more two by two.  (Rows one by one, and a division per
+// column here, for the mask and for the result: 64 requests of 512 tokens, 32 columns 61.2 us instead of
+// 51.4; four rows two by two: the long-context workload 110.8 instead of 109.7.)
 template <int kNT, bool kFold>
-__device__ __forceinline__ void stage_q(const Q4AttnArgs& a, int b, int h0, int nh, uint8_t* qb, float* qs, int lane) {
-  constexpr int kCols = Q4Cfg<kNT>::kCols;
+__device__ __forceinline__ void stage_q(const Q4AttnArgs& a, int b, int h0, int nh, uint8_t* qb, Q4Columns<kNT>& cols,
+                                        int lane) {
+  static_assert(!kFold || kNT == 1, "four columns");
+  constexpr int kRows = kFold ? 4 : 8 * kNT;
+  int rel = 0;
+  if (lane < 8 * kNT) {
+    const int qh = h0 + min(kFold ? lane & 3 : lane, nh - 1);
+    const int h = a.tokens == 1 ? qh : qh / a.tokens, tok = qh - h * a.tokens;
+    rel = tok * (a.tokens == 1 ? a.hq : a.hq / a.tokens) + h;
+    cols.at[lane] = rel;
+    cols.token[lane] = tok;
+  }
+  const bool negate = a.scale_log2 < 0.f;
+  // a row's factor from the largest magnitude among its values (their bits)
+  auto factor = [&](uint32_t big, float& s) {
+    const int k = min(138 - static_cast<int>(big >> 7), 126);           // (big >> 7: biased exponent)
+    // positive, so that the largest raw score has the largest score, and -inf stays one
+    s = fmaxf(__int_as_float((127 - k) << 23) * fabsf(a.scale_log2), 1e-37f);
+    return __int_as_float(((127 + k) << 23) | (negate ? 0x80000000 : 0));
+  };
+  if constexpr (kFold) {
+    const uint32_t* base = reinterpret_cast<const uint32_t*>(a.q + static_cast<size_t>(b) * a.hq * ZF_HEAD_DIM) + lane;
+    uint32_t v[kRows][2];
 #pragma unroll
-  for (int r0 = 0; r0 < kCols; r0 += 8) {
-    uint32_t v[8][2];
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t* src = base + static_cast<size_t>(__shfl_sync(0xFFFFFFFFu, rel, r)) * (ZF_HEAD_DIM / 2);
+      v[r][0] = r < nh ? __ldg(src) : 0u;                    // (read-only: every row's loads may go first)
+      v[r][1] = r < nh ? __ldg(src + 32) : 0u;
+    }
+    uint8_t* dst = qb + 64 * ((lane >> 2) & 3) + 16 * (lane >> 4) + 4 * (lane & 3);        // channel 2 lane; 2 lane + 64 is 32 on
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int c = kFold ? r & 3 : r0 + r;
-      const int qh = h0 + min(c, nh - 1);
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + query_row(b, qh, a.tokens, a.hq) * ZF_HEAD_DIM);
-      v[r][0] = c < nh ? __ldg(src + lane) : 0u;            // (read-only: every row's loads may go first)
-      v[r][1] = c < nh ? __ldg(src + lane + 32) : 0u;
+    for (int r = 0; r < kRows; ++r) {
+      const uint32_t m2 = __vmaxu2(v[r][0] & 0x7FFF7FFFu, v[r][1] & 0x7FFF7FFFu);
+      float s;
+      const float f = factor(__reduce_max_sync(0xFFFFFFFFu, max(m2 & 0xFFFFu, m2 >> 16)), s);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {                          // (columns 4 to 7 repeat 0 to 3)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          *reinterpret_cast<uint32_t*>(dst + (r + 4 * c) * kQ4QRowBytes + 32 * h) =
+              pack_f16x2(bf16lo_to_f32(v[r][h]) * f, bf16hi_to_f32(v[r][h]) * f);
+        if (lane == 0) cols.scale[r + 4 * c] = s;
+      }
+    }
+  } else {
+    const int m = lane & 15;                                   // channels 8m .. 8m + 7
+    const uint4* base = reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(b) * a.hq * ZF_HEAD_DIM) + m;
+    uint8_t* dst = qb + 64 * (m & 3) + 16 * (m >> 2);
+    uint4 v[kRows / 2];
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const size_t row = static_cast<size_t>(__shfl_sync(0xFFFFFFFFu, rel, r)) * (ZF_HEAD_DIM / 8);
+      v[i] = r < nh ? __ldg(base + row) : make_uint4(0u, 0u, 0u, 0u);          // (read-only: every row's loads may go first)
     }
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float inv = store_q_row(qb + (r0 + r) * kQ4QRowBytes, lane, v[r][0], v[r][1], a.scale_log2 < 0.f);
-      // positive, so that the largest raw score has the largest score, and -inf stays one
-      if (lane == 0) qs[r0 + r] = fmaxf(inv * fabsf(a.scale_log2), 1e-37f);
+    for (int i = 0; i < kRows / 2; ++i) {
+      const int r = 2 * i + (lane >> 4);
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t big = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) big = __vmaxu2(big, __shfl_xor_sync(0xFFFFFFFFu, big, d));
+      float s;
+      const float f = factor(max(big & 0xFFFFu, big >> 16), s);
+      uint32_t y[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[x] = pack_f16x2(bf16lo_to_f32(w[x]) * f, bf16hi_to_f32(w[x]) * f);
+      *reinterpret_cast<uint4*>(dst + r * kQ4QRowBytes) = make_uint4(y[0], y[1], y[2], y[3]);
+      if (m == 0) cols.scale[r] = s;
     }
   }
 }
@@ -304,7 +349,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L.bars) + warp * kWarpStages;       // this warp's
   uint8_t* stages = smem + L.stages + static_cast<size_t>(warp) * kWarpStages * kStageQ4;
   uint8_t* qbuf = smem + L.qbuf + static_cast<size_t>(warp) * C::kCols * kQ4QRowBytes;
-  float* qscale = reinterpret_cast<float*>(smem + L.qscale) + warp * C::kCols;
+  Q4Columns<kNT>& cols = reinterpret_cast<Q4Columns<kNT>*>(smem + L.cols)[warp];
   if (lane < kWarpStages) mbar_init(&bars[lane], 1);
   fence_mbar_init();
   wait_prior_grid();          // inputs may come from the preceding grid
@@ -376,7 +421,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   float mx[kNT][2], l[kNT][2];                  // running maximum (rounded up) less kPShift, sum; columns 2ti, 2ti+1
   float cs[kNT][2];                             // kNT = 1: score factor (read per unit otherwise, to spare registers)
   float o[kNT][8][4];
-  int len = 0, causal_lim = 0, h0 = 0, nh = 0;
+  int len = 0, causal_lim = 0, nh = 0;
   int slot = 0;                                 // partial of the range the current pair would write
   bool whole = false;                           // the current pair began with its first record
   int cb = 0;                                   // its request
@@ -394,9 +439,9 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
       len = min(max(a.seq_lens[u.b], 0), max_len);
       const int g = a.slices == 1 ? u.r : u.r / a.slices;
       const int s = u.r - g * a.slices;
-      h0 = g * a.group + s * C::kCols;
+      const int h0 = g * a.group + s * C::kCols;
       nh = min(C::kCols, a.group - s * C::kCols);
-      stage_q<kNT, kFold>(a, u.b, h0, nh, qbuf, qscale, lane);
+      stage_q<kNT, kFold>(a, u.b, h0, nh, qbuf, cols, lane);
       __syncwarp();
       causal_lim = kMulti ? len - a.tokens : 0;
 #pragma unroll
@@ -405,7 +450,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         for (int e = 0; e < 2; ++e) {
           mx[n][e] = kUnseen;
           l[n][e] = 0.f;
-          if (kNT == 1) cs[n][e] = qscale[2 * ti + e];
+          if (kNT == 1) cs[n][e] = cols.scale[2 * ti + e];
         }
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) o[n][mt][0] = o[n][mt][1] = o[n][mt][2] = o[n][mt][3] = 0.f;
@@ -479,7 +524,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
       bool grow = false;
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        const F2 f = kNT == 1 ? F2{cs[n][0], cs[n][1]} : F2{qscale[8 * n + 2 * ti], qscale[8 * n + 2 * ti + 1]};
+        const F2 f = kNT == 1 ? F2{cs[n][0], cs[n][1]} : F2{cols.scale[8 * n + 2 * ti], cols.scale[8 * n + 2 * ti + 1]};
 #pragma unroll
         for (int i = 0; i < kUnitTiles; ++i) {
 #pragma unroll
@@ -499,8 +544,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               // (kMulti) the last position that column sees
-              const int last =
-                  kMulti ? causal_lim + (h0 + (kFold ? (2 * ti + e) & 3 : 8 * n + 2 * ti + e)) % a.tokens : INT_MAX;
+              const int last = kMulti ? causal_lim + cols.token[8 * n + 2 * ti + e] : INT_MAX;
               if (gi >= ntok[i] || pos > last) x[n][i][e] = -CUDART_INF_F;
               if (gi + 8 >= ntok[i] || pos + 8 > last) x[n][i][e + 2] = -CUDART_INF_F;
             }
@@ -643,7 +687,7 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
           float* dst;
           float f = 1.f;
           if (done) {
-            const size_t row = query_row(cb, h0 + col, a.tokens, a.hq);
+            const size_t row = static_cast<size_t>(cb) * a.hq + cols.at[col];
             dst = a.out + row * ZF_HEAD_DIM;
             f = s == 0.f ? 0.f : a.v_factor / s;           // a sum of 0: nothing was seen; a NaN sum stays a NaN
             if (gi == 0) a.lse[row] = s == 0.f ? -CUDART_INF_F : (m + log2f(s)) * kLn2;
@@ -796,10 +840,10 @@ __global__ void __launch_bounds__(kMergeRows<kPerRow> * kPerRow * 32) q4_merge_k
 
 // Passes over a kv head's records (slices) and 8-column tiles per pass (1 to 4): as few passes as hold the
 // columns, of equal width.  Wider passes decode each record once for more columns.  Measured at 32 requests
-// of 8192 tokens: 28/4 heads, two new tokens (14 columns) 58.0 us in one pass of two tiles, 70.7 in two of
-// one; three (21) 76.8 in one of three, 96.5 in one of four, 99.3 in two of two; four (28) 97.9 in one of
-// four, 100.0 in two of two, 127.3 in four of one.  32/8 heads, five new tokens (20) 137.1 in one of three,
-// 169.7 in one of four.
+// of 8192 tokens: 28/4 heads, two new tokens (14 columns) 57.2 us in one pass of two tiles, 71.1 in two of
+// one; three (21) 77.8 in one of three, 93.8 in one of four, 96.9 in two of two; four (28) 94.8 in one of
+// four, 97.9 in two of two, 127.9 in four of one.  32/8 heads, five new tokens (20) 139.8 in one of three,
+// 171.5 in one of four.
 int q4_slices(int cols) { return (cols + 31) / 32; }
 int q4_col_tiles(int cols) {
   const int tiles = (cols + 7) / 8, slices = q4_slices(cols);
