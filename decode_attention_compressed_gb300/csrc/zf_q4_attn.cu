@@ -29,6 +29,14 @@
 //    of two tokens are interleaved by nibble, so that one conversion gives a register of the
 //    operand (two tokens, one channel).
 //  * e2m1 pairs become half pairs in one conversion, and one multiplication applies the scale.
+//
+// Bound.  Up to 8 columns: issue slots and half-rate operations beside the copies (331 and 356 instructions per
+// record; 106 and 127 cycles per record and SM, the copies alone 101).  Wider: the matrix instructions, each of
+// which holds its scheduler for 9.4 cycles and overlaps other work only in part (28 columns: 96 per
+// record, 226 of 430 cycles).  The 5th-generation tensor cores do not pay here: with K in tensor memory, V^T
+// in shared memory and a product per 128 tokens the softmax's chain of dependent steps sets the pace,
+// 2700 to 3100 cycles per 128 tokens for 16 to 32 columns alike (28 columns, 32 requests of 8192 tokens 87 us
+// against 95 here, of 2048 tokens and 64 requests 125 against 105, of 128 tokens 41 against 27).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -51,7 +59,7 @@ constexpr float kUnseen = -3e38f;                        // a maximum before any
 constexpr float kPShift = 7.f;                           // weights are 2^7 times their usual size
 
 // Warps per CTA by the number of 8-column tiles of a pass (kNT), from the registers they need (128, 168
-// and 255 per thread).
+// and, for three and four tiles, 255 per thread).
 template <int kNT>
 struct Q4Cfg {
   static constexpr int kWarps = kNT == 1 ? 16 : kNT == 2 ? 12 : 8;
