@@ -442,11 +442,8 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
     // With up to 4 columns, where the copies set the pace, a pair's query rows are staged before the next unit's
     // copies start, so that the range's first unit arrives sooner (ragged workload 68.7 -> 67.2 us, long
     // context 109.4 -> 107.6); with more the copies go first (five to eight columns 127.0 against 127.4).
-    auto fetch = [&]() {
-      if (more)
-        next = next_unit(a, prefix, HS, tpp, f, stages + (sidx ^ 1) * kStageQ4, &bars[sidx ^ 1], lane, policy);
-    };
-    if (!kFold) fetch();
+    if (!kFold && more)
+      next = next_unit(a, prefix, HS, tpp, f, stages + (sidx ^ 1) * kStageQ4, &bars[sidx ^ 1], lane, policy);
     if (u.start) {
       whole = u.tile == 0;
       cb = u.b;
@@ -470,7 +467,8 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
         for (int mt = 0; mt < 8; ++mt) o[n][mt][0] = o[n][mt][1] = o[n][mt][2] = o[n][mt][3] = 0.f;
       }
     }
-    if (kFold) fetch();
+    if (kFold && more)
+      next = next_unit(a, prefix, HS, tpp, f, stages + (sidx ^ 1) * kStageQ4, &bars[sidx ^ 1], lane, policy);
     if (u.have) {
       if (!mbar_wait(&bars[sidx], (phase >> sidx) & 1u)) {
         if (lane == 0) report(a.status, ZF_DEV_TIMEOUT);
