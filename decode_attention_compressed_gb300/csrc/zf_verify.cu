@@ -372,7 +372,11 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
           t < acc ? a.tokens_in[static_cast<size_t>(b) * T + t] : t == acc ? token : -1;
     if (lane == 0) {
       a.accepted[b] = acc;
-      if (a.out_lens) a.out_lens[b] = a.seq_lens[b] - (n - acc);
+      if (a.out_lens) {
+        const int len = a.seq_lens[b] - (n - acc);
+        if (len < 0) report(a.status, ZF_DEV_BAD_SEQ_LEN);
+        a.out_lens[b] = max(len, 0);
+      }
     }
   }
   // no CTA reads another's shared memory after the last barrier (the sums were pushed), so none has to wait

@@ -74,7 +74,8 @@ typedef int32_t zf_status;
 #define ZF_DEV_BAD_PAGE_ID 0x1         /* page id outside [0, num_pages) */
 #define ZF_DEV_BAD_RAW_SLOT 0x2        /* a page head needed raw storage and its raw slot was missing or out of range */
 #define ZF_DEV_BAD_N_VALID 0x4         /* n_valid outside [0, page_size] */
-#define ZF_DEV_BAD_SEQ_LEN 0x8         /* seq_len outside [0, max_pages_per_req * page_size] */
+#define ZF_DEV_BAD_SEQ_LEN 0x8         /* seq_len outside [0, max_pages_per_req * page_size]; zf_verify_drafts: one that
+                                          falls below 0 */
 #define ZF_DEV_BAD_DIR 0x10            /* directory entry neither compressed nor a valid raw slot */
 #define ZF_DEV_TIMEOUT 0x20            /* a shared-memory pipeline wait gave up */
 #define ZF_DEV_BAD_SLOT 0x40           /* zf_validate_pages: a compressed slot's metadata is malformed */
@@ -508,7 +509,7 @@ zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max_pages_per_
  *   tokens: [batch][T+1]: the accepted drafts, the sampled token, then -1.
  *   seq_lens, new_seq_lens: optional (both or neither; may be the same array): new_seq_lens[b] =
  *                 seq_lens[b] - (n - a), the length without the refused drafts' places (the request's
- *                 last ones).
+ *                 last ones).  One that falls below 0 becomes 0 and sets ZF_DEV_BAD_SEQ_LEN.
  *   A draft token outside [0, vocab) is refused (with draft_probs NULL nothing is then taken off p_a) and
  *   an n_drafts outside [0, T] is clamped, both setting ZF_DEV_BAD_DRAFT; a row whose weights have no
  *   positive finite sum gives token -1 and sets ZF_DEV_BAD_PROBS.  status: optional device word.
