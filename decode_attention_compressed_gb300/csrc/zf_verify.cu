@@ -41,6 +41,7 @@ struct VerifyArgs {
   const int32_t* tokens_in;
   const int32_t* n_drafts;
   const float* uniform;
+  const int32_t* token_start;    // or null: every request was given its places
   int32_t* accepted;
   int32_t* tokens;
   const int32_t* seq_lens;
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
   __shared__ int sh_piece, sh_zero;
   __shared__ DF sh_x, sh_before;
   __shared__ int sh_acc, sh_n;
+  __shared__ bool sh_idle;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank, ranks;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -283,6 +285,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
       v[k] = t < T ? a.uniform[static_cast<size_t>(b) * (T + 1) + t] : 0.f;
     }
     int n = a.n_drafts ? a.n_drafts[b] : T;
+    // places that zf_map_tokens gave the request; a count that is no step's is refused like none
+    const int places = a.token_start ? a.token_start[b + 1] - a.token_start[b] : T + 1;
+    if (places < 1 || places > T + 1) {
+      if (places != 0 && rank == 0 && lane == 0) report(a.status, ZF_DEV_BAD_DRAFT);
+      n = 0;
+    }
     if (n < 0 || n > T) {
       if (rank == 0 && lane == 0) report(a.status, ZF_DEV_BAD_DRAFT);
       n = min(max(n, 0), T);
@@ -310,9 +318,20 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     if (lane == 0) {
       sh_acc = acc;
       sh_n = n;
+      sh_idle = places < 1 || places > T + 1;
     }
   }
   __syncthreads();
+  if (sh_idle) {              // the whole cluster: no tokens, and the length stays
+    if (rank == 0 && warp == 0) {
+      for (int t = lane; t <= T; t += 32) a.tokens[static_cast<size_t>(b) * (T + 1) + t] = -1;
+      if (lane == 0) {
+        a.accepted[b] = 0;
+        if (a.out_lens) a.out_lens[b] = a.seq_lens[b];
+      }
+    }
+    return;
+  }
   const int acc = sh_acc, n = sh_n;
   Row row;
   row.p = a.target + (static_cast<size_t>(b) * (T + 1) + acc) * V;
@@ -405,18 +424,18 @@ zf_status launch_verify(const VerifyArgs& a, int ctas, cudaStream_t stream) {
 
 using namespace zf;
 
-extern "C" zf_status zf_verify_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, const float* target_probs,
-                                      const float* draft_probs, const int32_t* draft_tokens, const int32_t* n_drafts,
-                                      const float* uniform, int32_t* accepted, int32_t* tokens,
-                                      const int32_t* seq_lens, int32_t* new_seq_lens, int32_t* status, void* stream) {
+static zf_status verify(int32_t batch, int32_t max_drafts, int32_t vocab, const float* target_probs,
+                        const float* draft_probs, const int32_t* draft_tokens, const int32_t* n_drafts,
+                        const float* uniform, const int32_t* token_start, int32_t* accepted, int32_t* tokens,
+                        const int32_t* seq_lens, int32_t* new_seq_lens, int32_t* status, void* stream) {
   if (batch < 0 || batch > ZF_MAX_BATCH || max_drafts < 1 || max_drafts > ZF_MAX_TOKENS || vocab < 1 ||
       vocab > ZF_MAX_VOCAB)
     return ZF_ERR_INVALID_ARGUMENT;
   if ((seq_lens == nullptr) != (new_seq_lens == nullptr)) return ZF_ERR_INVALID_ARGUMENT;
   if (batch == 0) return ZF_OK;
   if (!target_probs || !draft_tokens || !uniform || !accepted || !tokens) return ZF_ERR_INVALID_ARGUMENT;
-  const void* all[] = {target_probs, draft_probs, draft_tokens, n_drafts, uniform, accepted, tokens, seq_lens,
-                       new_seq_lens, status};
+  const void* all[] = {target_probs, draft_probs, draft_tokens, n_drafts, uniform, token_start, accepted, tokens,
+                       seq_lens, new_seq_lens, status};
   for (const void* p : all)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return ZF_ERR_INVALID_ARGUMENT;
   VerifyArgs a{};
@@ -425,6 +444,7 @@ extern "C" zf_status zf_verify_drafts(int32_t batch, int32_t max_drafts, int32_t
   a.tokens_in = draft_tokens;
   a.n_drafts = n_drafts;
   a.uniform = uniform;
+  a.token_start = token_start;
   a.accepted = accepted;
   a.tokens = tokens;
   a.seq_lens = seq_lens;
@@ -453,4 +473,22 @@ extern "C" zf_status zf_verify_drafts(int32_t batch, int32_t max_drafts, int32_t
   const bool vec = vocab % 4 == 0 && aligned16(target_probs) && aligned16(draft_probs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return vec ? launch_verify<true>(a, ctas, s) : launch_verify<false>(a, ctas, s);
+}
+
+extern "C" zf_status zf_verify_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, const float* target_probs,
+                                      const float* draft_probs, const int32_t* draft_tokens, const int32_t* n_drafts,
+                                      const float* uniform, int32_t* accepted, int32_t* tokens,
+                                      const int32_t* seq_lens, int32_t* new_seq_lens, int32_t* status, void* stream) {
+  return verify(batch, max_drafts, vocab, target_probs, draft_probs, draft_tokens, n_drafts, uniform, nullptr, accepted,
+                tokens, seq_lens, new_seq_lens, status, stream);
+}
+
+extern "C" zf_status zf_verify_mapped_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, const float* target_probs,
+                                             const float* draft_probs, const int32_t* draft_tokens,
+                                             const int32_t* n_drafts, const float* uniform, const int32_t* token_start,
+                                             int32_t* accepted, int32_t* tokens, const int32_t* seq_lens,
+                                             int32_t* new_seq_lens, int32_t* status, void* stream) {
+  if (batch > 0 && !token_start) return ZF_ERR_INVALID_ARGUMENT;
+  return verify(batch, max_drafts, vocab, target_probs, draft_probs, draft_tokens, n_drafts, uniform, token_start, accepted,
+                tokens, seq_lens, new_seq_lens, status, stream);
 }

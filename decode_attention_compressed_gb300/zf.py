@@ -105,6 +105,9 @@ SIGNATURES = {
                                  _c_void_p, _c_int32, _c_void_p, _c_void_p]),
     "zf_verify_drafts": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                     _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "zf_verify_mapped_drafts": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                           _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                           _c_void_p]),
     "zf_kv_create": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_int32, _c_int32, _c_int32, ctypes.POINTER(_c_void_p)]),
     "zf_kv_destroy": (None, [_c_void_p]),
     "zf_kv_admit": (_c_int32, [_c_void_p, _c_int32, _c_int32, _P32, _P32, _P32, _P32]),
@@ -725,12 +728,13 @@ def map_tokens(page_table, seq_lens, pages_held, new_tokens, free_pages, free_po
 
 @_on_stream
 def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_drafts=None, seq_lens=None,
-                  new_seq_lens=None, status=None):
+                  new_seq_lens=None, status=None, token_start=None):
     """zf_verify_drafts: target_probs [B][T+1][V] float32, draft_tokens [B][T] int32, uniform [B][T+1] float32 in
     [0, 1), draft_probs [B][T][V] float32 (None: the drafts were not sampled), n_drafts [B] int32 (None: T
     each).  Returns (accepted [B], tokens [B][T+1]) int32: the accepted drafts, one sampled token, then -1.
     With seq_lens (and new_seq_lens, which may be the same tensor) the lengths are shortened by the
-    refused drafts."""
+    refused drafts.  token_start [B+1] int32: what map_tokens gave in this step (zf_verify_mapped_drafts); a
+    request that got no places there keeps its length and gets accepted 0 and tokens -1."""
     if not isinstance(draft_tokens, torch.Tensor) or draft_tokens.dim() != 2:
         raise ValueError("draft_tokens must be a [batch][drafts] tensor")
     B, T = draft_tokens.shape
@@ -754,13 +758,20 @@ def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_draft
         before, after = seq_lens.data_ptr(), _tensor(new_seq_lens, "new_seq_lens", _I32, dev, (B,), write=True).data_ptr()
     if status is not None:
         word = _tensor(status, "status", _I32, dev, (1,), write=True).data_ptr()
+    if token_start is not None:
+        token_start = _tensor(token_start, "token_start", _I32, dev, (B + 1,))
     s = _launch_stream(dev)
     accepted = torch.empty(B, dtype=torch.int32, device=dev)
     tokens = torch.empty((B, T + 1), dtype=torch.int32, device=dev)
-    code = lib().zf_verify_drafts(B, T, V, target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, uniform.data_ptr(),
-                                  accepted.data_ptr(), tokens.data_ptr(), before, after, word, s)
+    if token_start is None:
+        code = lib().zf_verify_drafts(B, T, V, target_probs.data_ptr(), q, draft_tokens.data_ptr(), n, uniform.data_ptr(),
+                                      accepted.data_ptr(), tokens.data_ptr(), before, after, word, s)
+    else:
+        code = lib().zf_verify_mapped_drafts(B, T, V, target_probs.data_ptr(), q, draft_tokens.data_ptr(), n,
+                                             uniform.data_ptr(), token_start.data_ptr(), accepted.data_ptr(),
+                                             tokens.data_ptr(), before, after, word, s)
     if code:
-        _check("zf_verify_drafts", code)
+        _check("zf_verify_drafts" if token_start is None else "zf_verify_mapped_drafts", code)
     return accepted, tokens
 
 

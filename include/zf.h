@@ -477,7 +477,9 @@ zf_status zf_q4_decode_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t
  *   zf_q4_write_tokens takes), seq_positions [max_tokens]: position in the request.  Entries from
  *   token_start[batch] on are set to -1.
  *   When the pages or the max_tokens entries do not suffice, nothing is mapped: every request is
- *   treated as if it had no new tokens, and ZF_DEV_CAPACITY is set.  A request with a negative length or
+ *   treated as if it had no new tokens, and ZF_DEV_CAPACITY is set.  The step's other calls then run
+ *   on requests whose tokens have no places: zf_q4_write_tokens skips every entry, attention's rows
+ *   mean nothing, and zf_verify_mapped_drafts, given token_start, leaves tokens and lengths alone.  A request with a negative length or
  *   count, more pages than max_pages_per_req, or more tokens than its pages hold gets no tokens and
  *   sets ZF_DEV_BAD_SEQ_LEN.
  *   status: optional device word.  batch <= ZF_MAX_BATCH; max_pages_per_req * page_size < 2^31;
@@ -509,7 +511,9 @@ zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max_pages_per_
  *   tokens: [batch][T+1]: the accepted drafts, the sampled token, then -1.
  *   seq_lens, new_seq_lens: optional (both or neither; may be the same array): new_seq_lens[b] =
  *                 seq_lens[b] - (n - a), the length without the refused drafts' places (the request's
- *                 last ones).  One that falls below 0 becomes 0 and sets ZF_DEV_BAD_SEQ_LEN.
+ *                 last ones).  One that falls below 0 becomes 0 and sets ZF_DEV_BAD_SEQ_LEN.  (This call
+ *                 trusts that the drafts have their places: after zf_map_tokens, which may refuse them,
+ *                 use zf_verify_mapped_drafts.)
  *   A draft token outside [0, vocab) is refused (with draft_probs NULL nothing is then taken off p_a) and
  *   an n_drafts outside [0, T] is clamped, both setting ZF_DEV_BAD_DRAFT; a row whose weights have no
  *   positive finite sum gives token -1 and sets ZF_DEV_BAD_PROBS.  status: optional device word.
@@ -520,6 +524,22 @@ zf_status zf_verify_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, con
                            const float* draft_probs, const int32_t* draft_tokens, const int32_t* n_drafts,
                            const float* uniform, int32_t* accepted, int32_t* tokens, const int32_t* seq_lens,
                            int32_t* new_seq_lens, int32_t* status, void* stream);
+
+/*
+ * zf_verify_mapped_drafts — zf_verify_drafts in the step whose places zf_map_tokens handed out.
+ *   token_start:  [batch+1] as zf_map_tokens wrote it in this step; the difference of two entries is the
+ *                 number of places the request was given.  A request that was given none (the call or the
+ *                 request was refused, or it had no new tokens) has nothing to verify: accepted 0, every
+ *                 token -1, its length unchanged (run its step again once pages are free).  So does, with
+ *                 ZF_DEV_BAD_DRAFT, one that was given more than the T + 1 places of its last token and
+ *                 T drafts.
+ *   Other arguments and results as for zf_verify_drafts.
+ */
+zf_status zf_verify_mapped_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, const float* target_probs,
+                                  const float* draft_probs, const int32_t* draft_tokens, const int32_t* n_drafts,
+                                  const float* uniform, const int32_t* token_start, int32_t* accepted,
+                                  int32_t* tokens, const int32_t* seq_lens, int32_t* new_seq_lens, int32_t* status,
+                                  void* stream);
 
 /* ------------------------------------------------------------------------------------------
  * zf_kv — host-side page manager for the caches above.  ZipFusion §III.D (KV Cache Management and

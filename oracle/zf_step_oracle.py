@@ -231,3 +231,29 @@ def verify(target, draft, drafts, n_drafts, uniform):
         tokens.append([int(x) for x in drafts[b, :a]] + [token] + [-1] * (T - a))
         gaps.append(gap)
     return accepted, tokens, gaps, status
+
+
+def verify_step(target, draft, drafts, n_drafts, uniform, starts, lens):
+    """verify after map_tokens in one step: starts are its list starts, lens the lengths it gave.
+    (accepted, tokens, lens, gaps, status); a request without places keeps its length."""
+    B, T = drafts.shape
+    accepted, tokens, after, gaps, status = [], [], [], [], 0
+    for b in range(B):
+        places = int(starts[b + 1]) - int(starts[b])
+        if not 1 <= places <= T + 1:
+            status |= DEV_BAD_DRAFT if places else 0
+            accepted.append(0)
+            tokens.append([-1] * (T + 1))
+            after.append(int(lens[b]))
+            gaps.append(math.inf)
+            continue
+        a, t, g, st = verify(target[b:b + 1], None if draft is None else draft[b:b + 1], drafts[b:b + 1],
+                             None if n_drafts is None else n_drafts[b:b + 1], uniform[b:b + 1])
+        n = T if n_drafts is None else min(max(int(n_drafts[b]), 0), T)
+        left = int(lens[b]) - (n - a[0])
+        status |= st | (DEV_BAD_SEQ_LEN if left < 0 else 0)
+        accepted.append(a[0])
+        tokens.append(t[0])
+        after.append(max(left, 0))
+        gaps.append(g[0])
+    return accepted, tokens, after, gaps, status
