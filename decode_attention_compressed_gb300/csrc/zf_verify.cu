@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
   __shared__ float2 blocks[kVerifyWarps][kMaxBlocks];         // of this CTA's pieces
   __shared__ int sh_piece, sh_zero;
   __shared__ DF sh_x, sh_before;
-  __shared__ int sh_acc, sh_n;
+  __shared__ int sh_acc, sh_n, sh_off;
   __shared__ bool sh_idle;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t rank, ranks;
@@ -284,17 +284,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
       x[k] = t < T ? a.tokens_in[static_cast<size_t>(b) * T + t] : -1;
       v[k] = t < T ? a.uniform[static_cast<size_t>(b) * (T + 1) + t] : 0.f;
     }
-    int n = a.n_drafts ? a.n_drafts[b] : T;
-    // places that zf_map_tokens gave the request; a count that is no step's is refused like none
+    // places that zf_map_tokens gave the request (the last token's, then its drafts'); a count that is no
+    // step's is refused like none
     const int places = a.token_start ? a.token_start[b + 1] - a.token_start[b] : T + 1;
-    if (places < 1 || places > T + 1) {
-      if (places != 0 && rank == 0 && lane == 0) report(a.status, ZF_DEV_BAD_DRAFT);
-      n = 0;
-    }
-    if (n < 0 || n > T) {
+    const bool idle = places < 1 || places > T + 1;
+    const int most = idle ? 0 : places - 1;
+    int n = a.n_drafts ? a.n_drafts[b] : most;
+    if (idle ? places != 0 : n < 0 || n > most) {
       if (rank == 0 && lane == 0) report(a.status, ZF_DEV_BAD_DRAFT);
-      n = min(max(n, 0), T);
     }
+    n = min(max(n, 0), most);
     float p[2], q[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -318,7 +317,8 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     if (lane == 0) {
       sh_acc = acc;
       sh_n = n;
-      sh_idle = places < 1 || places > T + 1;
+      sh_off = a.token_start ? most : n;
+      sh_idle = idle;
     }
   }
   __syncthreads();
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     if (lane == 0) {
       a.accepted[b] = acc;
       if (a.out_lens) {
-        const int len = a.seq_lens[b] - (n - acc);
+        const int len = a.seq_lens[b] - (sh_off - acc);      // (places behind a request's drafts go too)
         if (len < 0) report(a.status, ZF_DEV_BAD_SEQ_LEN);
         a.out_lens[b] = max(len, 0);
       }

@@ -734,7 +734,8 @@ def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_draft
     each).  Returns (accepted [B], tokens [B][T+1]) int32: the accepted drafts, one sampled token, then -1.
     With seq_lens (and new_seq_lens, which may be the same tensor) the lengths are shortened by the
     refused drafts.  token_start [B+1] int32: what map_tokens gave in this step (zf_verify_mapped_drafts); a
-    request that got no places there keeps its length and gets accepted 0 and tokens -1."""
+    request that got no places there keeps its length and gets accepted 0 and tokens -1, one that got m
+    keeps m - 1 - accepted places fewer, whatever its n_drafts (at most m - 1)."""
     if not isinstance(draft_tokens, torch.Tensor) or draft_tokens.dim() != 2:
         raise ValueError("draft_tokens must be a [batch][drafts] tensor")
     B, T = draft_tokens.shape

@@ -446,7 +446,8 @@ size_t zf_q4_decode_attn_workspace_size(int32_t batch, int32_t tokens, int32_t n
  *   q [batch][T][num_q_heads][128] BF16; page_table, seq_lens, softmax_scale, out [batch][T]
  *   [num_q_heads][128] float32, lse [batch][T][num_q_heads] float32 and the workspace as for
  *   zf_decode_attn_multi: token t of request b attends to positions 0 .. seq_lens[b] - T + t, one
- *   that sees none gets out = 0 and lse = -inf.  A NaN or an infinity in a query row stays in that row.
+ *   that sees none gets out = 0 and lse = -inf.  (So row T - 1 is always a request's last token; see
+ *   zf_verify_mapped_drafts for requests with fewer new tokens than T.)  A NaN or an infinity in a query row stays in that row.
  *   A (kv head)'s records are read once per 32 columns (query heads per kv head x T).
  *   K and V are multiplied as the exact stored values, scores and sums in float32; the softmax
  *   weights enter the second product as two fp16 parts (about 22 bits).
@@ -533,6 +534,14 @@ zf_status zf_verify_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, con
  *                 token -1, its length unchanged (run its step again once pages are free).  So does, with
  *                 ZF_DEV_BAD_DRAFT, one that was given more than the T + 1 places of its last token and
  *                 T drafts.
+ *   A request that was given m places uses at most m - 1 drafts (n_drafts NULL: m - 1; a larger
+ *   n_drafts[b] is clamped and sets ZF_DEV_BAD_DRAFT), and its length becomes seq_lens[b] - (m - 1 - a):
+ *   the last token and the accepted drafts stay, refused drafts and padding go.
+ *   Steps in which requests have different numbers of drafts: map T + 1 places for every request, with any
+ *   tokens behind a request's drafts.  Row t of the queries, of attention's results and of
+ *   target_probs is then the request's token t throughout.  (Mapping n_b + 1 places saves pages, but the
+ *   attention calls put a request's last token into the last of its T + 1 rows: its tokens are rows T -
+ *   n_b .. T there and rows 0 .. n_b of target_probs here, so they have to be moved in between.)
  *   Other arguments and results as for zf_verify_drafts.
  */
 zf_status zf_verify_mapped_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, const float* target_probs,

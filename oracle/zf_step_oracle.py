@@ -235,7 +235,8 @@ def verify(target, draft, drafts, n_drafts, uniform):
 
 def verify_step(target, draft, drafts, n_drafts, uniform, starts, lens):
     """verify after map_tokens in one step: starts are its list starts, lens the lengths it gave.
-    (accepted, tokens, lens, gaps, status); a request without places keeps its length."""
+    (accepted, tokens, lens, gaps, status); a request without places keeps its length, any other ends with
+    its last token and the accepted drafts."""
     B, T = drafts.shape
     accepted, tokens, after, gaps, status = [], [], [], [], 0
     for b in range(B):
@@ -247,10 +248,12 @@ def verify_step(target, draft, drafts, n_drafts, uniform, starts, lens):
             after.append(int(lens[b]))
             gaps.append(math.inf)
             continue
-        a, t, g, st = verify(target[b:b + 1], None if draft is None else draft[b:b + 1], drafts[b:b + 1],
-                             None if n_drafts is None else n_drafts[b:b + 1], uniform[b:b + 1])
-        n = T if n_drafts is None else min(max(int(n_drafts[b]), 0), T)
-        left = int(lens[b]) - (n - a[0])
+        n = places - 1 if n_drafts is None else int(n_drafts[b])
+        if not 0 <= n <= places - 1:
+            status |= DEV_BAD_DRAFT
+            n = min(max(n, 0), places - 1)
+        a, t, g, st = verify(target[b:b + 1], None if draft is None else draft[b:b + 1], drafts[b:b + 1], [n], uniform[b:b + 1])
+        left = int(lens[b]) - (places - 1 - a[0])
         status |= st | (DEV_BAD_SEQ_LEN if left < 0 else 0)
         accepted.append(a[0])
         tokens.append(t[0])

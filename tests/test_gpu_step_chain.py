@@ -1,5 +1,5 @@
-"""The calls of a speculative step in a row (map, write, attend, verify) when requests get no places, over several
-steps, eager and captured, against the oracle step by step."""
+"""The calls of a speculative step in a row (map, write, attend, verify) when requests get no places, and when they
+have different numbers of drafts, over several steps, eager and captured, against the oracle step by step."""
 import numpy as np
 import pytest
 import torch
@@ -101,7 +101,12 @@ class Loop:
         assert self.d_lens.tolist() == w_lens and self.d_pos.tolist() == [pos]
         assert (self.c.records.cpu().numpy() == self.o.records).all()
         assert int(self.status) == st | vst and self.c.status_word() == 0
+        self.accepted = w_acc
         return st | vst
+
+    def step_accepted(self, x):
+        assert self.step(x) == 0
+        return self.accepted
 
 
 def inputs(B, T, seed, new=None):
@@ -173,3 +178,39 @@ def test_places_that_are_no_steps(zf, vocab):
     a, t = zf.verify_drafts(target.cuda(), drafts.cuda(), uniform.cuda(), seq_lens=out, new_seq_lens=out, status=status)
     assert a.tolist() == acc and t.tolist() == tok
     assert out.tolist() == [max(L, 0) for L in after] and int(status) == S.DEV_BAD_SEQ_LEN
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("padded", [True, False])
+def test_ragged_drafts_leave_no_padding(zf, padded, graph):
+    """0 to T drafts per request, with T + 1 places for every request or one more than its drafts: after every step a
+    request holds its last token and the accepted drafts and nothing else."""
+    B, T = 5, 4
+    loop = Loop(zf, B, T, [20, 0, 33, 15, 64], 8, 40, 53, graph)
+    rng = np.random.default_rng(54)
+    for s in range(5):
+        n = [0, 0, 0, 0, 0] if s == 2 else rng.permutation([0, 1, 2, T, T]).tolist()
+        x = inputs(B, T, 90 + s, [T + 1] * B if padded else [k + 1 for k in n])
+        x["n"] = i32(n)
+        before, kept = list(loop.lens), loop.step_accepted(x)
+        assert loop.lens == [L + 1 + a for L, a in zip(before, kept)] and all(a <= k for a, k in zip(kept, n))
+
+
+def test_drafts_without_places(zf):
+    """More drafts than places: only the placed ones count, and the status word says so; without n_drafts the places
+    decide."""
+    T, lens, places, n = 4, [50, 50, 50, 50], [2, 1, 5, 3], [3, 0, 5, -1]
+    B, vocab = len(lens), 100
+    g = torch.Generator().manual_seed(1)
+    target = torch.softmax(torch.randn(B, T + 1, vocab, generator=g), -1)
+    drafts = target[:, :T].argmax(-1).to(torch.int32)
+    uniform = torch.full((B, T + 1), 2.0 ** -10)               # every draft is accepted
+    starts = np.concatenate(([0], np.cumsum(places)))
+    for count in (n, None):
+        want = S.verify_step(target.numpy(), None, drafts.numpy(), count, uniform.numpy(), starts, lens)
+        assert want[0] == ([1, 0, 4, 0] if count else [1, 0, 4, 2]) and want[2] == ([50, 50, 50, 48] if count else [50] * 4)
+        status, out = torch.zeros(1, dtype=torch.int32, device="cuda"), i32(lens).cuda()
+        acc, tok = zf.verify_drafts(target.cuda(), drafts.cuda(), uniform.cuda(), n_drafts=None if count is None else i32(n).cuda(),
+                                    seq_lens=out, new_seq_lens=out, token_start=i32(starts).cuda(), status=status)
+        assert acc.tolist() == want[0] and tok.tolist() == want[1] and out.tolist() == want[2]
+        assert int(status) == want[4] == (S.DEV_BAD_DRAFT if count else 0)

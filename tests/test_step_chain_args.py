@@ -49,3 +49,7 @@ def test_oracle_step_pins():
     assert acc == [0, 0, 0] and tok == [[0, -1], [-1, -1], [0, -1]] and lens == [8, 7, 0] and st == S.DEV_BAD_SEQ_LEN
     acc, tok, lens, _, st = S.verify_step(p[:1], None, drafts[:1], None, u[:1], [0, 3], [9])
     assert acc == [0] and tok == [[-1, -1]] and lens == [9] and st == S.DEV_BAD_DRAFT
+    # two drafts' places, one draft: the place behind it goes too
+    acc, tok, lens, _, st = S.verify_step(p[:1].repeat(2, 1)[:, :3], None, np.array([[1, 1]]), [1], np.array([[0.1, 0.1, 0.9]], np.float32),
+                                          [0, 3], [9])
+    assert acc == [1] and lens == [8] and st == 0
