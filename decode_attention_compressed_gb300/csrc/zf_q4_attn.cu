@@ -82,6 +82,8 @@ struct Q4AttnArgs {
   int32_t tokens;             // new tokens per request T: query head qh = head * T + token (hq, group count them)
   float scale_log2;           // softmax scale * log2(e) * scales of the decoding
   float v_factor;
+  uint64_t wait_limit_ns;     // limit of the waits for copies (kWaitTimeoutNs; tests shorten it)
+  int32_t hold_copies;        // tests: every warp's first wait runs out (see the barriers' initial counts)
 };
 
 // What a warp keeps of the query columns of its current pair.
@@ -358,7 +360,8 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
   uint8_t* stages = smem + L.stages + static_cast<size_t>(warp) * kWarpStages * kStageQ4;
   uint8_t* qbuf = smem + L.qbuf + static_cast<size_t>(warp) * C::kCols * kQ4QRowBytes;
   Q4Columns<kNT>& cols = reinterpret_cast<Q4Columns<kNT>*>(smem + L.cols)[warp];
-  if (lane < kWarpStages) mbar_init(&bars[lane], 1);
+  // (tests of the waits: the first stage expects one arrival more, which comes when its wait has run out)
+  if (lane < kWarpStages) mbar_init(&bars[lane], a.hold_copies && lane == 0 ? 2 : 1);
   fence_mbar_init();
   wait_prior_grid();          // inputs may come from the preceding grid
   allow_next_grid();
@@ -470,8 +473,14 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
     if (kFold && more)
       next = next_unit(a, prefix, HS, tpp, f, stages + (sidx ^ 1) * kStageQ4, &bars[sidx ^ 1], lane, policy);
     if (u.have) {
-      if (!mbar_wait(&bars[sidx], (phase >> sidx) & 1u)) {
-        if (lane == 0) report(a.status, ZF_DEV_TIMEOUT);
+      // One outcome for the warp: lanes time their waits on their own, and what follows needs all of them.  (The
+      // vote costs the ragged workload 68.3 -> 68.9 us and the long context 109.3 -> 110.6; taken together with
+      // the vote on the scores below, the same and 4% at 14 and 21 columns.)
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars[sidx], (phase >> sidx) & 1u, a.wait_limit_ns))) {
+        if (lane == 0) {
+          report(a.status, ZF_DEV_TIMEOUT);
+          if (a.hold_copies) mbar_arrive(&bars[0]);
+        }
         // copies still in flight must land before the CTA exits
         mbar_wait(&bars[sidx], (phase >> sidx) & 1u);
         if (next.have) mbar_wait(&bars[sidx ^ 1], (phase >> (sidx ^ 1)) & 1u);
@@ -932,10 +941,11 @@ extern "C" size_t zf_q4_decode_attn_workspace_size(int32_t batch, int32_t tokens
   return q4_plan(batch, num_q_heads * tokens, num_kv_heads, page_size, max_pages_per_req, sms).bytes();
 }
 
-extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, int32_t batch, int32_t tokens,
-                                       int32_t num_q_heads, const int32_t* page_table, int32_t max_pages,
-                                       const int32_t* seq_lens, float softmax_scale, float* out, float* lse,
-                                       void* workspace, size_t workspace_bytes, void* stream) {
+static zf_status q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, int32_t batch, int32_t tokens,
+                                int32_t num_q_heads, const int32_t* page_table, int32_t max_pages,
+                                const int32_t* seq_lens, float softmax_scale, float* out, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream, uint64_t wait_limit_ns = kWaitTimeoutNs,
+                                bool hold_copies = false) {
   zf_status st = check_q4_cache(c);
   if (st != ZF_OK) return st;
   if (!q4_shape_ok(batch, tokens, num_q_heads, c->num_kv_heads, max_pages)) return ZF_ERR_INVALID_ARGUMENT;
@@ -977,6 +987,8 @@ extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, 
   a.max_pages = max_pages;
   a.scale_log2 = scale_log2;
   a.v_factor = c->v_scale * kQ4ScaleFactor;
+  a.wait_limit_ns = wait_limit_ns;
+  a.hold_copies = hold_copies;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool multi = tokens > 1;
@@ -1007,4 +1019,22 @@ extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* c, const uint16_t* q, 
   if (parts <= kMergeOne) return launch_pdl(q4_merge_kernel<1>, (rows + 3) / 4, 128, 0, s, m);
   if (parts <= kMergeFour) return launch_pdl(q4_merge_kernel<4>, rows, 128, 0, s, m);
   return launch_pdl(q4_merge_kernel<16>, rows, 512, 0, s, m);
+}
+
+extern "C" zf_status zf_q4_decode_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t batch, int32_t tokens,
+                                       int32_t num_q_heads, const int32_t* page_table, int32_t max_pages_per_req,
+                                       const int32_t* seq_lens, float softmax_scale, float* out, float* lse,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  return q4_decode_attn(cache, q, batch, tokens, num_q_heads, page_table, max_pages_per_req, seq_lens, softmax_scale, out,
+                        lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" zf_status zf_q4_decode_attn_wait_test(const zf_q4_cache* cache, const uint16_t* q, int32_t batch,
+                                                 int32_t tokens, int32_t num_q_heads, const int32_t* page_table,
+                                                 int32_t max_pages_per_req, const int32_t* seq_lens,
+                                                 float softmax_scale, float* out, float* lse, void* workspace,
+                                                 size_t workspace_bytes, uint64_t wait_limit_ns, void* stream) {
+  if (wait_limit_ns < 1000 || wait_limit_ns > kWaitTimeoutNs) return ZF_ERR_INVALID_ARGUMENT;
+  return q4_decode_attn(cache, q, batch, tokens, num_q_heads, page_table, max_pages_per_req, seq_lens, softmax_scale, out,
+                        lse, workspace, workspace_bytes, stream, wait_limit_ns, true);
 }

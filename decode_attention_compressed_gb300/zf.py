@@ -100,6 +100,9 @@ SIGNATURES = {
     "zf_q4_decode_attn": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_int32, _c_int32, _c_int32, _c_void_p,
                                      _c_int32, _c_void_p, _c_float, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
                                      _c_void_p]),
+    "zf_q4_decode_attn_wait_test": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_int32, _c_int32, _c_int32,
+                                               _c_void_p, _c_int32, _c_void_p, _c_float, _c_void_p, _c_void_p,
+                                               _c_void_p, _c_size_t, ctypes.c_uint64, _c_void_p]),
     "zf_map_tokens": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_void_p, _c_int32, _c_void_p, _c_void_p]),
@@ -664,6 +667,28 @@ def q4_decode_attn(cache: Q4Cache, q, page_table, seq_lens, scale=None, out=None
                                    out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, s)
     if code:
         _check("zf_q4_decode_attn", code)
+    return out, lse
+
+
+@_on_stream
+def q4_decode_attn_wait_test(cache: Q4Cache, q, page_table, seq_lens, scale=None, wait_limit_ns=1000000):
+    """zf_q4_decode_attn_wait_test (tests of the failure path): q4_decode_attn on q [B][T][Hq][128] whose warps' first
+    wait for copied records runs out after wait_limit_ns.  Returns (out, lse), which are not meaningful; the
+    cache's status word gets DEV_TIMEOUT."""
+    dev = cache._device
+    B, T, Hq = q.shape[:3]
+    q = _tensor(q, "q", _BITS16, dev, (B, T, Hq, HEAD_DIM))
+    page_table, seq_lens = _tables(page_table, seq_lens, dev, B)
+    max_pages = page_table.shape[1]
+    s = _launch_stream(dev)
+    out = torch.empty((B, T, Hq, HEAD_DIM), dtype=torch.float32, device=dev)
+    lse = torch.empty((B, T, Hq), dtype=torch.float32, device=dev)
+    workspace = new_workspace(q4_workspace_size(B, T, Hq, cache._sizes[1], cache._sizes[2], max_pages), dev)
+    _check("zf_q4_decode_attn_wait_test",
+           lib().zf_q4_decode_attn_wait_test(cache._ref, q.data_ptr(), B, T, Hq, page_table.data_ptr(), max_pages,
+                                             seq_lens.data_ptr(), 1.0 / math.sqrt(HEAD_DIM) if scale is None else scale,
+                                             out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                             int(wait_limit_ns), s))
     return out, lse
 
 

@@ -453,12 +453,26 @@ size_t zf_q4_decode_attn_workspace_size(int32_t batch, int32_t tokens, int32_t n
  *   weights enter the second product as two fp16 parts (about 22 bits).
  *   Two kernels are enqueued (attention, then merge), launched with programmatic stream
  *   serialisation; results are deterministic (no atomics).  A page id out of range sets
- *   ZF_DEV_BAD_PAGE_ID and its tokens are skipped.
+ *   ZF_DEV_BAD_PAGE_ID and its tokens are skipped.  A wait for copied records that takes 2 s gives up: it
+ *   sets ZF_DEV_TIMEOUT, and out and lse of that call mean nothing.
  */
 zf_status zf_q4_decode_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t batch, int32_t tokens,
                             int32_t num_q_heads, const int32_t* page_table, int32_t max_pages_per_req,
                             const int32_t* seq_lens, float softmax_scale, float* out, float* lse,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * zf_q4_decode_attn_wait_test — for tests of the failure path: zf_q4_decode_attn whose warps' first wait for
+ * copied records runs out on purpose after wait_limit_ns (1 us .. 2 s; zf_q4_decode_attn's limit is 2 s).
+ * ZF_DEV_TIMEOUT is then set, the warps let their copies land and stop, out and lse mean nothing, and
+ * the context and the stream stay usable for the next call.  No fault, trap or endless wait is involved.
+ * ZF_ERR_INVALID_ARGUMENT for a limit out of range; other arguments as for zf_q4_decode_attn.
+ */
+zf_status zf_q4_decode_attn_wait_test(const zf_q4_cache* cache, const uint16_t* q, int32_t batch, int32_t tokens,
+                                      int32_t num_q_heads, const int32_t* page_table,
+                                      int32_t max_pages_per_req, const int32_t* seq_lens, float softmax_scale,
+                                      float* out, float* lse, void* workspace, size_t workspace_bytes,
+                                      uint64_t wait_limit_ns, void* stream);
 
 /*
  * zf_map_tokens — block tables and slot maps on the GPU: gives every request's new tokens their
