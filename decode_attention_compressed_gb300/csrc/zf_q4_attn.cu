@@ -186,11 +186,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // The query rows of a pair (query heads h0 .. h0 + nh - 1 of request b), by one warp, into shared memory as fp16:
 // each row times a power of two that brings its largest exponent to 11; its factor takes that back.  Rows
-// past nh are zero.  Channel c = 32 t + 8 j + e goes to byte 64 j + 16 t + 2 e: lane t's words of k-steps
-// 2j, 2j+1 are 16 bytes, and the rows' stride spreads a warp's reads over the banks.  A warp takes four rows one
-// by one (one maximum over the lanes each), more two by two.  (Rows one by one, and a division per
-// column here, for the mask and for the result: 64 requests of 512 tokens, 32 columns 61.2 us instead of
-// 51.4; four rows two by two: the long-context workload 110.8 instead of 109.7.)
+// past nh are zero.  All loads come before the first store, so they are under way together.  (Ordinary loads, at
+// the same times as read-only ones, which need q to stay as it is for the whole grid: this grid starts while the
+// kernel ahead of it may still be writing q.)  Channel c = 32 t + 8 j + e goes to byte 64 j + 16 t + 2 e: lane
+// t's words of k-steps 2j, 2j+1 are 16 bytes, and the rows' stride spreads a warp's reads over the banks.  A
+// warp takes four rows one by one (one maximum over the lanes each), more two by two.  (Rows one by one, and a
+// division per column here, for the mask and for the result: 64 requests of 512 tokens, 32 columns 61.2 us
+// instead of 51.4; four rows two by two: the long-context workload 110.8 instead of 109.7.)
 template <int kNT, bool kFold>
 __device__ __forceinline__ void stage_q(const Q4AttnArgs& a, int b, int h0, int nh, uint8_t* qb, Q4Columns<kNT>& cols,
                                         int lane) {
@@ -218,8 +220,8 @@ __device__ __forceinline__ void stage_q(const Q4AttnArgs& a, int b, int h0, int 
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const uint32_t* src = base + static_cast<size_t>(__shfl_sync(0xFFFFFFFFu, rel, r)) * (ZF_HEAD_DIM / 2);
-      v[r][0] = r < nh ? __ldg(src) : 0u;                    // (read-only: every row's loads may go first)
-      v[r][1] = r < nh ? __ldg(src + 32) : 0u;
+      v[r][0] = r < nh ? src[0] : 0u;
+      v[r][1] = r < nh ? src[32] : 0u;
     }
     uint8_t* dst = qb + 64 * ((lane >> 2) & 3) + 16 * (lane >> 4) + 4 * (lane & 3);        // channel 2 lane; 2 lane + 64 is 32 on
 #pragma unroll
@@ -245,7 +247,7 @@ __device__ __forceinline__ void stage_q(const Q4AttnArgs& a, int b, int h0, int 
     for (int i = 0; i < kRows / 2; ++i) {
       const int r = 2 * i + (lane >> 4);
       const size_t row = static_cast<size_t>(__shfl_sync(0xFFFFFFFFu, rel, r)) * (ZF_HEAD_DIM / 8);
-      v[i] = r < nh ? __ldg(base + row) : make_uint4(0u, 0u, 0u, 0u);          // (read-only: every row's loads may go first)
+      v[i] = r < nh ? base[row] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int i = 0; i < kRows / 2; ++i) {
