@@ -95,6 +95,12 @@ __device__ __forceinline__ void sleep_for_ns(uint64_t ns) {
 __device__ __forceinline__ void wait_prior_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void allow_next_grid() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Barrier of a cluster's threads.  The .aligned form needs each warp to arrive as one, whatever branches lie ahead.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // ------------------------------------------------------------------------------- bulk copies
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
   uint64_t policy;

@@ -111,9 +111,6 @@ __device__ __forceinline__ int entry_chunks(const MapArgs& a) {
   return static_cast<int>((static_cast<long long>(a.max_tokens) + 3) >> 2);
 }
 
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

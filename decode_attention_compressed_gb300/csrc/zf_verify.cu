@@ -50,10 +50,6 @@ struct VerifyArgs {
   int32_t batch, T, vocab;
 };
 
-__device__ __forceinline__ void v_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Store a sum into the shared memory of CTA `rank` of the cluster, at this CTA's address of `p`.
 __device__ __forceinline__ void dsmem_store(float2* p, uint32_t rank, float hi, float lo) {
   uint32_t addr;
@@ -270,7 +266,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
   const int T = a.T, V = a.vocab;
   allow_next_grid();
   wait_prior_grid();
-  v_cluster_sync();           // the cluster's CTAs all run before their shared memory is written
+  cluster_sync();           // the cluster's CTAs all run before their shared memory is written
 
   // ---- accepted drafts (warp 0 of every CTA; T <= 64: two per lane)
   if (warp == 0) {
@@ -351,7 +347,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     const DF s = row.q ? piece_sum<kVec, true>(row, lo, hi, blen, blocks[warp], lane)
                        : piece_sum<kVec, false>(row, lo, hi, blen, blocks[warp], lane);
     if (lane < static_cast<int>(ranks)) dsmem_store(&sums[mine], lane, s.hi, s.lo);
-    v_cluster_sync();
+    cluster_sync();
     if (warp == 0) {                                    // the same in every CTA of the cluster
       DF x, before = {0.f, 0.f};
       bool zero;
@@ -367,7 +363,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_kernel(const VerifyA
     if (!sh_zero || (!row.q && row.drop < 0)) break;    // uniform over the cluster
     row.q = nullptr;                                    // p nowhere above q: sample from p itself
     row.drop = -1;
-    v_cluster_sync();                                   // the sums have been read everywhere
+    cluster_sync();                                   // the sums have been read everywhere
   }
   const int piece = sh_piece;
   if (piece >= 0 ? piece == mine : mine == 0) {         // one warp of the cluster
