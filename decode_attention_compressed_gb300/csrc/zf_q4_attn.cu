@@ -4,10 +4,11 @@
 // Mathematics.  K and V are code * s (16-channel blocks, e2m1 codes of two significant bits, e4m3
 // scales of four): every product code * s has at most six significant bits and is exact in fp16, so
 // the operands of the matrix instructions are the stored values themselves.  q (BF16) is brought into
-// fp16 by a power of two per row, which its scores take back: exact down to 2^-36 of the row's
-// largest value.  Scores, running maximum and sum and the output are float32.  The softmax weights p
-// (times 2^7, so that the remainder of a small weight stays clear of fp16's subnormals) are split
-// into an fp16 high part and an fp16 remainder, two MMAs: about 22 bits.
+// fp16 by a power of two per row, which its scores take back: values down to 2^-28 of the row's largest exponent
+// are exact, smaller ones fall on a grid of 2^-35 (off by 2^-36 at most).  Scores, running maximum and sum
+// and the output are float32.  The softmax weights p (times 2^7, so that the remainder of a small weight
+// stays clear of fp16's subnormals) are split into an fp16 high part and an fp16 remainder, two MMAs: off by
+// at most 2^-22 of the weight or, where parts are subnormal, 2^-30 of the range's largest (which is above 2^6).
 //
 // Work split.  The 16-token records of all (request, kv head, column slice) pairs, laid end to end, are
 // cut into one equal contiguous range per warp of the grid (one CTA per SM).  A warp goes through its
@@ -30,11 +31,11 @@
 //    operand (two tokens, one channel).
 //  * e2m1 pairs become half pairs in one conversion, and one multiplication applies the scale.
 //
-// Bound.  Up to 8 columns: issue slots and half-rate operations beside the copies (331 and 356 instructions per
-// record; 106 and 127 cycles per record and SM, the copies alone 101).  Wider: the matrix instructions, each of
-// which holds its scheduler for 9.4 cycles and overlaps other work only in part (28 columns: 96 per
-// record, 226 of 430 cycles).  The 5th-generation tensor cores do not pay here: with K in tensor memory, V^T
-// in shared memory and a product per 128 tokens the softmax's chain of dependent steps sets the pace,
+// Bound.  Up to 8 columns no unit is near its limit (issue slots 62 to 65% busy, ALU 52 to 57%, DRAM 54 to 62%):
+// 340 and 369 instructions per record, many of half rate, beside the copies; 106 and 127 cycles per record and
+// SM, the copies alone 101.  Wider: the matrix instructions, each of which holds its scheduler for 9.4 cycles and
+// overlaps other work only in part (28 columns: 96 per record, 226 of 430 cycles).  The 5th-generation tensor
+// cores do not pay here: with K in tensor memory, V^T in shared memory and a product per 128 tokens the softmax's chain of dependent steps sets the pace,
 // 2700 to 3100 cycles per 128 tokens for 16 to 32 columns alike (28 columns, 32 requests of 8192 tokens 87 us
 // against 95 here, of 2048 tokens and 64 requests 125 against 105, of 128 tokens 41 against 27).
 #include <cuda_runtime.h>
@@ -59,7 +60,8 @@ constexpr float kUnseen = -3e38f;                        // a maximum before any
 constexpr float kPShift = 7.f;                           // weights are 2^7 times their usual size
 
 // Warps per CTA by the number of 8-column tiles of a pass (kNT), from the registers they need (128, 168
-// and, for three and four tiles, 255 per thread).
+// and, for three and four tiles, 255 per thread).  Only the instances for up to 4 columns need no more than that;
+// the others spill (bytes stored: 5 to 8 columns 4 to 8, two tiles 24, three 28, four 104).
 template <int kNT>
 struct Q4Cfg {
   static constexpr int kWarps = kNT == 1 ? 16 : kNT == 2 ? 12 : 8;
@@ -168,8 +170,9 @@ __device__ __forceinline__ F2 mul2(F2 a, F2 b) {
 }
 
 // d += s, rounded to nearest.  The matrix instructions cut their float sums off instead, a bias that
-// grows along a chain of accumulations, so a chain is one unit long and is added to the output here: error
-// against 64 bits at the long-context workload 6.1e-7 instead of 2.1e-6, for 2 to 8% of the time.
+// grows along a chain of accumulations, so a chain is one unit long and is added to the output here: a quarter of
+// the error against 64 bits at the long-context workload (now 5.3e-7 of the outputs' root mean square; a plain
+// float32 form 4.7e-7), for 2 to 8% of the time.
 __device__ __forceinline__ void add4(float (&d)[4], const float (&s)[4]) {
   const F2 a = add2(F2{d[0], d[1]}, F2{s[0], s[1]}), b = add2(F2{d[2], d[3]}, F2{s[2], s[3]});
   d[0] = a.x;

@@ -448,7 +448,8 @@ static zf_status verify(int32_t batch, int32_t max_drafts, int32_t vocab, const 
   a.batch = batch;
   a.T = max_drafts;
   a.vocab = vocab;
-  // CTAs per request: enough to fill the 152 SMs with two CTAs each, at least 4096 entries per CTA.
+  // CTAs per request: a power of two that brings the grid to 256 CTAs or more (at two per SM most of the GPU's
+  // 152), with at least 2048 entries per CTA.
   int ctas = 1;
   while (ctas < kVerifyMaxCluster && batch * ctas < 256 && vocab / (2 * ctas) >= 2048) ctas *= 2;
   static std::mutex mu;

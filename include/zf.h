@@ -447,10 +447,13 @@ size_t zf_q4_decode_attn_workspace_size(int32_t batch, int32_t tokens, int32_t n
  *   [num_q_heads][128] float32, lse [batch][T][num_q_heads] float32 and the workspace as for
  *   zf_decode_attn_multi: token t of request b attends to positions 0 .. seq_lens[b] - T + t, one
  *   that sees none gets out = 0 and lse = -inf.  (So row T - 1 is always a request's last token; see
- *   zf_verify_mapped_drafts for requests with fewer new tokens than T.)  A NaN or an infinity in a query row stays in that row.
+ *   zf_verify_mapped_drafts for requests with fewer new tokens than T.)  A NaN or an infinity in a
+ *   query row stays in that row.
  *   A (kv head)'s records are read once per 32 columns (query heads per kv head x T).
- *   K and V are multiplied as the exact stored values, scores and sums in float32; the softmax
- *   weights enter the second product as two fp16 parts (about 22 bits).
+ *   K and V are multiplied as the exact stored values, scores and sums in float32; a query row's values
+ *   enter as fp16 numbers times a power of two of its own (exact down to 2^-28 of the row's largest
+ *   exponent, off by at most 2^-36 of it below), the softmax weights as two fp16 parts (off by at
+ *   most 2^-22 of the weight or 2^-30 of the largest one).
  *   Two kernels are enqueued (attention, then merge), launched with programmatic stream
  *   serialisation; results are deterministic (no atomics).  A page id out of range sets
  *   ZF_DEV_BAD_PAGE_ID and its tokens are skipped.  A wait for copied records that takes 2 s gives up: it
