@@ -35,9 +35,10 @@
 // 340 and 369 instructions per record, many of half rate, beside the copies; 106 and 127 cycles per record and
 // SM, the copies alone 101.  Wider: the matrix instructions, each of which holds its scheduler for 9.4 cycles and
 // overlaps other work only in part (28 columns: 96 per record, 226 of 430 cycles).  The 5th-generation tensor
-// cores do not pay here: with K in tensor memory, V^T in shared memory and a product per 128 tokens the softmax's chain of dependent steps sets the pace,
-// 2700 to 3100 cycles per 128 tokens for 16 to 32 columns alike (28 columns, 32 requests of 8192 tokens 87 us
-// against 95 here, of 2048 tokens and 64 requests 125 against 105, of 128 tokens 41 against 27).
+// cores do not pay here: with K in tensor memory, V^T in shared memory and a product per 128 tokens the softmax's
+// chain of dependent steps sets the pace, 2700 to 3100 cycles per 128 tokens for 16 to 32 columns alike (28
+// columns, 32 requests of 8192 tokens 87 us against 95 here, of 2048 tokens and 64 requests 125 against 105, of
+// 128 tokens 41 against 27).
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>

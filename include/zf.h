@@ -556,8 +556,9 @@ zf_status zf_verify_drafts(int32_t batch, int32_t max_drafts, int32_t vocab, con
  *   the last token and the accepted drafts stay, refused drafts and padding go.
  *   Steps in which requests have different numbers of drafts: map T + 1 places for every request, with any
  *   tokens behind a request's drafts.  Row t of the queries, of attention's results and of
- *   target_probs is then the request's token t throughout.  (Mapping n_b + 1 places saves pages, but the
- *   attention calls put a request's last token into the last of its T + 1 rows: its tokens are rows T -
+ *   target_probs is then the request's token t throughout.  (A request whose row of the page table has room
+ *   for fewer is refused then.  Mapping n_b + 1 places needs no more room than the drafts, but the attention
+ *   calls put a request's last token into the last of its T + 1 rows: its tokens are rows T -
  *   n_b .. T there and rows 0 .. n_b of target_probs here, so they have to be moved in between.)
  *   Other arguments and results as for zf_verify_drafts.
  */

@@ -214,3 +214,32 @@ def test_drafts_without_places(zf):
                                     seq_lens=out, new_seq_lens=out, token_start=i32(starts).cuda(), status=status)
         assert acc.tolist() == want[0] and tok.tolist() == want[1] and out.tolist() == want[2]
         assert int(status) == want[4] == (S.DEV_BAD_DRAFT if count else 0)
+
+
+def test_two_loops_at_once_on_streams_of_their_own(zf):
+    """Two loops whose steps overlap on two streams: every call of a step is ordered on its loop's stream."""
+    B, T = 3, 3
+    loops = [Loop(zf, B, T, lens, 8, 20, 55 + i, False) for i, lens in enumerate(([30, 5, 17], [16, 0, 40]))]
+    streams = [torch.cuda.Stream() for _ in loops]
+    steps = [[inputs(B, T, 200 + 10 * i + s) for s in range(2)] for i in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for s in range(2):
+        for i, (loop, stream) in enumerate(zip(loops, streams)):
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(2_000_000)                 # the streams' work piles up and overlaps
+                loop.x = {n: t.cuda(non_blocking=True) for n, t in steps[i][s].items()}
+                got[i].append([t.clone() for t in loop.call()[2:]])
+    torch.cuda.synchronize()
+    for i, loop in enumerate(loops):
+        table, lens, held, pos = loop.table, loop.lens, loop.held, 0
+        for x, (acc, tok) in zip(steps[i], got[i]):
+            table, lens, held, pos, starts, ids, positions, _, st = S.map_tokens(table, lens, held, x["new"].tolist(), loop.free,
+                                                                                 pos, PAGE, B * (T + 1))
+            assert st == 0
+            loop.o.write(H.np_bits(x["k"]), H.np_bits(x["v"]), ids, positions)
+            w_acc, w_tok, lens, gaps, _ = S.verify_step(x["target"].numpy(), x["draft"].numpy(), x["drafts"].numpy(), None,
+                                                        x["uniform"].numpy(), starts, lens)
+            assert min(gaps) > 2.0 ** -44 and acc.tolist() == w_acc and tok.tolist() == w_tok
+        assert loop.d_lens.tolist() == lens and (loop.c.records.cpu().numpy() == loop.o.records).all()
+        assert int(loop.status) == 0

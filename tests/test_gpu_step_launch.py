@@ -165,12 +165,11 @@ def test_a_step_behind_a_late_writer(zf):
     """Map, write, attend and verify in a row, each started early behind the one before, behind a kernel that writes
     the lengths and the numbers of new tokens late."""
     B, T, hkv, hq, page, V = 3, 3, 2, 8, 16, 4000
-    lens, pool = [300, 17, 95], 40
+    lens = [300, 17, 95]
     c, o, table, sl = build(zf, lens, hkv, page, 33)
     held = [-(-L // page) for L in lens]
     wide = np.full((B, table.shape[1] + 3), -1)
     wide[:, :table.shape[1]] = table.numpy()
-    spare = i32([c.num_pages - 1, c.num_pages - 2])
     used = set(wide[b, j] for b in range(B) for j in range(held[b]))
     free = [p for p in range(c.num_pages) if p not in used]
     g = torch.Generator().manual_seed(34)
@@ -180,7 +179,7 @@ def test_a_step_behind_a_late_writer(zf):
     drafts, uniform = torch.randint(0, V, (B, T), generator=g).to(torch.int32), torch.rand(B, T + 1, generator=g)
     new = [T + 1, 0, T + 1]
     w_table, w_lens, w_held, w_pos, starts, ids, pos, _, st = S.map_tokens(wide, lens, held, new, free, 0, page, B * (T + 1))
-    assert st == 0 and len(spare) == 2
+    assert st == 0
     live_lens, live_new = i32([5, 5, 5]).cuda(), i32([1, 1, 1]).cuda()
     d_table, d_held, d_free, d_pos = i32(wide).cuda(), i32(held).cuda(), i32(free).cuda(), i32([0]).cuda()
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
