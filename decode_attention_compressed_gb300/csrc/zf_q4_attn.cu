@@ -480,8 +480,8 @@ __global__ void __launch_bounds__(Q4Cfg<kNT>::kThreads, 1) attn_q4_kernel(const 
       next = next_unit(a, prefix, HS, tpp, f, stages + (sidx ^ 1) * kStageQ4, &bars[sidx ^ 1], lane, policy);
     if (u.have) {
       // One outcome for the warp: lanes time their waits on their own, and what follows needs all of them.  (The
-      // vote costs the ragged workload 68.3 -> 68.9 us and the long context 109.3 -> 110.6; taken together with
-      // the vote on the scores below, the same and 4% at 14 and 21 columns.)
+      // vote costs the ragged workload 68.3 -> 68.9 us and the long context 109.3 -> 110.6, as much as a bare warp
+      // barrier does; taken together with the vote on the scores below, the same and 4% at 14 and 21 columns.)
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bars[sidx], (phase >> sidx) & 1u, a.wait_limit_ns))) {
         if (lane == 0) {
           report(a.status, ZF_DEV_TIMEOUT);
