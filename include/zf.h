@@ -497,9 +497,9 @@ zf_status zf_q4_decode_attn_wait_test(const zf_q4_cache* cache, const uint16_t* 
  *   When the pages or the max_tokens entries do not suffice, nothing is mapped: every request is
  *   treated as if it had no new tokens, and ZF_DEV_CAPACITY is set.  The step's other calls then run
  *   on requests whose tokens have no places: zf_q4_write_tokens skips every entry, attention's rows
- *   mean nothing, and zf_verify_mapped_drafts, given token_start, leaves tokens and lengths alone.  A request with a negative length or
- *   count, more pages than max_pages_per_req, or more tokens than its pages hold gets no tokens and
- *   sets ZF_DEV_BAD_SEQ_LEN.
+ *   mean nothing, and zf_verify_mapped_drafts, given token_start, leaves tokens and lengths alone.
+ *   A request with a negative length or count, more pages than max_pages_per_req, or more tokens than its
+ *   pages hold gets no tokens and sets ZF_DEV_BAD_SEQ_LEN.
  *   status: optional device word.  batch <= ZF_MAX_BATCH; max_pages_per_req * page_size < 2^31;
  *   max_tokens <= 2^30.  One kernel (two for long lists), launched with programmatic stream serialisation.
  */
