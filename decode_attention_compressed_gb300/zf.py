@@ -103,6 +103,10 @@ SIGNATURES = {
     "zf_q4_decode_attn_wait_test": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_int32, _c_int32, _c_int32,
                                                _c_void_p, _c_int32, _c_void_p, _c_float, _c_void_p, _c_void_p,
                                                _c_void_p, _c_size_t, ctypes.c_uint64, _c_void_p]),
+    "zf_q4_chunk_attn_workspace_size": (_c_size_t, [_c_int32, _c_int32, _c_int32, _c_int32, _c_int32, _c_int32]),
+    "zf_q4_chunk_attn": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_int32, _c_int32, _c_int32, _c_void_p,
+                                    _c_void_p, _c_int32, _c_void_p, _c_float, _c_int32, _c_float, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
     "zf_map_tokens": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_void_p, _c_int32, _c_void_p, _c_void_p]),
@@ -689,6 +693,55 @@ def q4_decode_attn_wait_test(cache: Q4Cache, q, page_table, seq_lens, scale=None
                                              seq_lens.data_ptr(), 1.0 / math.sqrt(HEAD_DIM) if scale is None else scale,
                                              out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
                                              int(wait_limit_ns), s))
+    return out, lse
+
+
+def q4_chunk_workspace_size(batch, rows, num_q_heads, num_kv_heads, page_size, max_pages) -> int:
+    return int(lib().zf_q4_chunk_attn_workspace_size(batch, rows, num_q_heads, num_kv_heads, page_size, max_pages))
+
+
+@_on_stream
+def q4_chunk_attn(cache: Q4Cache, q, page_table, seq_lens, token_start, scale=None, window=0, softcap=0.0, slopes=None,
+                  out=None, lse=None, workspace=None):
+    """zf_q4_chunk_attn: attention of a ragged batch of new tokens over the 4-bit cache.  q [rows][Hq][128] int16 BF16
+    bits or bfloat16: rows token_start[b] .. token_start[b+1] - 1 are the last of request b's seq_lens[b] tokens
+    (token_start [B+1] int32 as map_tokens gives it); page_table [>= B][*], seq_lens [>= B].  window > 0: a row
+    sees that many positions, its own the last; softcap > 0: scores c tanh(s / c); slopes [Hq] float32: plus
+    slopes[h] * (j - p).  Returns (out bfloat16 of q's shape, lse float32 [rows][Hq]); rows of no request are left
+    as they are (undefined in tensors made here)."""
+    dev = cache._device
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    shape = q.shape
+    if len(shape) != 3 or shape[-1] != HEAD_DIM:
+        raise ValueError(f"q: shape {list(shape)}, expected [*][*][{HEAD_DIM}]")
+    q = _tensor(q, "q", _BITS16, dev, shape)
+    if not isinstance(token_start, torch.Tensor) or token_start.dim() != 1 or token_start.shape[0] < 1:
+        raise ValueError("token_start must be a [batch + 1] tensor")
+    token_start = _tensor(token_start, "token_start", _I32, dev, token_start.shape)
+    N, Hq, B = shape[0], shape[1], token_start.shape[0] - 1
+    page_table, seq_lens = _tables(page_table, seq_lens, dev, B)
+    max_pages = page_table.shape[1]
+    slope_ptr = None
+    if slopes is not None:
+        slopes = _tensor(slopes, "slopes", _F32, dev, (Hq,))
+        slope_ptr = slopes.data_ptr()
+    out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if out is None else \
+        _tensor(out, "out", _BITS16, dev, shape, write=True)
+    lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if lse is None else \
+        _tensor(lse, "lse", _F32, dev, shape[:-1], write=True)
+    if workspace is not None:
+        workspace = _tensor(workspace, "workspace", (getattr(workspace, "dtype", None),), dev,
+                            getattr(workspace, "shape", None), write=True)
+    s = _launch_stream(dev)
+    if workspace is None:
+        workspace = new_workspace(q4_chunk_workspace_size(B, N, Hq, cache._sizes[1], cache._sizes[2], max_pages), dev)
+    code = lib().zf_q4_chunk_attn(cache._ref, q.data_ptr(), N, B, Hq, token_start.data_ptr(), page_table.data_ptr(),
+                                  max_pages, seq_lens.data_ptr(), 1.0 / math.sqrt(HEAD_DIM) if scale is None else scale,
+                                  window, softcap, slope_ptr, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                  workspace.nbytes, s)
+    if code:
+        _check("zf_q4_chunk_attn", code)
     return out, lse
 
 

@@ -477,6 +477,40 @@ zf_status zf_q4_decode_attn_wait_test(const zf_q4_cache* cache, const uint16_t* 
                                       float* out, float* lse, void* workspace, size_t workspace_bytes,
                                       uint64_t wait_limit_ns, void* stream);
 
+/* Workspace bytes zf_q4_chunk_attn needs for these sizes on the current device.  0 on invalid sizes.  More rows
+ * never need fewer, the other sizes change nothing but the query heads per kv head. */
+size_t zf_q4_chunk_attn_workspace_size(int32_t batch, int32_t rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                       int32_t page_size, int32_t max_pages_per_req);
+
+/*
+ * zf_q4_chunk_attn — attention of a ragged batch of new tokens over the 4-bit cache: chunks of prompts, single
+ * tokens, or both in one call.  The new tokens' keys and values are already in the cache.
+ *   q [rows][num_q_heads][128] BF16: rows token_start[b] .. token_start[b+1] - 1 are request b's new tokens, the
+ *                 last ones of its seq_lens[b] tokens (token_start [batch+1] as zf_map_tokens writes it; it must not
+ *                 decrease).  Rows before token_start[0] and from token_start[batch] on are not read, and theirs
+ *                 of out and lse are left as they are.
+ *   page_table [batch][max_pages_per_req], seq_lens [batch]: as for zf_q4_decode_attn.
+ *   A row at position p sees positions 0 .. p, with window > 0 only the last `window` of them (p itself among
+ *   them).  Its scores are s_j = softmax_scale * q.k_j; with softcap > 0 (1e-3 .. 1e6) softcap * tanh(s_j /
+ *   softcap); with slopes (NULL or [num_q_heads] float32, by query head) plus slopes[h] * (j - p).
+ *   out [rows][num_q_heads][128] BF16, lse [rows][num_q_heads] float32: the logarithm of the sum of exp(scores).  A
+ *   row that sees nothing (a request with fewer tokens than new ones) gets out = 0 and lse = -inf.
+ *   K and V are multiplied as the exact stored values; a query row's values enter as for zf_q4_decode_attn; scores
+ *   and sums are float32; the softmax weights enter the product as fp16 (off by at most 2^-12 of the weight, or
+ *   2^-33 of the row's largest one); the result is rounded once more, to BF16.  A NaN or an infinity in a query row
+ *   stays in that row.
+ *   A token_start entry that decreases or passes rows leaves that request out, a seq_len out of range is clamped;
+ *   both set ZF_DEV_BAD_SEQ_LEN.  A page id out of range sets ZF_DEV_BAD_PAGE_ID and its tokens are not seen.
+ *   A wait that takes 2 s gives up: it sets ZF_DEV_TIMEOUT, and out and lse of that call mean nothing.
+ *   batch <= ZF_MAX_BATCH.  rows == 0 or batch == 0 is a no-op.  Two kernels (attention, then the joining of units
+ *   split over CTAs), launched with programmatic stream serialisation; results are deterministic (no atomics).
+ */
+zf_status zf_q4_chunk_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t rows, int32_t batch,
+                           int32_t num_q_heads, const int32_t* token_start, const int32_t* page_table,
+                           int32_t max_pages_per_req, const int32_t* seq_lens, float softmax_scale, int32_t window,
+                           float softcap, const float* slopes, uint16_t* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 /*
  * zf_map_tokens — block tables and slot maps on the GPU: gives every request's new tokens their
  * places, taking pages from a free list, without a host round trip (zf_kv below does the same
