@@ -25,6 +25,7 @@ ENCODE_FORCE_RAW = 1
 DEV_BAD_PAGE_ID, DEV_BAD_RAW_SLOT, DEV_BAD_N_VALID = 0x1, 0x2, 0x4
 DEV_BAD_SEQ_LEN, DEV_BAD_DIR, DEV_TIMEOUT, DEV_BAD_SLOT = 0x8, 0x10, 0x20, 0x40
 DEV_NOT_FINITE, DEV_CAPACITY, DEV_BAD_DRAFT, DEV_BAD_PROBS = 0x80, 0x100, 0x200, 0x400
+DEV_BAD_FORK = 0x800
 Q4_RECORD_BYTES = 2304
 
 _c_int32, _c_void_p, _c_size_t, _c_float = ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
@@ -110,6 +111,17 @@ SIGNATURES = {
     "zf_map_tokens": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_void_p, _c_int32, _c_void_p, _c_void_p]),
+    "zf_fork_requests": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_int32,
+                                    _c_void_p, _c_void_p, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_void_p, _c_void_p]),
+    "zf_q4_copy_pages": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_void_p, _c_int32, _c_void_p]),
+    "zf_release_requests_workspace_size": (_c_size_t, [_c_int32]),
+    "zf_release_requests": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                       _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t,
+                                       _c_void_p]),
+    "zf_compact_pages_workspace_size": (_c_size_t, [_c_int32]),
+    "zf_compact_pages": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
     "zf_verify_drafts": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                     _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
     "zf_verify_mapped_drafts": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
@@ -852,6 +864,167 @@ def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_draft
     if code:
         _check("zf_verify_drafts" if token_start is None else "zf_verify_mapped_drafts", code)
     return accepted, tokens
+
+
+# ------------------------------------------------------------ sharing, freeing and moving pages
+class Fork(NamedTuple):
+    """What zf_fork_requests gives: the requests' lengths and pages after the call, the position in the free list, and
+    per entry the page to copy and where to (-1: none)."""
+    seq_lens: torch.Tensor
+    pages_held: torch.Tensor
+    free_pos: torch.Tensor
+    copy_src: torch.Tensor
+    copy_dst: torch.Tensor
+
+
+class Release(NamedTuple):
+    """What zf_release_requests gives: lengths and pages after the call, and the position in the free list."""
+    seq_lens: torch.Tensor
+    pages_held: torch.Tensor
+    free_pos: torch.Tensor
+
+
+class Compaction(NamedTuple):
+    """What zf_compact_pages gives: the renumbered page table, a free list over the whole pool and the position in it
+    (the number of pages in use), and the pages to copy and where to (-1 past the last)."""
+    page_table: torch.Tensor
+    free_pages: torch.Tensor
+    free_pos: torch.Tensor
+    copy_src: torch.Tensor
+    copy_dst: torch.Tensor
+
+
+def _table_2d(page_table):
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [batch][max_pages] tensor")
+    return page_table.shape
+
+
+def _list_1d(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError(f"{name} must be a one-dimensional tensor")
+    return t.shape
+
+
+def _outputs(kind, out, shapes, dev):
+    """The int32 outputs of a call as `kind`: made here (in one allocation), or `out` checked."""
+    if out is not None:
+        return kind(*(_tensor(t, "out." + name, _I32, dev, s, write=True) for t, name, s in zip(out, kind._fields, shapes)))
+    sizes = [math.prod(s) for s in shapes]
+    return kind(*(t.view(s) for t, s in zip(torch.empty(sum(sizes), dtype=torch.int32, device=dev)
+                                            .unsafe_split_with_sizes(sizes), shapes)))
+
+
+def _status_ptr(status, dev):
+    return None if status is None else _tensor(status, "status", _I32, dev, (1,), write=True).data_ptr()
+
+
+def _workspace(workspace, nbytes, dev):
+    if workspace is None:
+        return new_workspace(nbytes, dev)
+    return _tensor(workspace, "workspace", (getattr(workspace, "dtype", None),), dev, getattr(workspace, "shape", None),
+                   write=True)
+
+
+@_on_stream
+def fork_requests(page_table, seq_lens, pages_held, src, dst, free_pages, free_pos, page_size, out=None, status=None) -> Fork:
+    """zf_fork_requests: rows dst[i] of page_table [B][max_pages] (empty ones) go on from rows src[i]: full pages are
+    shared, a last page that is not full gets a page from free_pages[free_pos ..].  seq_lens, pages_held [B], src,
+    dst [n], free_pages [F], free_pos [1], all int32 on the device; page_table is written in place.  Then, per layer:
+    q4_copy_pages(cache, fork.copy_src, fork.copy_dst).  out: a Fork to write into (its seq_lens, pages_held and
+    free_pos may be the arguments themselves); status: an int32 device word."""
+    B, max_pages = _table_2d(page_table)
+    dev = page_table.device
+    page_table = _tensor(page_table, "page_table", _I32, dev, (B, max_pages), write=True)
+    seq_lens = _tensor(seq_lens, "seq_lens", _I32, dev, (B,))
+    pages_held = _tensor(pages_held, "pages_held", _I32, dev, (B,))
+    src = _tensor(src, "src", _I32, dev, _list_1d(src, "src"))
+    n = src.shape[0]
+    dst = _tensor(dst, "dst", _I32, dev, (n,))
+    free_pages = _tensor(free_pages, "free_pages", _I32, dev, _list_1d(free_pages, "free_pages"))
+    free_pos = _tensor(free_pos, "free_pos", _I32, dev, (1,))
+    word = _status_ptr(status, dev)
+    s = _launch_stream(dev)
+    out = _outputs(Fork, out, ((B,), (B,), (1,), (n,), (n,)), dev)
+    code = lib().zf_fork_requests(B, page_size, max_pages, seq_lens.data_ptr(), pages_held.data_ptr(), src.data_ptr(),
+                                  dst.data_ptr(), n, page_table.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
+                                  free_pos.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
+                                  out[3].data_ptr(), out[4].data_ptr(), word, s)
+    if code:
+        _check("zf_fork_requests", code)
+    return out
+
+
+@_on_stream
+def q4_copy_pages(cache: Q4Cache, src, dst):
+    """zf_q4_copy_pages: pages src[i] to dst[i], int32 on the device (both -1: skipped); no page may be a destination
+    twice, nor a source and a destination."""
+    src = _tensor(src, "src", _I32, cache._device, _list_1d(src, "src"))
+    dst = _tensor(dst, "dst", _I32, cache._device, src.shape)
+    s = _launch_stream(cache._device)
+    code = lib().zf_q4_copy_pages(cache._ref, src.data_ptr(), dst.data_ptr(), src.shape[0], s)
+    if code:
+        _check("zf_q4_copy_pages", code)
+
+
+@_on_stream
+def release_requests(page_table, seq_lens, pages_held, release, free_pages, free_pos, num_pages, out=None, status=None,
+                     workspace=None) -> Release:
+    """zf_release_requests: the rows with release[b] != 0 give back the pages that no other row holds, into
+    free_pages[.. free_pos - 1] (written in place).  page_table [B][max_pages], seq_lens, pages_held, release [B],
+    free_pages [F], free_pos [1], all int32 on the device.  out: a Release to write into (its tensors may be the
+    arguments); status: an int32 device word; workspace: see release_workspace_size."""
+    B, max_pages = _table_2d(page_table)
+    dev = page_table.device
+    page_table = _tensor(page_table, "page_table", _I32, dev, (B, max_pages))
+    seq_lens = _tensor(seq_lens, "seq_lens", _I32, dev, (B,))
+    pages_held = _tensor(pages_held, "pages_held", _I32, dev, (B,))
+    release = _tensor(release, "release", _I32, dev, (B,))
+    free_pages = _tensor(free_pages, "free_pages", _I32, dev, _list_1d(free_pages, "free_pages"), write=True)
+    free_pos = _tensor(free_pos, "free_pos", _I32, dev, (1,))
+    word = _status_ptr(status, dev)
+    s = _launch_stream(dev)
+    out = _outputs(Release, out, ((B,), (B,), (1,)), dev)
+    workspace = _workspace(workspace, release_workspace_size(num_pages), dev)
+    code = lib().zf_release_requests(B, max_pages, num_pages, page_table.data_ptr(), seq_lens.data_ptr(),
+                                     pages_held.data_ptr(), release.data_ptr(), free_pages.data_ptr(),
+                                     free_pages.shape[0], free_pos.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
+                                     out[2].data_ptr(), word, workspace.data_ptr(), workspace.nbytes, s)
+    if code:
+        _check("zf_release_requests", code)
+    return out
+
+
+@_on_stream
+def compact_pages(page_table, pages_held, num_pages, out=None, status=None, workspace=None) -> Compaction:
+    """zf_compact_pages: the pages in use, n of them, get the ids 0 .. n - 1.  page_table [B][max_pages], pages_held
+    [B], int32 on the device.  Then, per layer: q4_copy_pages(cache, c.copy_src, c.copy_dst).  out: a Compaction to
+    write into (its page_table may be the argument); status: an int32 device word; workspace: see
+    compact_workspace_size."""
+    B, max_pages = _table_2d(page_table)
+    dev = page_table.device
+    page_table = _tensor(page_table, "page_table", _I32, dev, (B, max_pages))
+    pages_held = _tensor(pages_held, "pages_held", _I32, dev, (B,))
+    if num_pages < 0:
+        raise ValueError("num_pages must not be negative")
+    word = _status_ptr(status, dev)
+    s = _launch_stream(dev)
+    out = _outputs(Compaction, out, ((B, max_pages), (num_pages,), (1,), (num_pages // 2,), (num_pages // 2,)), dev)
+    workspace = _workspace(workspace, compact_workspace_size(num_pages), dev)
+    code = lib().zf_compact_pages(B, max_pages, num_pages, page_table.data_ptr(), pages_held.data_ptr(), out[0].data_ptr(),
+                                  out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), word,
+                                  workspace.data_ptr(), workspace.nbytes, s)
+    if code:
+        _check("zf_compact_pages", code)
+    return out
+
+
+def release_workspace_size(num_pages) -> int:
+    return int(lib().zf_release_requests_workspace_size(num_pages))
+
+
+def compact_workspace_size(num_pages) -> int:
+    return int(lib().zf_compact_pages_workspace_size(num_pages))
 
 
 # --------------------------------------------------------------------------------- page manager

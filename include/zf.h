@@ -80,9 +80,12 @@ typedef int32_t zf_status;
 #define ZF_DEV_TIMEOUT 0x20            /* a shared-memory pipeline wait gave up */
 #define ZF_DEV_BAD_SLOT 0x40           /* zf_validate_pages: a compressed slot's metadata is malformed */
 #define ZF_DEV_NOT_FINITE 0x80         /* zf_q4_write_tokens: a NaN or an infinity was stored (as 0 / the largest value) */
-#define ZF_DEV_CAPACITY 0x100          /* zf_map_tokens: too few free pages or token entries; nothing was mapped */
+#define ZF_DEV_CAPACITY 0x100          /* zf_map_tokens: too few free pages or token entries; nothing was mapped
+                                          (zf_fork_requests, zf_release_requests: nothing was forked, freed) */
 #define ZF_DEV_BAD_DRAFT 0x200         /* zf_verify_drafts: a draft token or count out of range */
-#define ZF_DEV_BAD_PROBS 0x400         /* zf_verify_drafts: a row with no positive or no finite sum to sample from */
+#define ZF_DEV_BAD_PROBS 0x400         /* zf_verify_drafts: a row with no positive or no finite sum to sample from;
+                                          zf_sample_tokens: a row without a finite largest logit, or a bad parameter */
+#define ZF_DEV_BAD_FORK 0x800          /* zf_fork_requests: a source or a destination that cannot be used */
 
 #define ZF_HEAD_DIM 128
 #define ZF_BLOCK_TOKENS 16
@@ -543,6 +546,78 @@ zf_status zf_map_tokens(int32_t batch, int32_t page_size, int32_t max_pages_per_
                         int32_t* new_seq_lens, int32_t* new_pages_held, int32_t* new_free_pos,
                         int32_t* token_start, int32_t* page_ids, int32_t* positions, int32_t* seq_positions,
                         int32_t max_tokens, int32_t* status, void* stream);
+
+/*
+ * zf_fork_requests — requests that go on from another's tokens (several answers to a prompt, a common prefix): each
+ * destination row gets the source's full pages, shared, and a page of its own for a last page that is not full.
+ * No token is moved: zf_q4_copy_pages with copy_src and copy_dst, once per layer, copies those last pages.  Pages
+ * held by several rows are counted nowhere: zf_release_requests and zf_compact_pages read who holds a page from the
+ * page table.
+ *   seq_lens, pages_held [batch], page_table [batch][max_pages_per_req]: as for zf_map_tokens.  Of the table only
+ *                 the destinations' rows are written.
+ *   src, dst [n]: rows.  A source may be named several times.  A destination must be empty (seq_len and pages_held
+ *                 0) and must not be its source; the first entry that names a destination has it.  An entry that
+ *                 breaks this, or whose source's length does not fit its pages, is left out and sets
+ *                 ZF_DEV_BAD_FORK.
+ *   free_pages [num_free], free_pos [1]: as for zf_map_tokens; forks take pages in the order of the list.  When
+ *                 they do not suffice nothing is forked, and ZF_DEV_CAPACITY is set.
+ *   Outputs: new_seq_lens, new_pages_held [batch], new_free_pos [1] (each may be the same array as its input);
+ *   copy_src, copy_dst [n]: the pages to copy, -1 where there is none.
+ *   Fork between steps: a request shortened later (zf_verify_drafts) below the length it had when it was forked
+ *   would write into shared pages.
+ *   status: optional device word.  batch, n <= ZF_MAX_BATCH; max_pages_per_req * page_size < 2^31.  One kernel,
+ *   launched with programmatic stream serialisation.
+ */
+zf_status zf_fork_requests(int32_t batch, int32_t page_size, int32_t max_pages_per_req, const int32_t* seq_lens,
+                           const int32_t* pages_held, const int32_t* src, const int32_t* dst, int32_t n,
+                           int32_t* page_table, const int32_t* free_pages, int32_t num_free, const int32_t* free_pos,
+                           int32_t* new_seq_lens, int32_t* new_pages_held, int32_t* new_free_pos, int32_t* copy_src,
+                           int32_t* copy_dst, int32_t* status, void* stream);
+
+/* zf_q4_copy_pages — copies pages src[i] to dst[i] (all kv heads) for i < n.  Entries with both -1 are skipped; a page
+ * id out of range sets ZF_DEV_BAD_PAGE_ID and its entry is skipped.  A page must not be a destination twice, nor a
+ * source and a destination of different entries. */
+zf_status zf_q4_copy_pages(const zf_q4_cache* cache, const int32_t* src, const int32_t* dst, int32_t n, void* stream);
+
+/*
+ * zf_release_requests — gives finished requests' pages back to the free list.
+ *   release [batch]: rows to release (not 0).  A page that one of the other rows holds too stays in use; one that
+ *                 several released rows hold is freed once.
+ *   free_pages [num_free], free_pos [1]: as for zf_map_tokens.  With k pages freed, entries free_pos - k .. free_pos
+ *                 - 1 are written, in the order in which rows first mention the pages, and new_free_pos is free_pos
+ *                 - k.  (A list with an entry for every page of the pool has room for all.)  When k is above
+ *                 free_pos nothing is released, and ZF_DEV_CAPACITY is set.
+ *   Outputs: new_seq_lens, new_pages_held [batch] (0 for released rows), new_free_pos [1], each may be the same array
+ *   as its input.  The page table is not written.
+ *   A page id out of range sets ZF_DEV_BAD_PAGE_ID and is not freed; a pages_held out of range is clamped and sets
+ *   ZF_DEV_BAD_SEQ_LEN.  status: optional device word.  workspace: any contents, 16-byte aligned.  batch <=
+ *   ZF_MAX_BATCH, batch * max_pages_per_req <= 2^30.  One kernel, launched with programmatic stream serialisation.
+ */
+size_t zf_release_requests_workspace_size(int32_t num_pages);
+zf_status zf_release_requests(int32_t batch, int32_t max_pages_per_req, int32_t num_pages, const int32_t* page_table,
+                              const int32_t* seq_lens, const int32_t* pages_held, const int32_t* release,
+                              int32_t* free_pages, int32_t num_free, const int32_t* free_pos, int32_t* new_seq_lens,
+                              int32_t* new_pages_held, int32_t* new_free_pos, int32_t* status, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * zf_compact_pages — renumbers the pages in use, n of them, to 0 .. n-1, so that the rest of the pool is one piece:
+ * pages with ids below n stay, the others move to the unused ids below n, both in ascending order.  No token is
+ * moved: zf_q4_copy_pages with copy_src and copy_dst, once per layer, does that (before anything is written to a
+ * page of the new free list).
+ *   page_table [batch][max_pages_per_req], pages_held [batch]: a row's first pages_held entries are in use; a page
+ *                 may be held by several rows.
+ *   Outputs: new_page_table (may be page_table; entries past those held are copied); free_pages [num_pages]: entry
+ *   i is i from n on, -1 before; free_pos [1]: n; copy_src, copy_dst [num_pages / 2]: the moves, then -1.
+ *   A page id out of range sets ZF_DEV_BAD_PAGE_ID and stays as it is; a pages_held out of range is clamped and sets
+ *   ZF_DEV_BAD_SEQ_LEN.  status: optional device word.  workspace: any contents, 16-byte aligned.  batch <=
+ *   ZF_MAX_BATCH.  One kernel, launched with programmatic stream serialisation.
+ */
+size_t zf_compact_pages_workspace_size(int32_t num_pages);
+zf_status zf_compact_pages(int32_t batch, int32_t max_pages_per_req, int32_t num_pages, const int32_t* page_table,
+                           const int32_t* pages_held, int32_t* new_page_table, int32_t* free_pages, int32_t* free_pos,
+                           int32_t* copy_src, int32_t* copy_dst, int32_t* status, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /*
  * zf_verify_drafts — verification of drafted tokens against the target's probabilities, from given
