@@ -122,6 +122,8 @@ SIGNATURES = {
     "zf_compact_pages_workspace_size": (_c_size_t, [_c_int32]),
     "zf_compact_pages": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                     _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
+    "zf_sample_tokens": (_c_int32, [_c_int32, _c_int32, _c_void_p, _c_int32, ctypes.c_int64, _c_void_p, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
     "zf_verify_drafts": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                     _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
     "zf_verify_mapped_drafts": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
@@ -864,6 +866,57 @@ def verify_drafts(target_probs, draft_tokens, uniform, draft_probs=None, n_draft
     if code:
         _check("zf_verify_drafts" if token_start is None else "zf_verify_mapped_drafts", code)
     return accepted, tokens
+
+
+# ------------------------------------------------------------------------------------- sampling
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+@_on_stream
+def sample_tokens(logits, uniform=None, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, tokens=None,
+                  status=None):
+    """zf_sample_tokens: logits [R][V] float32, bfloat16 or float16 (rows may be a stride apart); uniform [R] float32 in
+    [0, 1); temperature, top_p, min_p [R] float32 and top_k [R] int32, each None for none.  Returns tokens [R] int32
+    (None when uniform is None).  probs [R][V] float32 is filled with the distribution sampled from; uniform may be
+    None when only that is wanted.  tokens: a tensor to write into; status: an int32 device word."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a [rows][vocab] tensor")
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None:
+        raise ValueError(f"logits: dtype {logits.dtype}, expected torch.float32, torch.bfloat16 or torch.float16")
+    R, V = logits.shape
+    dev = logits.device
+    if logits.stride(1) != 1 or logits.stride(0) < V:
+        logits = logits.contiguous()
+    rows = (R,)
+    u = t = k = p = m = out = dist = word = None
+    if uniform is not None:
+        u = (uniform := _tensor(uniform, "uniform", _F32, dev, rows)).data_ptr()
+    elif tokens is not None:
+        raise ValueError("tokens need uniform")
+    elif probs is None:
+        raise ValueError("uniform, probs or both are needed")
+    if temperature is not None:
+        t = (temperature := _tensor(temperature, "temperature", _F32, dev, rows)).data_ptr()
+    if top_k is not None:
+        k = (top_k := _tensor(top_k, "top_k", _I32, dev, rows)).data_ptr()
+    if top_p is not None:
+        p = (top_p := _tensor(top_p, "top_p", _F32, dev, rows)).data_ptr()
+    if min_p is not None:
+        m = (min_p := _tensor(min_p, "min_p", _F32, dev, rows)).data_ptr()
+    if probs is not None:
+        dist = _tensor(probs, "probs", _F32, dev, (R, V), write=True).data_ptr()
+    if status is not None:
+        word = _tensor(status, "status", _I32, dev, (1,), write=True).data_ptr()
+    s = _launch_stream(dev)
+    if uniform is not None:
+        tokens = torch.empty(R, dtype=torch.int32, device=dev) if tokens is None else \
+            _tensor(tokens, "tokens", _I32, dev, rows, write=True)
+        out = tokens.data_ptr()
+    code = lib().zf_sample_tokens(R, V, logits.data_ptr(), kind, max(logits.stride(0), V), u, t, k, p, m, out, dist, word, s)
+    if code:
+        _check("zf_sample_tokens", code)
+    return tokens
 
 
 # ------------------------------------------------------------ sharing, freeing and moving pages

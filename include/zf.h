@@ -103,6 +103,12 @@ typedef int32_t zf_status;
 #define ZF_Q4_RECORD_BYTES 2304        /* 4-bit cache: 16 tokens of one (page, kv head), K and V */
 #define ZF_MAX_VOCAB (1 << 24)         /* zf_verify_drafts */
 
+#define ZF_MAX_SAMPLE_VOCAB (1 << 21)  /* zf_sample_tokens */
+#define ZF_MAX_SAMPLE_ROWS (1 << 20)
+#define ZF_F32 0                       /* types of zf_sample_tokens' logits */
+#define ZF_BF16 1
+#define ZF_F16 2
+
 #define ZF_ENCODE_FORCE_RAW 1          /* zf_encode_pages flag: store every page raw */
 
 /* One layer's cache.  Only the pointers a call uses must be valid for that call. */
@@ -618,6 +624,30 @@ zf_status zf_compact_pages(int32_t batch, int32_t max_pages_per_req, int32_t num
                            const int32_t* pages_held, int32_t* new_page_table, int32_t* free_pages, int32_t* free_pos,
                            int32_t* copy_src, int32_t* copy_dst, int32_t* status, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/*
+ * zf_sample_tokens — a token per row of logits, and the distribution it is drawn from (what zf_verify_drafts takes as
+ * target_probs and draft_probs).
+ *   logits [rows][vocab], row r at entry r * row_stride (>= vocab); logits_type ZF_F32, ZF_BF16 or ZF_F16.  A NaN
+ *                 counts as -inf.
+ *   temperature, top_k, top_p, min_p [rows], each NULL for none.  w_i = exp((x_i - max) / temperature); a temperature
+ *                 below 1e-6 takes the largest logit, the first of equal ones.  In the order of (x descending, index
+ *                 ascending) these are kept: the first top_k (0: all), of them those with w_i >= min_p (in [0, 1]),
+ *                 of them the shortest run from the front whose sum reaches top_p (1 or more: all) times theirs; at
+ *                 least the first.
+ *   uniform [rows] in [0, 1), tokens [rows] (both or neither): the first index, in index order, at which the running
+ *                 sum of kept weights is above uniform times their sum.
+ *   probs [rows][vocab] float32 or NULL: kept weights over their sum, 0 elsewhere.  (tokens or probs or both.)
+ *   Weights are taken as integers times 2^-42, off by at most 2^-30 of themselves or 2^-43, and summed exactly, so
+ *   neither a choice nor a probability depends on how the work is split.
+ *   A row without a finite largest logit, or with a parameter that is NaN, negative or (temperature) infinite, a
+ *   min_p above 1 or a uniform outside [0, 1) gives token -1 and probabilities 0 and sets ZF_DEV_BAD_PROBS.
+ *   status: optional device word.  rows <= ZF_MAX_SAMPLE_ROWS, vocab <= ZF_MAX_SAMPLE_VOCAB.  One kernel, launched
+ *   with programmatic stream serialisation.
+ */
+zf_status zf_sample_tokens(int32_t rows, int32_t vocab, const void* logits, int32_t logits_type, int64_t row_stride,
+                           const float* uniform, const float* temperature, const int32_t* top_k, const float* top_p,
+                           const float* min_p, int32_t* tokens, float* probs, int32_t* status, void* stream);
 
 /*
  * zf_verify_drafts — verification of drafted tokens against the target's probabilities, from given
