@@ -29,8 +29,8 @@
 // Every wait is bounded; one that gives up sets ZF_DEV_TIMEOUT and the CTA winds down.
 //
 // Numbers.  Scores, maxima and sums are fp32.  The weights enter the second product as fp16, 2^7 times their size
-// relative to the running maximum (11 bits down to 2^-21 of it, then steps of 2^-32): half of BF16's rounding error,
-// to which the result is rounded at the end.
+// relative to the running maximum (off by at most 2^-11 of themselves down to 2^-21 of it, then by 2^-32 of it): an
+// eighth of the error of the result's own rounding to BF16.
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>

@@ -151,7 +151,7 @@ __device__ __forceinline__ unsigned long long fixed(const Weight& w) {
   return s > 43 ? 0ull : (v + (1ull << (s - 1))) >> s;
 }
 __device__ __forceinline__ float as_float(const Weight& w) {
-  return w.shift < -100 ? 0.f : __uint2float_rn(w.m) * __int_as_float((127 - 31 + w.shift) << 23);
+  return w.shift < -126 ? 0.f : __uint2float_rn(w.m) * 0x1p-31f * __int_as_float((127 + w.shift) << 23);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {

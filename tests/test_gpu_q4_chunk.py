@@ -1,0 +1,344 @@
+"""Attention of a ragged batch of new tokens over the 4-bit cache, against the float64 oracle with bounds from the
+number of roundings."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import zf_serve_oracle as R
+from oracle import zf_step_oracle as S
+from tests import helpers as H
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def zf():
+    return H.zf_module()
+
+
+def f64(x):
+    return S.bf16_to_f64(H.np_bits(x.view(torch.int16)))
+
+
+class Case:
+    """Requests of given lengths and new tokens over a shuffled pool; keys with strong channels."""
+
+    def __init__(self, zf, page, hkv, group, lens, new, seed=0, scales=(1.0, 1.0), lead=0, behind=0, spread=1.0):
+        g = torch.Generator().manual_seed(seed)
+        self.hkv, self.hq, self.page, self.lens, self.new, self.lead = hkv, hkv * group, page, lens, new, lead
+        count = [-(-L // page) for L in lens]
+        pool, max_pages = sum(count) + 2, max(count + [1])
+        perm = torch.randperm(pool, generator=g).tolist()
+        table, at = np.full((len(lens), max_pages), -1, np.int32), 0
+        for b, c in enumerate(count):
+            table[b, :c] = perm[at:at + c]
+            at += c
+        self.table = torch.from_numpy(table)
+        self.cache = zf.Q4Cache(pool, hkv, page, k_scale=scales[0], v_scale=scales[1])
+        self.k, self.v = [], []
+        s = torch.ones(128) * spread
+        s[:4] *= 8
+        for b, L in enumerate(lens):
+            k = (torch.randn(L, hkv, 128, generator=g) * s * scales[0]).to(torch.bfloat16)
+            v = (torch.randn(L, hkv, 128, generator=g) * scales[1]).to(torch.bfloat16)
+            ids = [int(table[b, p // page]) for p in range(L)]
+            pos = [p % page for p in range(L)]
+            zf.q4_write_tokens(self.cache, k.cuda(), v.cuda(), ids, pos)
+            raw = zf.Q4Cache(pool, hkv, page, records=self.cache.records)            # scale 1: exact in BF16
+            rk, rv = zf.q4_read_tokens(raw, ids, pos)
+            self.k.append(f64(rk) * np.float32(scales[0]).astype(np.float64))
+            self.v.append(f64(rv) * np.float32(scales[1]).astype(np.float64))
+        self.start = np.cumsum([lead] + list(new)).astype(np.int32)
+        self.rows = int(self.start[-1]) + behind
+        self.q = torch.randn(self.rows, self.hq, 128, generator=g).to(torch.bfloat16)
+
+    def args(self):
+        return (self.cache, self.q.cuda(), self.table.cuda(), torch.tensor(self.lens, dtype=torch.int32).cuda(),
+                torch.from_numpy(self.start).cuda())
+
+    def check(self, out, lse, scale=None, window=0, softcap=0.0, slopes=None, requests=None, seen=None):
+        scale = 1 / math.sqrt(128) if scale is None else scale
+        out, lse = f64(out), lse.double().cpu().numpy()
+        for b in range(len(self.lens)) if requests is None else requests:
+            a, e = self.start[b], self.start[b + 1]
+            want, wl, wv, sv, mag = R.chunk_attention(f64(self.q[a:e]), self.k[b], self.v[b], self.lens[b] - self.new[b],
+                                                      scale, window, softcap, slopes, None if seen is None else seen[b])
+            # a score: up to 128 additions of products, each off by 2^-23 of their magnitudes' sum (the tensor core
+            # truncates), a few roundings more, in log2 units and back; the cap's tanh; the slopes' products
+            far = 0 if slopes is None else np.abs(slopes).max() * min(self.lens[b], window or self.lens[b])
+            off = mag * 2.0 ** -16 + 2.0 ** -20 + softcap * 2.0 ** -20 + far * 2.0 ** -22
+            # weights: fp16 (2^-11, or 2^-32 of the row's largest) and a score's error twice (numerator, sum)
+            tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * off + 2.0 ** -18)[..., None] * wv + 2.0 ** -32 * sv + 1e-30
+            assert (np.abs(out[a:e] - want) <= tol).all(), (b, np.abs(out[a:e] - want).max(), (np.abs(out[a:e] - want) / tol).max())
+            none = np.isinf(wl)
+            assert (lse[a:e][none] == -np.inf).all() and not out[a:e][none].any()
+            assert (np.abs(lse[a:e][~none] - wl[~none]) <= off[~none] + 2.0 ** -20 * (1 + np.abs(wl[~none]))).all()
+
+
+SHAPES = [
+    (16, 1, 1, [1], [1]),                                            # one token over itself
+    (16, 2, 4, [200, 37, 0, 129, 16], [64, 37, 0, 1, 16]),           # a last tile of every kind
+    (48, 1, 7, [127, 128, 129, 255, 256, 257], [127, 1, 3, 36, 37, 19]),   # rows 889, 7, 21, 252, 259, 133
+    (64, 2, 8, [300, 16], [16, 16]),                                 # exactly 128 rows
+    (32, 1, 3, [500, 90], [86, 43]),                                 # 258 and 129 rows
+    (128, 3, 5, [700], [13]),
+    (16, 1, 300, [40], [2]),                                         # one token's rows span units
+    (16, 4, 2, [5, 3, 140], [9, 4, 150]),                            # more new tokens than tokens: rows that see nothing
+]
+
+
+@pytest.mark.parametrize("page,hkv,group,lens,new", SHAPES)
+@pytest.mark.parametrize("mod", [{}, dict(window=1), dict(window=5), dict(window=130), dict(softcap=20.0), dict(slopes=True),
+                                 dict(window=64, softcap=5.0, slopes=True)])
+def test_against_the_oracle(zf, page, hkv, group, lens, new, mod):
+    c = Case(zf, page, hkv, group, lens, new, seed=len(lens) + hkv)
+    mod = dict(mod)
+    if mod.get("slopes"):
+        mod["slopes"] = np.float32(2.0) ** -np.linspace(1, 8, c.hq, dtype=np.float32) * np.where(np.arange(c.hq) % 5, 1, -0.1).astype(np.float32)
+    kw = {**mod, "slopes": torch.from_numpy(mod["slopes"]).cuda()} if "slopes" in mod else mod
+    out, lse = zf.q4_chunk_attn(*c.args(), **kw)
+    c.check(out, lse, **mod)
+    assert c.cache.status_word() == 0
+
+
+@pytest.mark.parametrize("scale,scales", [(0.3, (1.0, 1.0)), (-0.08, (1.0, 1.0)), (0.08, (0.37, 5.0)), (0.0, (1.0, 1.0))])
+def test_scales(zf, scale, scales):
+    c = Case(zf, 16, 2, 4, [260, 31], [70, 2], seed=5, scales=scales)
+    out, lse = zf.q4_chunk_attn(*c.args(), scale=scale)
+    c.check(out, lse, scale=scale)
+
+
+def test_large_scores_keep_their_weights(zf):
+    """Scores beyond 2^22, where floats lie further apart than exponents: the largest one has the weight."""
+    c = Case(zf, 16, 1, 2, [300], [40], seed=9, spread=50.0)
+    for scale in (3e3, 3e5, -3e5):
+        out, lse = zf.q4_chunk_attn(*c.args(), scale=scale)
+        q, k, v = f64(c.q), c.k[0], c.v[0]
+        for t in range(40):
+            for h in range(2):
+                x = scale * (k[:261 + t, 0] @ q[t, h])
+                order = np.argsort(x)
+                gap = x[order[-1]] - x[order[-2]]
+                assert np.isfinite(lse[t, h].item())
+                if gap > 2.0 ** -15 * np.abs(x).max() + 40:          # one token has it all
+                    want = v[order[-1], 0]
+                    assert (np.abs(f64(out[t, h]) - want) <= 2.0 ** -7 * np.abs(want) + 1e-12).all()
+
+
+def test_rows_of_no_request_are_left_alone(zf):
+    c = Case(zf, 16, 2, 4, [50, 200], [5, 40], seed=2, lead=3, behind=6)
+    out = torch.full((c.rows, c.hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.rows, c.hq), 7.0, device="cuda")
+    o, l = zf.q4_chunk_attn(*c.args(), out=out, lse=lse)
+    assert o.data_ptr() == out.data_ptr() and l.data_ptr() == lse.data_ptr()
+    c.check(out, lse)
+    for part in (slice(0, 3), slice(48, 54)):
+        assert (out[part] == 7).all() and (lse[part] == 7).all()
+
+
+def test_bad_pages_are_skipped(zf):
+    c = Case(zf, 16, 2, 4, [200, 150], [10, 150], seed=4)
+    seen = [np.ones(200, bool), np.ones(150, bool)]
+    c.table[0, 3], c.table[1, 0] = 10000, -5
+    seen[0][48:64], seen[1][:16] = False, False
+    out, lse = zf.q4_chunk_attn(*c.args())
+    c.check(out, lse, seen=seen)                                     # rows 0 .. 15 of the second see nothing
+    assert c.cache.status_word() == zf.DEV_BAD_PAGE_ID
+
+
+def test_bad_starts_and_lengths(zf):
+    c = Case(zf, 16, 1, 4, [60, 40, 80, 30], [6, 5, 7, 4], seed=6)
+    cache, q, table, lens, start = c.args()
+    out, lse = torch.full((22, 4, 128), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((22, 4), 7.0, device="cuda")
+    bad = start.clone()
+    bad[4] = 23                                                      # the last request passes the rows
+    zf.q4_chunk_attn(cache, q, table, lens, bad, out=out, lse=lse)
+    c.check(out, lse, requests=[0, 1, 2])
+    assert (out[18:] == 7).all() and cache.status_word() == zf.DEV_BAD_SEQ_LEN
+    cache.status.zero_()
+    bad = start.clone()
+    bad[2] = 2                                                       # request 1 ends before it starts, request 2 begins there
+    zf.q4_chunk_attn(cache, q, table, lens, bad)
+    assert cache.status_word() == zf.DEV_BAD_SEQ_LEN
+    cache.status.zero_()
+    long = lens.clone()
+    long[1], long[3] = -3, table.shape[1] * 16 + 1                   # clamped: nothing, and the whole row of pages
+    out, lse = zf.q4_chunk_attn(cache, q, table, long, start)
+    c.check(out, lse, requests=[0, 2])
+    assert not out[6:11].any() and (lse[6:11] == -math.inf).all()
+    assert cache.status_word() & zf.DEV_BAD_SEQ_LEN
+
+
+def test_a_nan_or_infinity_stays_in_its_row(zf):
+    c = Case(zf, 16, 1, 4, [300, 20], [50, 3], seed=8)
+    want, wl = zf.q4_chunk_attn(*c.args())
+    q = c.q.clone()
+    q[7, 2, 5], q[20, 0, 100], q[51, 3, 0] = float("nan"), float("inf"), -float("inf")
+    cache, _, table, lens, start = c.args()
+    out, lse = zf.q4_chunk_attn(cache, q.cuda(), table, lens, start)
+    hit = torch.zeros(53, 4, dtype=torch.bool)
+    hit[7, 2] = hit[20, 0] = hit[51, 3] = True
+    assert torch.isnan(lse.cpu()[hit]).all() and torch.isnan(out.cpu()[hit]).all()
+    assert torch.equal(out.cpu()[~hit], want.cpu()[~hit]) and torch.equal(lse.cpu()[~hit], wl.cpu()[~hit])
+
+
+def test_small_and_large_query_rows(zf):
+    """Rows of very different size in one call: each has a power of two of its own."""
+    c = Case(zf, 16, 1, 4, [200], [40], seed=11)
+    f = torch.exp2(torch.randint(-60, 3, (40, 4, 1), generator=torch.Generator().manual_seed(1)).float())
+    c.q = (c.q.float() * f).to(torch.bfloat16)
+    c.q[3] = 0
+    out, lse = zf.q4_chunk_attn(*c.args())
+    c.check(out, lse)
+
+
+def torch_reference(zf, cache, q, table, lens, start, page, window=0, rows=None):
+    """float64 on the GPU, for contexts too long for the oracle's loops."""
+    out, lse = [], []
+    for b in range(len(lens)):
+        L, T = lens[b], start[b + 1] - start[b]
+        at = torch.arange(L, device="cuda")
+        k, v = (x.view(torch.bfloat16).double() for x in
+                zf.q4_read_tokens(cache, table[b][(at // page).long()].int(), (at % page).int()))
+        group = q.shape[1] // k.shape[1]
+        k, v = k.repeat_interleave(group, 1), v.repeat_interleave(group, 1)
+        for t0 in range(0, T, 64):
+            qq = q[start[b] + t0:start[b] + min(T, t0 + 64)].double()
+            x = torch.einsum("thd,nhd->thn", qq, k) / math.sqrt(128)
+            pos = L - T + t0 + torch.arange(qq.shape[0], device="cuda")
+            hide = at[None] > pos[:, None]
+            if window:
+                hide |= at[None] <= pos[:, None] - window
+            x.masked_fill_(hide[:, None], -math.inf)
+            lse.append(torch.logsumexp(x, -1))
+            out.append(torch.einsum("thn,nhd->thd", torch.softmax(x, -1), v))
+    return torch.cat(out), torch.cat(lse)
+
+
+@pytest.mark.parametrize("lens,new,window", [([40000], [3], 0), ([30000, 12], [200, 12], 0), ([20000, 20001], [1, 130], 5000)])
+def test_units_split_over_ctas(zf, lens, new, window):
+    """Long contexts and few rows: parts of units are joined."""
+    page, hkv, group = 64, 2, 4
+    g = torch.Generator(device="cuda").manual_seed(7)
+    count = [-(-L // page) for L in lens]
+    pool = sum(count)
+    cache = zf.Q4Cache(pool, hkv, page)
+    perm = torch.randperm(pool, generator=g, device="cuda").int()
+    table = torch.full((len(lens), max(count)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for b, n in enumerate(count):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    every = torch.arange(pool * page, device="cuda")
+    k, v = (torch.randn(pool * page, hkv, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    zf.q4_write_tokens(cache, k, v, (every // page).int(), (every % page).int())
+    start = [0] + np.cumsum(new).tolist()
+    q = torch.randn(start[-1], hkv * group, 128, generator=g, device="cuda").to(torch.bfloat16)
+    out, lse = zf.q4_chunk_attn(cache, q, table, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                torch.tensor(start, dtype=torch.int32, device="cuda"), window=window)
+    want, wl = torch_reference(zf, cache, q, table, lens, start, page, window)
+    # values of some 1 / sqrt(contexts): half a BF16 step and the fp16 weights' errors, which average out
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * 0.9).all()
+    assert ((lse.double() - wl).abs() <= 2.0 ** -16 * 40).all()
+    # the decode kernel agrees where it has the same rows
+    if len(set(new)) == 1 and new[0] <= 4 and not window:
+        o, l = zf.q4_decode_attn(cache, q.view(len(lens), new[0], -1, 128), table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        assert ((out.double() - o.view(out.shape).double()).abs() <= 2.0 ** -8 * o.view(out.shape).abs() + 2.0 ** -11).all()
+        assert ((lse - l.view(lse.shape)).abs() <= 2.0 ** -16 * 40).all()
+
+
+def test_many_requests(zf):
+    """4096 requests, most without new tokens; every CTA finds its own."""
+    B, page = 4096, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    new = torch.zeros(B, dtype=torch.int64)
+    new[[5, 6, 900, 2047, 2048, 4095]] = torch.tensor([3, 1, 200, 40, 1, 7])
+    lens = torch.full((B,), 30)
+    lens[900] = 256
+    table = torch.randint(0, 50, (B, 16), generator=torch.Generator().manual_seed(1), dtype=torch.int32).cuda()
+    cache = zf.Q4Cache(50, 1, page)
+    every = torch.arange(50 * page, device="cuda")
+    k, v = (torch.randn(50 * page, 1, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    zf.q4_write_tokens(cache, k, v, (every // page).int(), (every % page).int())
+    start = torch.cat((torch.zeros(1, dtype=torch.int64), new.cumsum(0)))
+    q = torch.randn(int(start[-1]), 4, 128, generator=g, device="cuda").to(torch.bfloat16)
+    lens[2047] = 41
+    out, lse = zf.q4_chunk_attn(cache, q, table, lens.int().cuda(), start.int().cuda())
+    keep = [b for b in range(B) if new[b]]
+    some = [0] + new[keep].cumsum(0).tolist()
+    want, wl = torch_reference(zf, cache, q, table[keep], lens[keep].tolist(), some, page)
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * 4).all()
+    assert ((lse.double() - wl).abs() <= 2.0 ** -16 * 40).all()
+
+
+def test_offsets_beyond_32_bits(zf):
+    """Pages whose records lie beyond 4 GiB."""
+    page, hkv = 128, 8
+    pool = (5 << 30) // (hkv * 8 * 2304)
+    cache = zf.Q4Cache(pool, hkv, page)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    ids = torch.tensor([pool - 1, 3, pool - 2], device="cuda")
+    L = 300
+    at = torch.arange(L, device="cuda")
+    k, v = (torch.randn(L, hkv, 128, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    zf.q4_write_tokens(cache, k, v, ids[at // page].int(), (at % page).int())
+    q = torch.randn(9, 16, 128, generator=g, device="cuda").to(torch.bfloat16)
+    table = ids.int()[None]
+    lens, start = torch.tensor([L], dtype=torch.int32, device="cuda"), torch.tensor([0, 9], dtype=torch.int32, device="cuda")
+    out, lse = zf.q4_chunk_attn(cache, q, table, lens, start)
+    want, wl = torch_reference(zf, cache, q, table, [L], [0, 9], page)
+    assert ((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -11 * 4).all()
+    assert ((lse.double() - wl).abs() <= 2.0 ** -16 * 40).all()
+
+
+def test_same_bits_again_captured_and_on_other_streams(zf):
+    c = Case(zf, 16, 2, 4, [900, 37, 129, 400], [200, 37, 1, 1], seed=12)
+    args = c.args()
+    need = zf.q4_chunk_workspace_size(4, c.rows, c.hq, 2, 16, c.table.shape[1])
+    want = zf.q4_chunk_attn(*args)
+    ws = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]      # exactly enough, any contents
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [zf.q4_chunk_attn(*args, workspace=w, stream=s) for w, s in zip(ws * 3, streams * 3)]
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want[0]) and torch.equal(l, want[1])
+    with pytest.raises(zf.ZfError, match="workspace"):
+        zf.q4_chunk_attn(*args, workspace=ws[0][:need - 1])
+    # two graphs that share a workspace, replayed one after the other, with other lengths than captured
+    cache, q, table, lens, start = args
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    graphs = []
+    for kw in ({}, dict(window=50)):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            zf.q4_chunk_attn(cache, q, table, lens, start, out=out, lse=lse, workspace=ws[0], **kw)
+        graphs.append(gr)
+    shorter = torch.tensor([880, 37, 100, 399], dtype=torch.int32, device="cuda")
+    for values in (shorter, lens.clone()):
+        lens.copy_(values)
+        for gr, kw in zip(graphs, ({}, dict(window=50))):
+            gr.replay()
+            o, l = zf.q4_chunk_attn(cache, q, table, lens, start, workspace=ws[1], **kw)
+            assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_behind_a_late_writer(zf):
+    """The kernel ahead lets the next one start and then writes its lengths and rows."""
+    late = H.late_writer()
+    c = Case(zf, 16, 1, 4, [120, 60], [30, 2], seed=13)
+    cache, q, table, lens, start = c.args()
+    want = zf.q4_chunk_attn(cache, q, table, lens, start)
+    d_lens, d_q = torch.zeros_like(lens), torch.zeros_like(q)
+    d_start = torch.zeros_like(start)
+    ws = zf.new_workspace(zf.q4_chunk_workspace_size(2, c.rows, 4, 1, 16, table.shape[1]))
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    s = torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    d_lens.copy_(lens)
+    assert late(start.data_ptr(), d_start.data_ptr(), 3, q.data_ptr(), d_q.data_ptr(), q.numel() // 2, 300000, s) == 0
+    zf.q4_chunk_attn(cache, d_q, table, d_lens, d_start, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
