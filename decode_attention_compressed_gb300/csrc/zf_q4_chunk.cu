@@ -11,21 +11,20 @@
 // workspace, which a second kernel joins.
 //
 // One CTA, 20 warps:
-//  * warps 0-3 and 4-7, two softmax groups, a thread per row.  More than 128 rows: group A has rows 0-127, B the
-//    rest, and both take every step.  Up to 128 rows: both have the same rows, A the even steps, B the odd ones,
-//    and A joins the two at the end from tensor memory (a group's chain from scores to weights is long, so two
-//    are under way in either case).  Scores (fp32, 128 x 128) come out of tensor memory twice, for the maximum
-//    and for the weights, which go back over them as fp16: the A operand of the second product.  A row's maximum
-//    is raised only when a score exceeds it by 2^8 (the output in tensor memory is then rescaled in place).
+//  * warps 0-7, softmax: all on the same job, which is a tile of 128 rows and a step, 16 rows a warp, so that a job's
+//    chain from scores to weights is short.  Two tiles of up to 256 rows take turns; up to 128 rows, one tile takes
+//    one step after the other.  Scores (fp32, 128 x 128) come out of tensor memory once; the weights go back over
+//    them as fp16, the A operand of the second product.  A row's maximum is raised only when a score exceeds it
+//    by 2^8 (the output in tensor memory is then rescaled in place).  These warps also stage query rows as fp16, each
+//    row times a power of two (exact down to 2^-28 of its largest value).
 //  * warps 8-15 decode: warp r takes the 16 tokens of record r of each step from shared memory to the fp16
 //    operands.  A code is e2m1 and a scale e4m3, so their product is exact in fp16; K is K-major, V is stored the
 //    same way (a token's 8 channels are one row of a core matrix) and read as an MN-major operand.  The operands
 //    go round three buffers of 32 KB.
 //  * warp 16 issues the products: S = Q K^T (8 x M128 N128 K16 from shared memory) and O += P V (P from tensor
-//    memory), alternating between the groups.
+//    memory).
 //  * warp 17 finds the CTA's range, walks its pieces, resolves pages and starts the records' bulk copies, three
 //    steps ahead.
-//  * warps 18-19 stage query rows as fp16, each row times a power of two (exact down to 2^-28 of its largest value).
 // Every wait is bounded; one that gives up sets ZF_DEV_TIMEOUT and the CTA winds down.
 //
 // Numbers.  Scores, maxima and sums are fp32.  The weights enter the second product as fp16, 2^7 times their size
@@ -47,9 +46,11 @@ namespace {
 
 constexpr int kThreads = 640;
 constexpr int kDecodeWarp0 = 8, kDecodeWarps = 8;
-constexpr int kMmaWarp = 16, kWalkWarp = 17, kQWarp0 = 18, kQWarps = 2;
-constexpr int kWarps = kThreads / 32;
-constexpr int kStep = 128;                       // tokens per step
+constexpr int kMmaWarp = 16, kWalkWarp = 17;       // (18 and 19 fill up a warpgroup)
+// Registers per thread: the launch's, and what the softmax, decode and other warpgroups (4 warps) make of them.
+constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsDecode = 72, kRegsOther = 80;
+static_assert(2 * kRegsSoftmax + 2 * kRegsDecode + kRegsOther <= 5 * kRegs, "a larger sum would wait for registers forever");
+constexpr int kStep = 128;                       // tokens per step: of the operands
 constexpr int kUnitRows = 256;                   // query rows per unit
 constexpr int kStages = 3;                       // steps of records in flight
 constexpr int kRing = 3;                         // operand buffers
@@ -63,7 +64,7 @@ constexpr float kBigScore = 1048576.f;           // scores (log2 units) from whi
 constexpr float kRaise = 8.f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2f = 0.6931471805599453f;
 
-// Tensor memory: scores (and weights over them) of A and B, outputs of A and B.
+// Tensor memory: two buffers of scores (weights go over them), outputs of the two tiles.
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 
 struct ChunkArgs {
@@ -81,7 +82,7 @@ struct ChunkArgs {
   int4* part_at;                 // [CTA][2][2]: see write_part
   int32_t batch, rows, hq, hkv, group, page_size, num_pages, max_pages, part_rows, window;
   float scale_log2;              // softmax scale * log2(e) * the decoding's factors
-  float cap_log2, inv_cap;       // cap * log2(e), 1 / (cap * log2(e)); kMod only
+  float cap_log2, two_over_cap;  // cap * log2(e), 2 / cap (kCap: scores in log2 units to twice the tanh's argument in them)
   float v_factor;
   uint64_t wait_limit_ns;
 };
@@ -103,14 +104,11 @@ enum : int {
   kBarRecEmpty = kBarRecFull + kStages * 8,
   kBarOpFull = kBarRecEmpty + kStages * 8,     // [kRing] operand decoded
   kBarOpEmpty = kBarOpFull + kRing,            // [kRing] its last product done (commit)
-  kBarSFull = kBarOpEmpty + kRing,             // [2] scores of a group (commit)
-  kBarPFull = kBarSFull + 2,                   // [2] weights of a group
-  kBarOFull = kBarPFull + 2,                   // [2] output of a group complete (commit)
-  kBarQFull = kBarOFull + 2,
-  kBarQEmpty = kBarQFull + 1,                  // last score product of a piece done (commit)
-  kBarBDone = kBarQEmpty + 1,                  // group B's part of a shared piece is final
-  kBarADone = kBarBDone + 1,                   // group A has read it
-  kBarDrain = kBarADone + 1,
+  kBarSFull = kBarOpEmpty + kRing,             // [2] scores of a job in a buffer (commit)
+  kBarPFull = kBarSFull + 2,                   // [2] its weights
+  kBarPvDone = kBarPFull + 2,                  // [2] its product with the values (commit)
+  kBarQFull = kBarPvDone + 2,                  // query rows of a piece
+  kBarDrain = kBarQFull + 1,
   kNumBars = kBarDrain + 1,
 };
 
@@ -119,16 +117,17 @@ constexpr int kSmRing = 0;
 constexpr int kSmQ = kSmRing + kRing * kOperand;
 constexpr int kSmRec = kSmQ + 2 * kOperand;
 constexpr int kSmScale = kSmRec + kStages * 8 * kQ4Record;     // [2][256] score factors of the rows
-constexpr int kSmMl = kSmScale + 2 * kUnitRows * 4;            // [128] float2: group B's maxima and sums
-constexpr int kSmPiece = kSmMl + 128 * 8;                      // [2] Piece
+constexpr int kSmPos = kSmScale + 2 * kUnitRows * 4;           // [2][256] their positions
+constexpr int kSmSlope = kSmPos + 2 * kUnitRows * 4;           // [2][256] their slopes
+constexpr int kSmPiece = kSmSlope + 2 * kUnitRows * 4;         // [2] Piece
 constexpr int kSmAbsent = kSmPiece + 2 * 48;                   // [8 steps][8 records] 1: no tokens there
 constexpr int kSmBars = kSmAbsent + 64;
 constexpr int kSmMisc = kSmBars + kNumBars * 8;                // abort flag, tensor-memory base, range
 constexpr int kSmTotal = kSmMisc + 64;
 static_assert(kSmTotal <= 227 * 1024 && kSmBars % 8 == 0 && sizeof(Piece) <= 48, "shared memory");
-static_assert((ZF_MAX_BATCH + 1) * 8 <= kRing * kOperand, "the plan's sums");
+static_assert((ZF_MAX_BATCH + 1) * 4 <= kRing * kOperand, "the plan's sums");
 
-// Instruction descriptor of kind::f16 with FP16 operands and an FP32 accumulator, N 128, M 128; B K-major or
+// Instruction descriptors of kind::f16 with FP16 operands and an FP32 accumulator, M 128 and N 128: B K-major, and
 // MN-major (bit 16).
 constexpr uint32_t kIdescS = (1u << 4) | (128u / 8 << 17) | (128u / 16 << 24);
 constexpr uint32_t kIdescO = kIdescS | (1u << 16);
@@ -142,22 +141,47 @@ __device__ __forceinline__ uint64_t desc_mn(const void* p) {
          (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
 }
 
-// The MMA warp's issue forms (the whole warp calls, one lane issues).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+template <int kN>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kN));
+}
+template <int kN>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kN));
+}
+
+// The MMA warp's issue forms (the whole warp calls, one lane issues: from a branch of one lane an instruction takes
+// about 120 cycles, more than the tensor cores need for it): S = Q K^T over 128 channels, O += P V over 128 tokens.
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred e, f, t;\n\t.reg .b64 x, y;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdescS), "r"(acc)
+      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
+      "add.s64 x, %1, 16;\n\tadd.s64 y, %2, 16;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 32;\n\tadd.s64 y, %2, 32;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 48;\n\tadd.s64 y, %2, 48;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 64;\n\tadd.s64 y, %2, 64;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 80;\n\tadd.s64 y, %2, 80;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 96;\n\tadd.s64 y, %2, 96;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
+      "add.s64 x, %1, 112;\n\tadd.s64 y, %2, 112;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(kIdescS)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
+  static_assert(2 * kCoreRow / 16 == 256, "descriptor steps");
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
+      "{\n\t.reg .pred e, f, t;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+      "add.u32 x, %1, 8;\n\tadd.s64 y, %2, 256;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+      "add.u32 x, %1, 16;\n\tadd.s64 y, %2, 512;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+      "add.u32 x, %1, 24;\n\tadd.s64 y, %2, 768;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+      "add.u32 x, %1, 32;\n\tadd.s64 y, %2, 1024;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+      "add.u32 x, %1, 40;\n\tadd.s64 y, %2, 1280;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+      "add.u32 x, %1, 48;\n\tadd.s64 y, %2, 1536;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
+      "add.u32 x, %1, 56;\n\tadd.s64 y, %2, 1792;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(kIdescO), "r"(acc)
       : "memory");
 }
@@ -169,10 +193,11 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
       : "memory");
 }
 
-// 32 TMEM lanes (thread t: lane t) x 32 consecutive columns.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 TMEM lanes x 64 columns: thread t gets rows t / 4 and t / 4 + 8, columns 8 j + 2 (t % 4) and + 1 (registers 4 j,
+// 4 j + 1 and 4 j + 2, 4 j + 3).
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
@@ -180,17 +205,34 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+// Stores: 32 columns in the same layout, and 32 columns of pairs of 16 bits (thread t: rows t / 4 and t / 4 + 8, column
+// 4 j + t % 4 in registers 2 j and 2 j + 1).
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 
+// Loads have arrived; the registers are named, so that nothing that uses them moves ahead of this.
+__device__ __forceinline__ void touch(uint32_t (&r)[32]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+               "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+               "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void touch(uint32_t (&r)[16]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+               "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -216,15 +258,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                              const ChunkArgs& a) {
-  if (*abort_flag) return false;
-  if (mbar_wait(bar, parity, a.wait_limit_ns)) return true;
+// A bounded wait that also ends when another warp's has given up (abort_flag).
+__device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const ChunkArgs& a) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t i = 0; i < (1u << 30) && !*abort_flag; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (global_timer_ns() - t0 > a.wait_limit_ns) break;
+  }
+  if (!*abort_flag) report(a.status, ZF_DEV_TIMEOUT);
   *abort_flag = 1;
-  report(a.status, ZF_DEV_TIMEOUT);
   return false;
 }
-
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const ChunkArgs& a) {
+  return mbar_try_wait(bar, parity) || wait_longer(bar, parity, abort_flag, a);
+}
 // The same for a whole warp, which takes one outcome.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const ChunkArgs& a) {
   return __all_sync(0xFFFFFFFFu, wait_or_abort(bar, parity, abort_flag, a));
@@ -276,7 +323,7 @@ struct Place {
   int b, g, i, s;
 };
 // The place of cost c (whole warp; sums[b]: cost of the requests before b).
-__device__ __forceinline__ Place find_place(const ChunkArgs& a, const long long* sums, long long c, int lane) {
+__device__ __forceinline__ Place find_place(const ChunkArgs& a, const int* sums, int c, int lane) {
   Place p{a.batch, 0, 0, 0};
   if (c >= sums[a.batch]) return p;
   int lo = 0, hi = a.batch;                          // sums[lo] <= c < sums[hi]
@@ -285,29 +332,29 @@ __device__ __forceinline__ Place find_place(const ChunkArgs& a, const long long*
     if (sums[mid] <= c) lo = mid; else hi = mid;
   }
   p.b = lo;
-  const long long head = (sums[lo + 1] - sums[lo]) / a.hkv;
-  long long rest = c - sums[lo];
-  p.g = static_cast<int>(rest / head);
+  const int head = (sums[lo + 1] - sums[lo]) / a.hkv;
+  int rest = c - sums[lo];
+  p.g = rest / head;
   rest -= p.g * head;
   const Request r = request<false>(a, lo);
   const int n = unit_count(a, r);
   for (int base = 0; base < n; base += 32) {
     const int i = base + lane;
-    long long in = i < n ? unit_cost(a, r, i) : 0;
+    int in = i < n ? unit_cost(a, r, i) : 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long x = __shfl_up_sync(0xFFFFFFFFu, in, d);
+      const int x = __shfl_up_sync(0xFFFFFFFFu, in, d);
       if (lane >= d) in += x;
     }
     const uint32_t above = __ballot_sync(0xFFFFFFFFu, i < n && in > rest);
     if (above) {
       const int k = __ffs(above) - 1;
-      const long long before = k > 0 ? __shfl_sync(0xFFFFFFFFu, in, k - 1) : 0;
+      const int before = k > 0 ? __shfl_sync(0xFFFFFFFFu, in, k - 1) : 0;
       int slo, shi, last;
       p.i = base + k;
       unit_steps(a, r, p.i, slo, shi, last);
       const int steps = shi - slo;
-      int s = static_cast<int>(min(max(rest - before - kUnitCost, 0ll), static_cast<long long>(steps)));
+      int s = min(max(rest - before - kUnitCost, 0), steps);
       if (s < kSnap) s = 0;
       else if (steps - s < kSnap) s = steps;
       p.s = s;
@@ -333,22 +380,28 @@ template <bool kV>
 __device__ __forceinline__ void decode_tile(const uint8_t* rec, uint8_t* op, int r, int lane) {
   const int t = lane & 7, q = lane >> 3;
   uint8_t* base = op + 2 * r * kCoreRow + t * 16;
+  uint32_t sw[2];
+  uint2 codes[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {                      // (all loads before the first store, which could be to their place)
+    const int block = (2 * (t >> 1) + (q & 1) + 2 * (q >> 1) + 4 * i) & 7;
+    sw[i] = *reinterpret_cast<const uint32_t*>(
+        rec + (kV ? kQ4VScales + block * 16 + (t >> 1) * 4 : kQ4KScales + t * 16 + (block >> 1) * 4));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      codes[i][h] = *reinterpret_cast<const uint2*>(rec + (kV ? q4_v_code_at(t + 8 * h, block) : q4_k_code_at(t + 8 * h, block)));
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int block = (2 * (t >> 1) + (q & 1) + 2 * (q >> 1) + 4 * i) & 7;
-    const uint32_t sw = *reinterpret_cast<const uint32_t*>(
-        rec + (kV ? kQ4VScales + block * 16 + (t >> 1) * 4 : kQ4KScales + t * 16 + (block >> 1) * 4));
     const uint32_t sel = kV ? t & 1 : block & 1;     // byte of token t; that of t + 8 is two on
-    const uint32_t two = __byte_perm(sw, 0u, sel | (4u << 4) | ((sel + 2) << 8) | (4u << 12)) << 7;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int tok = t + 8 * h;
-      const uint2 codes = *reinterpret_cast<const uint2*>(rec + (kV ? q4_v_code_at(tok, block) : q4_k_code_at(tok, block)));
-      const uint32_t one = h ? two >> 16 : two & 0xFFFFu;
-      const uint32_t s = (one & 0x3F80u) * 0x10001u;                 // scale byte & 0x7f as a half, twice
+      const uint32_t one = __byte_perm(sw[i], 0u, (sel + 2 * h) | 0x4440u);
+      const uint32_t s = ((one & 0x7Fu) << 7) * 0x10001u;              // scale byte & 0x7f as a half, twice
       uint32_t x[4], y[4];
-      q4_decode4(codes.x, x);
-      q4_decode4(codes.y, y);
+      q4_decode4(codes[i][h].x, x);
+      q4_decode4(codes[i][h].y, y);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         x[e] = mul_f16x2(x[e], s);
@@ -366,32 +419,21 @@ __device__ __forceinline__ void zero_tile(uint8_t* op, int r, int lane) {
 }
 
 // -------------------------------------------------------------------------------------- softmax
-// tanh with an error of a few units in the last place of the larger of it and 2^-12.
-__device__ __forceinline__ float tanh_f32(float x) {
-  const float ax = fabsf(x);
-  const float e = fast_exp2(ax * (2.f * kLog2e));                     // e^{2|x|}
-  const float big = 1.f - __fdividef(2.f, e + 1.f);
-  const float x2 = x * x;                                             // Taylor series, |x| < 0.35
-  const float small =
-      fmaf(fmaf(fmaf(fmaf(fmaf(-0.0088632355f, x2, 0.021869488f), x2, -0.053968254f), x2, 0.13333333f), x2, -0.33333333f),
-           x2 * ax, ax);
-  return copysignf(ax < 0.35f ? small : ax > 15.f ? 1.f : big, x);
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
-// A row's scores as they enter the exponential (log2 units): capped, biased, hidden ones -inf.
-template <bool kMod>
-__device__ __forceinline__ float score(const ChunkArgs& a, float s, float factor, float slope, int far, uint64_t absent, int j,
-                                       int window) {
-  float x = s * factor;
-  if (kMod) {
-    if (a.inv_cap > 0.f) x = a.cap_log2 * tanh_f32(x * a.inv_cap);
-    x = fmaf(slope, static_cast<float>(-far), x);
-  }
-  const bool hidden = far < 0 || far >= window || ((absent >> (8 * (j >> 4))) & 1u);
-  return hidden ? -CUDART_INF_F : x;
-}
+// What becomes of the scores: nothing; slopes; a cap, and slopes if there are any.
+enum : int { kPlain = 0, kSlope = 1, kCap = 2 };
 
-template <bool kMod>
+template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kSmBars);
@@ -402,10 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[kBarPieceFull + i], 1);
-      mbar_init(&bars[kBarPieceEmpty + i], kWarps - 1);
+      mbar_init(&bars[kBarPieceEmpty + i], 8 + kDecodeWarps + 1);
       mbar_init(&bars[kBarSFull + i], 1);
-      mbar_init(&bars[kBarPFull + i], 4);
-      mbar_init(&bars[kBarOFull + i], 1);
+      mbar_init(&bars[kBarPFull + i], 8);
+      mbar_init(&bars[kBarPvDone + i], 1);
     }
     for (int i = 0; i < kStages * 8; ++i) {
       mbar_init(&bars[kBarRecFull + i], 1);
@@ -415,10 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       mbar_init(&bars[kBarOpFull + i], kDecodeWarps);
       mbar_init(&bars[kBarOpEmpty + i], 1);
     }
-    mbar_init(&bars[kBarQFull], kQWarps);
-    mbar_init(&bars[kBarQEmpty], 1);
-    mbar_init(&bars[kBarBDone], 4);
-    mbar_init(&bars[kBarADone], 4);
+    mbar_init(&bars[kBarQFull], 8);
     mbar_init(&bars[kBarDrain], 1);
     *abort_flag = 0;
   }
@@ -429,13 +468,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
   wait_prior_grid();
 
   // ---- costs of the requests (a warp takes 32 at a time; those of many units with all its lanes)
-  long long* sums = reinterpret_cast<long long*>(smem + kSmRing);
+  int* sums = reinterpret_cast<int*>(smem + kSmRing);
   for (int base = warp * 32; base < a.batch; base += kThreads) {
     const int b = base + lane;
     Request r{0, 0, 0};
     if (b < a.batch) r = blockIdx.x == 0 ? request<true>(a, b) : request<false>(a, b);
     const int n = unit_count(a, r);
-    long long cost = 0;
+    int cost = 0;
     if (n <= 4)
       for (int i = 0; i < n; ++i) cost += unit_cost(a, r, i);
     uint32_t many = __ballot_sync(0xFFFFFFFFu, n > 4);
@@ -444,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       many &= many - 1;
       const Request o{0, __shfl_sync(0xFFFFFFFFu, r.tokens, src), __shfl_sync(0xFFFFFFFFu, r.len, src)};
       const int units = unit_count(a, o);
-      long long part = 0;
+      int part = 0;
       for (int i = lane; i < units; i += 32) part += unit_cost(a, o, i);
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
@@ -454,13 +493,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
   }
   __syncthreads();
   if (warp == 0) {
-    long long carry = 0;
+    int carry = 0;
     for (int base = 0; base < a.batch; base += 32) {
       const int b = base + lane;
-      long long v = b < a.batch ? sums[b + 1] : 0;
+      int v = b < a.batch ? sums[b + 1] : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        const int x = __shfl_up_sync(0xFFFFFFFFu, v, d);
         if (lane >= d) v += x;
       }
       if (b < a.batch) sums[b + 1] = carry + v;
@@ -471,19 +510,21 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
   __syncthreads();
   Place from{a.batch, 0, 0, 0}, to = from;
   if (warp == kWalkWarp) {
-    const long long total = sums[a.batch];
-    const long long ctas = min(static_cast<long long>(gridDim.x), (total + kMinCost - 1) / kMinCost);
-    const long long at = blockIdx.x;
+    const int total = sums[a.batch];
+    const int ctas = min(static_cast<int>(gridDim.x), (total + kMinCost - 1) / kMinCost), at = blockIdx.x;
     if (at < ctas) {
-      from = find_place(a, sums, total * at / ctas, lane);
-      to = find_place(a, sums, total * (at + 1) / ctas, lane);
+      const int each = total / ctas, more = total - each * ctas;       // the first `more` CTAs take one more
+      from = find_place(a, sums, each * at + min(at, more), lane);
+      to = find_place(a, sums, each * (at + 1) + min(at + 1, more), lane);
     }
   }
   tcgen05_after_sync();
   __syncthreads();
   const uint32_t tmem = *tmem_slot;
   Piece* pieces = reinterpret_cast<Piece*>(smem + kSmPiece);
-
+  // (a warpgroup's warps run one setmaxnreg together, so it stands before their ways part)
+  if (warp >= kMmaWarp) {
+  give_registers<kRegsOther>();
   if (warp == kWalkWarp) {
     // ================================================================== walk and copies
     const uint64_t policy = l2_evict_first_policy();
@@ -615,68 +656,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     for (int k = 0; k < kStages; ++k)
       if ((started >> k & 1) && !mbar_wait(&bars[kBarRecFull + k * 8 + lane], (phase >> k) & 1)) report(a.status, ZF_DEV_TIMEOUT);
     __syncwarp();
-  } else if (warp >= kQWarp0) {
-    // ================================================================== query rows
-    const int w = warp - kQWarp0, t8 = lane & 7, q4 = lane >> 3;
-    for (int n = 0;; ++n) {
-      const int buf = n & 1;
-      if (!wait_warp(&bars[kBarPieceFull + buf], (n >> 1) & 1, abort_flag, a)) break;
-      const Piece p = pieces[buf];
-      if (p.b < 0) break;
-      if (n > 0 && !wait_warp(&bars[kBarQEmpty], (n - 1) & 1, abort_flag, a)) break;
-      if (p.steps > 0) {
-        float* fac = reinterpret_cast<float*>(smem + kSmScale) + buf * kUnitRows;
-        const int groups = (p.rows > 128 ? kUnitRows : 128) / 8;
-        const bool negate = a.scale_log2 < 0.f;
-#pragma unroll 2
-        for (int gr = w; gr < groups; gr += kQWarps) {
-          const int rr = gr * 8 + t8;
-          uint4 v[4];
-          const bool in = rr < p.rows;
-          const int row = p.row0 + (in ? rr : 0), tok = row / a.group, h = row - tok * a.group;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              a.q + (static_cast<size_t>(p.q0 + tok) * a.hq + p.g * a.group + h) * ZF_HEAD_DIM);
-          uint32_t big = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[i] = in ? src[q4 + 4 * i] : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t m2 = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu),
-                                         __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-            big = max(big, max(m2 & 0xFFFFu, m2 >> 16));
-          }
-          big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 8));
-          big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 16));
-          // the power of two that brings the row's largest exponent to 11; the factor takes it back (positive, so
-          // that the largest raw score has the largest score: a negative scale negates the row)
-          const int k = min(138 - static_cast<int>(big >> 7), 126);
-          const float f = __int_as_float(((127 + k) << 23) | (negate ? 0x80000000 : 0));
-          if (q4 == 0) fac[rr] = fmaxf(__int_as_float((127 - k) << 23) * fabsf(a.scale_log2), 1e-37f);
-          uint8_t* dst = smem + kSmQ + gr * kCoreRow + t8 * 16;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = pack_f16(bf16lo_to_f32(x[e]) * f, bf16hi_to_f32(x[e]) * f);
-            *reinterpret_cast<uint4*>(dst + (q4 + 4 * i) * 128) = make_uint4(y[0], y[1], y[2], y[3]);
-          }
-        }
-        fence_proxy_async_smem();
-      }
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&bars[kBarQFull]);
-        mbar_arrive(&bars[kBarPieceEmpty + buf]);
-      }
-      __syncwarp();
-    }
   } else if (warp == kMmaWarp) {
     // ================================================================== products
-    uint32_t gs = 0;                              // steps before this piece
-    uint32_t jobs = 0;                            // parity of the next weights, per group
+    // Job j of a piece: the scores of a tile of 128 rows and a step, and the product of their weights.  More than 128
+    // rows: job j is tile j % 2 and step j / 2, else step j of the one tile.  The next job's scores are computed while
+    // the softmax has one job's, the one after it once the product that frees their buffer is issued.
+    uint32_t gs = 0, gj = 0;                      // steps and jobs before this piece
+    uint32_t rows_seen = 0;                       // pieces whose query rows were waited for
+    uint32_t fed = 0;                             // operands waited for
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int buf = n & 1;
@@ -684,57 +671,52 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       const int pb = pieces[buf].b, steps = pieces[buf].steps;
       const bool both = pieces[buf].rows > 128;
       if (pb < 0) break;
-      if (!wait_warp(&bars[kBarQFull], n & 1, abort_flag, a)) break;
+      if (steps > 0 && !wait_warp(&bars[kBarQFull], rows_seen++ & 1, abort_flag, a)) break;
       tcgen05_after_sync();
       const int N = both ? 2 * steps : steps;
-      auto op_wait = [&](uint32_t k) {             // operand k of the ring
-        return wait_warp(&bars[kBarOpFull + k % kRing], (k / kRing) & 1, abort_flag, a);
+      auto operand = [&](uint32_t k) -> bool {     // operand k of the ring (they come in order)
+        while (fed <= k) {
+          if (!wait_warp(&bars[kBarOpFull + fed % kRing], (fed / kRing) & 1, abort_flag, a)) return false;
+          ++fed;
+        }
+        return true;
       };
       auto scores = [&](int j) -> bool {
-        const int x = j & 1, s = both ? j >> 1 : j;
-        const uint32_t k = 2 * (gs + s);
-        if (!(both && x) && !op_wait(k)) return false;
+        const uint32_t k = 2 * (gs + (both ? j >> 1 : j)), b = (gj + j) & 1;
+        if (!operand(k)) return false;
         tcgen05_after_sync();
-        const uint64_t qa = desc_k(smem + kSmQ + (both && x ? kOperand : 0));
-        const uint64_t kb = desc_k(smem + kSmRing + (k % kRing) * kOperand);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mma_ss(tmem + kTmemS + 128 * x, qa + e * 16, kb + e * 16, e > 0);
-        commit(&bars[kBarSFull + x]);
-        if (!both || x) commit(&bars[kBarOpEmpty + k % kRing]);
-        if (j == N - 1) commit(&bars[kBarQEmpty]);
+        mma_scores(tmem + kTmemS + 128 * b, desc_k(smem + kSmQ + (both && (j & 1) ? kOperand : 0)),
+                   desc_k(smem + kSmRing + (k % kRing) * kOperand));
+        commit(&bars[kBarSFull + b]);
+        if (!both || (j & 1)) commit(&bars[kBarOpEmpty + k % kRing]);
         return true;
       };
       auto product = [&](int j) -> bool {
-        const int x = j & 1, s = both ? j >> 1 : j;
-        const uint32_t k = 2 * (gs + s) + 1;
-        if (!(both && x) && !op_wait(k)) return false;
-        if (!wait_warp(&bars[kBarPFull + x], (jobs >> x) & 1, abort_flag, a)) return false;
-        jobs ^= 1u << x;
+        const uint32_t k = 2 * (gs + (both ? j >> 1 : j)) + 1, b = (gj + j) & 1;
+        if (!operand(k)) return false;
+        if (!wait_warp(&bars[kBarPFull + b], ((gj + j) >> 1) & 1, abort_flag, a)) return false;
         tcgen05_after_sync();
-        const uint64_t vb = desc_mn(smem + kSmRing + (k % kRing) * kOperand);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          mma_ts(tmem + kTmemO + 128 * x, tmem + kTmemS + 128 * x + 8 * e, vb + e * (2 * kCoreRow / 16), j > 1 || e > 0);
-        if (!both || x) commit(&bars[kBarOpEmpty + k % kRing]);
-        if (j >= N - 2) commit(&bars[kBarOFull + x]);
+        mma_weights(tmem + kTmemO + (both && (j & 1) ? 128 : 0), tmem + kTmemS + 128 * b,
+                    desc_mn(smem + kSmRing + (k % kRing) * kOperand), j > (both ? 1 : 0));
+        commit(&bars[kBarPvDone + b]);
+        if (!both || (j & 1)) commit(&bars[kBarOpEmpty + k % kRing]);
         return true;
       };
-      if (N > 0) ok = scores(0);
-      if (ok && N > 1) ok = scores(1);
-      for (int j = 0; ok && j < N; ++j) {
-        ok = product(j);
-        if (ok && j + 2 < N) ok = scores(j + 2);
-      }
-      if (N == 0) commit(&bars[kBarQEmpty]);
+      for (int j = 0; ok && j < min(N, 2); ++j) ok = scores(j);
+      for (int j = 0; ok && j < N; ++j) ok = product(j) && (j + 2 >= N || scores(j + 2));
       gs += steps;
+      gj += N;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarPieceEmpty + buf]);
     }
     // every product issued has completed before the tensor memory is given back
     commit(&bars[kBarDrain]);
     if (!mbar_wait(&bars[kBarDrain], 0)) report(a.status, ZF_DEV_TIMEOUT);
+  }
   } else if (warp >= kDecodeWarp0) {
     // ================================================================== decoding
+    give_registers<kRegsDecode>();
+    constexpr int kPerWarp = 8 / kDecodeWarps;       // records of a step
     const int r = warp - kDecodeWarp0;
     uint32_t gs = 0;
     bool ok = true;
@@ -745,232 +727,356 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       if (pb < 0) break;
       for (int s = 0; s < steps; ++s, ++gs) {
         const int stage = gs % kStages;
-        if (!(ok = wait_warp(&bars[kBarRecFull + stage * 8 + r], (gs / kStages) & 1, abort_flag, a))) break;
-        const bool absent = *reinterpret_cast<volatile uint8_t*>(smem + kSmAbsent + (gs & 7) * 8 + r) != 0;
-        const uint8_t* rec = smem + kSmRec + (stage * 8 + r) * kQ4Record;
+        bool absent[kPerWarp];
+#pragma unroll
+        for (int i = 0; i < kPerWarp; ++i) {
+          const int rec = r + i * kDecodeWarps;
+          if (!(ok = wait_warp(&bars[kBarRecFull + stage * 8 + rec], (gs / kStages) & 1, abort_flag, a))) break;
+          absent[i] = *reinterpret_cast<volatile uint8_t*>(smem + kSmAbsent + (gs & 7) * 8 + rec) != 0;
+        }
+        if (!ok) break;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           const uint32_t k = 2 * gs + v;
           if (k >= kRing && !(ok = wait_warp(&bars[kBarOpEmpty + k % kRing], (k / kRing - 1) & 1, abort_flag, a))) break;
           uint8_t* op = smem + kSmRing + (k % kRing) * kOperand;
-          if (absent) zero_tile(op, r, lane);
-          else if (v) decode_tile<true>(rec, op, r, lane);
-          else decode_tile<false>(rec, op, r, lane);
+#pragma unroll
+          for (int i = 0; i < kPerWarp; ++i) {
+            const int rec = r + i * kDecodeWarps;
+            const uint8_t* at = smem + kSmRec + (stage * 8 + rec) * kQ4Record;
+            if (absent[i]) zero_tile(op, rec, lane);
+            else if (v) decode_tile<true>(at, op, rec, lane);
+            else decode_tile<false>(at, op, rec, lane);
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarOpFull + k % kRing]);
         }
         if (!ok) break;
-        if (lane == 0) mbar_arrive(&bars[kBarRecEmpty + stage * 8 + r]);
+        if (lane < kPerWarp) mbar_arrive(&bars[kBarRecEmpty + stage * 8 + r + lane * kDecodeWarps]);
       }
       __syncwarp();
       if (ok && lane == 0) mbar_arrive(&bars[kBarPieceEmpty + buf]);
     }
   } else {
     // ================================================================== softmax
-    const int x = warp >> 2;                                  // group
-    const int own = 32 * (warp & 3) + lane;                   // row of the 128
-    const uint32_t ts = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kTmemS + 128 * x;
-    const uint32_t to_x = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kTmemO;
-    float2* ml_b = reinterpret_cast<float2*>(smem + kSmMl);
-    uint32_t gs = 0, jobs = 0, outs = 0, joins = 0;           // steps before this piece; this group's jobs and outputs; joins
-    bool ok = true;
-    for (int n = 0; ok; ++n) {
+    take_registers<kRegsSoftmax>();
+    // All eight warps work on the same job, 16 rows of its tile each (warps w and w + 4 share the lanes that they can
+    // reach): a lane has rows lane / 4 and lane / 4 + 8 of them, and columns 8 i + 2 (lane % 4), + 1.
+    const int row16 = 32 * (warp & 3) + 16 * (warp >> 2);     // the warp's first row in a tile
+    const int quad = lane & 3, own = row16 + (lane >> 2);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(row16) << 16);
+    float* factors = reinterpret_cast<float*>(smem + kSmScale);
+    int* positions = reinterpret_cast<int*>(smem + kSmPos);
+    float* slopes = reinterpret_cast<float*>(smem + kSmSlope);
+    uint32_t gs = 0, jobs = 0;                                // steps and jobs before
+    // The warp's 16 rows of tile t of the query operand: 4 KB that no other warp writes.
+    auto my_q = [&](int t) { return smem + kSmQ + t * kOperand + (row16 >> 3) * kCoreRow; };
+
+    // Query rows of a piece, 16 of each tile: lane (row lane % 8 of 8, chunks lane / 8 + 4 i of 16 bytes).
+    auto q_rows = [&](int buf) {
+      const Piece& p = pieces[buf];
+      const bool negate = a.scale_log2 < 0.f;
+      const int tiles = p.rows > 128 ? 2 : 1;
+      for (int t = 0; t < tiles; ++t) {
+        uint4 v[2][4];
+        int at[2], tok[2], h[2];
+#pragma unroll
+        for (int r8 = 0; r8 < 2; ++r8) {
+          at[r8] = 128 * t + row16 + 8 * r8 + (lane & 7);
+          const bool in = at[r8] < p.rows;
+          const int row = p.row0 + min(at[r8], p.rows - 1);
+          tok[r8] = row / a.group;
+          h[r8] = p.g * a.group + (row - tok[r8] * a.group);
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(p.q0 + tok[r8]) * a.hq + h[r8]) * ZF_HEAD_DIM);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[r8][i] = in ? src[(lane >> 3) + 4 * i] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int r8 = 0; r8 < 2; ++r8) {
+          uint32_t big = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 x = v[r8][i];
+            const uint32_t m2 = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+            big = max(big, max(m2 & 0xFFFFu, m2 >> 16));
+          }
+          big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 8));
+          big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 16));
+          // the power of two that brings the row's largest exponent to 11; the factor takes it back (positive, so that
+          // the largest raw score has the largest score: a negative scale negates the row)
+          const int k = min(138 - static_cast<int>(big >> 7), 126);
+          const float f = __int_as_float(((127 + k) << 23) | (negate ? 0x80000000 : 0));
+          if (lane < 8) {
+            factors[buf * kUnitRows + at[r8]] = fmaxf(__int_as_float((127 - k) << 23) * fabsf(a.scale_log2), 1e-37f);
+            positions[buf * kUnitRows + at[r8]] = p.pos0 + tok[r8];
+            if (kMode != kPlain) slopes[buf * kUnitRows + at[r8]] = a.slopes ? a.slopes[h[r8]] * kLog2e : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {v[r8][i].x, v[r8][i].y, v[r8][i].z, v[r8][i].w};
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = pack_f16(bf16lo_to_f32(w[e]) * f, bf16hi_to_f32(w[e]) * f);
+            *reinterpret_cast<uint4*>(my_q(t) + r8 * kCoreRow + ((lane >> 3) + 4 * i) * 128 + (lane & 7) * 16) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarQFull]);
+    };
+
+    // What a lane keeps of its two rows of a tile.
+    struct Rows {
+      float top[2], c[2], sum[2];                             // maximum, -maximum + shift (log2 units), sum of weights
+      int seen_begin, seen_end;                               // positions that all rows of the warp see
+    };
+    bool ok = wait_warp(&bars[kBarPieceFull], 0, abort_flag, a);
+    if (ok && pieces[0].b >= 0 && pieces[0].steps > 0) q_rows(0);
+    for (int n = 0; ok && pieces[n & 1].b >= 0; ++n) {
+      // (a piece is read from shared memory where it is needed: registers are short in the loop over its jobs)
       const int buf = n & 1;
-      if (!wait_warp(&bars[kBarPieceFull + buf], (n >> 1) & 1, abort_flag, a)) break;
-      const Piece p = pieces[buf];
-      if (p.b < 0) break;
-      const bool both = p.rows > 128;
-      const int rr = own + (both ? 128 * x : 0);
-      const bool live = rr < p.rows;
-      const int row = p.row0 + min(rr, p.rows - 1), tok = row / a.group, h = p.g * a.group + (row - tok * a.group);
-      const int pos = p.pos0 + tok;                           // this row's position
-      const int window = a.window > 0 ? a.window : INT_MAX;
-      // steps of which all rows of the warp see everything: those within these tokens
-      const int seen_end = __reduce_min_sync(0xFFFFFFFFu, pos) + 1;
-      const int seen_begin = a.window > 0 ? __reduce_max_sync(0xFFFFFFFFu, pos) + 1 - a.window : INT_MIN;
-      const float slope = kMod && a.slopes ? a.slopes[h] * kLog2e : 0.f;
-      float factor = 0.f, top = -CUDART_INF_F, c = 0.f, sum = 0.f;
-      bool any = false;                                       // the output in tensor memory is defined
-      const int first = both ? 0 : x, stride = both ? 1 : 2;
-      for (int s = first; s < p.steps; s += stride, ++jobs) {
-        if (!(ok = wait_warp(&bars[kBarSFull + x], jobs & 1, abort_flag, a))) break;
+      const bool both = pieces[buf].rows > 128;
+      const int steps = pieces[buf].steps, step0 = pieces[buf].step0, count = both ? 2 * steps : steps;
+      Rows st{{-CUDART_INF_F, -CUDART_INF_F}, {0.f, 0.f}, {0.f, 0.f}, 0, 0}, other = st;
+      for (int j = 0; j < count; ++j, ++jobs) {
+        const uint32_t b = jobs & 1, ts = lanes + kTmemS + 128 * b;
+        const int t = both ? j & 1 : 0, s = both ? j >> 1 : j;
+        if (!(ok = wait_warp(&bars[kBarSFull + b], (jobs >> 1) & 1, abort_flag, a))) break;
         tcgen05_after_sync();
-        if (s == first) factor = reinterpret_cast<const float*>(smem + kSmScale)[buf * kUnitRows + rr];
-        const int t0 = (p.step0 + s) * kStep;
+        uint32_t v[2][32];
+        tmem_ld_16x256b_x8(ts, v[0]);
+        tmem_ld_16x256b_x8(ts + 64, v[1]);
+        const int at = buf * kUnitRows + 128 * t + own;
+        const int pos[2] = {positions[at], positions[at + 8]};
+        if (s == 0) {
+          st.seen_end = __reduce_min_sync(0xFFFFFFFFu, min(pos[0], pos[1])) + 1;
+          st.seen_begin = a.window > 0 ? __reduce_max_sync(0xFFFFFFFFu, max(pos[0], pos[1])) + 1 - a.window : INT_MIN;
+        }
+        const float factor[2] = {factors[at], factors[at + 8]};
+        const int t0 = (step0 + s) * kStep;
         const uint64_t absent = *reinterpret_cast<volatile uint64_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8);
-        bool plain = !kMod && absent == 0 && t0 + kStep <= seen_end && t0 >= seen_begin;
-        float mx = -CUDART_INF_F;
-        if (plain) {
-          float m[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+        const bool whole = absent == 0 && t0 + kStep <= st.seen_end && t0 >= st.seen_begin;
+        float mul[2] = {kMode == kPlain ? factor[0] : 1.f, kMode == kPlain ? factor[1] : 1.f};      // scores are mul * v
+        tmem_wait_ld();
+        touch(v[0]);
+        touch(v[1]);
+        if (kMode == kCap) {
+          // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), off by some 2^-23 of the cap
+          const float f[2] = {factor[0] * a.two_over_cap, factor[1] * a.two_over_cap}, two = -2.f * a.cap_log2;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t v[32];
-            tmem_ld32(ts + 32 * k, v);
-            tmem_wait_ld();
+          for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], __uint_as_float(v[e]));
-          }
-          mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * factor;
-          // (scores so large that their rounded differences could pass fp16's range take the other way)
-          if (__any_sync(0xFFFFFFFFu, fabsf(mx) >= kBigScore)) plain = false;
+            for (int e = 0; e < 32; ++e)
+              v[k][e] = __float_as_uint(fmaf(fast_rcp(1.f + fast_exp2(__uint_as_float(v[k][e]) * f[(e >> 1) & 1])), two, a.cap_log2));
         }
-        if (!plain) {
-          mx = -CUDART_INF_F;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t v[32];
-            tmem_ld32(ts + 32 * k, v);
-            tmem_wait_ld();
+        if (kMode != kPlain) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int j = 32 * k + e;
-              const float y = score<kMod>(a, __uint_as_float(v[e]), factor, slope, pos - (t0 + j), absent, j, window);
-              mx = fmaxf(mx, y);
-              v[e] = __float_as_uint(y);
+          for (int r = 0; r < 2; ++r) {
+            const float slope = slopes[at + 8 * r], base = -slope * static_cast<float>(pos[r] - t0 - 2 * quad);
+            const float m = kMode == kCap ? 1.f : factor[r];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+                  v[k][e + 2 * r + d] = __float_as_uint(fmaf(__uint_as_float(v[k][e + 2 * r + d]), m,
+                                                             fmaf(slope, static_cast<float>(64 * k + 2 * e + d), base)));
+              }
+          }
+        }
+        if (!whole) {
+          // column 64 k + 2 e + d + 2 quad (e a multiple of 4) against the row's ends; records of 16 that are absent
+          const int hi[2] = {pos[0] - t0 - 2 * quad, pos[1] - t0 - 2 * quad};
+          const int lo[2] = {a.window > 0 ? hi[0] + 1 - a.window : INT_MIN, a.window > 0 ? hi[1] + 1 - a.window : INT_MIN};
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const bool gone = (absent >> (8 * (4 * k + e / 8))) & 1u;
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                const int col = 64 * k + 2 * e + (d & 1), r = d >> 1;
+                if (gone || col > hi[r] || col < lo[r]) v[k][e + d] = 0xFF800000u;
+              }
             }
-            tmem_st32(ts + 32 * k, v);
-            tmem_wait_st();
-          }
         }
-        // ---- the maximum
-        const bool raise = mx > top + kRaise || (top == -CUDART_INF_F && mx > -CUDART_INF_F);
-        if (__any_sync(0xFFFFFFFFu, raise)) {
-          float alpha = 1.f;
-          if (raise) {
-            const float nc = fabsf(mx) < kBigScore ? kShift - mx : -mx;
-            alpha = top == -CUDART_INF_F ? 0.f : fast_exp2(nc - c);
-            top = mx;
-            c = nc;
-            sum *= alpha;
+        // ---- the rows' maxima, over the four lanes that share them
+        float mx[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float m0 = -CUDART_INF_F, m1 = m0;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            m0 = max3(m0, __uint_as_float(v[0][e + 2 * r]), __uint_as_float(v[0][e + 2 * r + 1]));
+            m1 = max3(m1, __uint_as_float(v[1][e + 2 * r]), __uint_as_float(v[1][e + 2 * r + 1]));
           }
-          if (any) {
+          mx[r] = fmaxf(m0, m1);
+        }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          const float x0 = __shfl_xor_sync(0xFFFFFFFFu, mx[0], d), x1 = __shfl_xor_sync(0xFFFFFFFFu, mx[1], d);
+          mx[0] = fmaxf(mx[0], x0);
+          mx[1] = fmaxf(mx[1], x1);
+        }
+        bool raise[2], big = false;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          mx[r] *= mul[r];
+          raise[r] = mx[r] > st.top[r] + kRaise || (st.top[r] == -CUDART_INF_F && mx[r] > -CUDART_INF_F);
+          big |= kMode == kPlain && fabsf(mx[r]) >= kBigScore;
+        }
+        if (__any_sync(0xFFFFFFFFu, raise[0] || raise[1] || big)) {
+          if (kMode == kPlain && __any_sync(0xFFFFFFFFu, big)) {
+            // scores so large that their rounded products could pass fp16's range are multiplied out
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[k][e] = __float_as_uint(__uint_as_float(v[k][e]) * mul[(e >> 1) & 1]);
+            mul[0] = mul[1] = 1.f;
+          }
+          float alpha[2] = {1.f, 1.f};
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (raise[r]) {
+              const float nc = fabsf(mx[r]) < kBigScore ? kShift - mx[r] : -mx[r];
+              alpha[r] = st.top[r] == -CUDART_INF_F ? 0.f : fast_exp2(nc - st.c[r]);
+              st.top[r] = mx[r];
+              st.c[r] = nc;
+              st.sum[r] *= alpha[r];
+            }
+          if (s > 0 && __any_sync(0xFFFFFFFFu, raise[0] || raise[1])) {
+            // the output so far in the new units, once the product before this one is in it (with two tiles it was when
+            // these scores were complete)
+            if (!both) {
+              if (!(ok = wait_warp(&bars[kBarPvDone + (b ^ 1)], ((jobs - 1) >> 1) & 1, abort_flag, a))) break;
+              tcgen05_after_sync();
+            }
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
-              uint32_t v[32];
-              tmem_ld32(to_x + 128 * x + 32 * k, v);
+              uint32_t u[16];
+              tmem_ld_16x256b_x4(lanes + kTmemO + 128 * t + 32 * k, u);
               tmem_wait_ld();
+              touch(u);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-              tmem_st32(to_x + 128 * x + 32 * k, v);
+              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha[(e >> 1) & 1]);
+              tmem_st_16x256b_x4(lanes + kTmemO + 128 * t + 32 * k, u);
             }
           }
         }
         // ---- weights
-        const float mul = plain ? factor : 1.f;
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t v[32], w[16];
-          tmem_ld32(ts + 32 * k, v);
-          tmem_wait_ld();
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float2 y = fma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), make_float2(mul, mul),
-                            make_float2(c, c));
+            const int r = e & 1;
+            float2 y = fma2(make_float2(__uint_as_float(v[k][2 * e]), __uint_as_float(v[k][2 * e + 1])), make_float2(mul[r], mul[r]),
+                            make_float2(st.c[r], st.c[r]));
             y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            if (e & 1) acc1 = add2(acc1, y); else acc0 = add2(acc0, y);
+            acc[r] = add2(acc[r], y);
             w[e] = pack_f16(y.x, y.y);
           }
-          tmem_st_32x32b_x16(ts + 16 * k, w);
+          tmem_st_16x128b_x8(ts + 32 * k, w);
         }
-        acc0 = add2(acc0, acc1);
-        sum += acc0.x + acc0.y;
-        any = true;
         tmem_wait_st();
         tcgen05_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarPFull + x]);
+        if (lane == 0) mbar_arrive(&bars[kBarPFull + b]);
+        st.sum[0] += acc[0].x + acc[0].y;
+        st.sum[1] += acc[1].x + acc[1].y;
+        if (both) {
+          const Rows x = st;
+          st = other;
+          other = x;
+        }
       }
       if (!ok) break;
-      // ---- the end of the piece
-      const bool has = both ? p.steps > 0 : p.steps > x;
-      if (has) {
-        if (!wait_warp(&bars[kBarOFull + x], outs++ & 1, abort_flag, a)) break;
+      // ---- the end of the piece: output rows, through the warp's part of the query operand (free once the products are
+      // done) so that they go to memory in one piece: 16 bytes c of row r lie at c ^ (r & 7)
+      if (steps > 0) {
+        // (the last product; the one two jobs before it was complete when its scores were)
+        if (!(ok = wait_warp(&bars[kBarPvDone + ((jobs - 1) & 1)], ((jobs - 1) >> 1) & 1, abort_flag, a))) break;
         tcgen05_after_sync();
       }
-      float fo = 1.f, fb = 0.f;                              // factors of this group's output, and of B's in a shared piece
-      bool join = false;
-      if (!both && p.steps > 1) {
-        if (x == 1) {
-          ml_b[own] = make_float2(sum > 0.f || sum != sum ? -c : -CUDART_INF_F, sum);
-          tcgen05_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kBarBDone]);
-          if (!wait_warp(&bars[kBarADone], joins++ & 1, abort_flag, a)) break;
-        } else {
-          if (!wait_warp(&bars[kBarBDone], joins++ & 1, abort_flag, a)) break;
-          tcgen05_after_sync();
-          join = true;
-          const float2 o = ml_b[own];
-          const float ma = sum > 0.f || sum != sum ? -c : -CUDART_INF_F;
-          const float m = fmaxf(ma, o.x);
-          fo = ma == -CUDART_INF_F ? 0.f : fast_exp2(ma - m);
-          fb = o.x == -CUDART_INF_F ? 0.f : fast_exp2(o.x - m);
-          sum = sum * fo + o.y * fb;
-          c = m == -CUDART_INF_F ? 0.f : -m;
-        }
-      }
-      if (both || x == 0) {
-        const size_t at = static_cast<size_t>(p.q0 + tok) * a.hq + h;
-        const size_t pr = (static_cast<size_t>(blockIdx.x) * 2 + max(p.slot, 0)) * a.part_rows + rr;
-        if (p.slot < 0) {
-          const float inv = sum == 0.f ? 0.f : a.v_factor / sum;
-          fo *= inv;
-          fb *= inv;
-        }
-#pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t v[32];
-          if (any) {
-            tmem_ld32(to_x + 128 * x + 32 * k, v);
-            tmem_wait_ld();
+      for (int t = 0; t < (both ? 2 : 1); ++t) {
+        const Piece& p = pieces[buf];
+        const int slot = p.slot, first = 128 * t + row16, live = min(16, p.rows - first);      // rows of this warp
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * a.part_rows;
+        uint8_t* stage = my_q(t);
+        float f[2];
+        long long to[2];                                      // this lane's rows' places in out and lse
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fo);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = 0u;
-          }
-          if (join) {
-            uint32_t u[32];
-            tmem_ld32(to_x + 128 + 32 * k, u);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(u[e]), fb, __uint_as_float(v[e])));
-          }
-          if (live) {
-            if (p.slot < 0) {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + at * ZF_HEAD_DIM + 32 * k);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t y[4];
-#pragma unroll
-                for (int f = 0; f < 4; ++f)
-                  y[f] = pack_bf16x2(__uint_as_float(v[8 * e + 2 * f]), __uint_as_float(v[8 * e + 2 * f + 1]));
-                dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
-              }
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(a.part_o + pr * ZF_HEAD_DIM + 32 * k);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) dst[e] = make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-            }
-          }
-        }
-        if (live) {
+        for (int r = 0; r < 2; ++r) {
+          const int row = p.row0 + min(first + (lane >> 2) + 8 * r, p.rows - 1), tok = row / a.group;
+          to[r] = static_cast<long long>(p.q0 + tok) * a.hq + p.g * a.group + (row - tok * a.group);
+          float sum = st.sum[r];
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
           const bool none = sum == 0.f;
-          if (p.slot < 0) a.lse[at] = none ? -CUDART_INF_F : (log2f(sum) - c) * kLn2f;
-          else a.part_ml[pr] = make_float2(none ? -CUDART_INF_F : -c, sum);
+          f[r] = slot >= 0 ? 1.f : none ? 0.f : a.v_factor / sum;
+          if (quad == 0 && (lane >> 2) + 8 * r < live) {
+            if (slot < 0) a.lse[to[r]] = none ? -CUDART_INF_F : (log2f(sum) - st.c[r]) * kLn2f;
+            else a.part_ml[part + first + (lane >> 2) + 8 * r] = make_float2(none ? -CUDART_INF_F : -st.c[r], sum);
+          }
         }
-        if (join) {
-          tcgen05_before_sync();
+        // 32 columns: rows lane / 4 (+ 8), columns 8 i + 2 quad (+ 1)
+        auto columns = [&](int k, uint32_t (&u)[16]) {
+          if (steps > 0) {
+            tmem_ld_16x256b_x4(lanes + kTmemO + 128 * t + 32 * k, u);
+            tmem_wait_ld();
+            touch(u);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) u[e] = steps > 0 ? __float_as_uint(__uint_as_float(u[e]) * f[(e >> 1) & 1]) : 0u;
+        };
+        if (slot < 0) {
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t u[16];
+            columns(k, u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                *reinterpret_cast<uint32_t*>(stage + ((lane >> 2) + 8 * r) * 256 + (((4 * k + i) ^ (lane >> 2)) * 16) + quad * 4) =
+                    pack_bf16x2(__uint_as_float(u[4 * i + 2 * r]), __uint_as_float(u[4 * i + 2 * r + 1]));
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kBarADone]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 2 * i + (lane >> 4);
+            const long long place = __shfl_sync(0xFFFFFFFFu, to[i >> 2], (row & 7) * 4);
+            if (row < live)
+              reinterpret_cast<uint4*>(a.out + place * ZF_HEAD_DIM)[lane & 15] =
+                  *reinterpret_cast<const uint4*>(stage + row * 256 + (((lane & 15) ^ (row & 7)) * 16));
+          }
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {
+            uint32_t u[16];
+            columns(k, u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if ((lane >> 2) + 8 * r < live)
+                  *reinterpret_cast<uint2*>(a.part_o + (part + first + (lane >> 2) + 8 * r) * ZF_HEAD_DIM + 32 * k + 8 * i + 2 * quad) =
+                      make_uint2(u[4 * i + 2 * r], u[4 * i + 2 * r + 1]);
+          }
         }
+        st = other;
       }
       tcgen05_before_sync();
-      gs += p.steps;
-      __syncwarp();
+      gs += steps;
+      // ---- the next piece
+      if (!(ok = wait_warp(&bars[kBarPieceFull + (buf ^ 1)], ((n + 1) >> 1) & 1, abort_flag, a))) break;
       if (lane == 0) mbar_arrive(&bars[kBarPieceEmpty + buf]);
+      if (pieces[buf ^ 1].b >= 0 && pieces[buf ^ 1].steps > 0) q_rows(buf ^ 1);
     }
   }
 
@@ -1103,6 +1209,11 @@ extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, i
   int sms = 0;
   if ((st = sm_count(&sms)) != ZF_OK) return st;
   const ChunkPlan p = chunk_plan(rows, num_q_heads / c->num_kv_heads, sms);
+  // the steps of all units, and what a unit is charged besides, are counted with 32 bits
+  const long long units = static_cast<long long>(rows) * (num_q_heads / c->num_kv_heads) / kUnitRows + batch;
+  if (units * c->num_kv_heads >= INT_MAX ||
+      units * c->num_kv_heads * (static_cast<long long>(max_pages) * c->page_size / kStep + 1 + kUnitCost) >= INT_MAX)
+    return ZF_ERR_UNSUPPORTED;
   if (workspace_bytes < p.bytes()) return ZF_ERR_WORKSPACE_TOO_SMALL;
 
   ChunkArgs a{};
@@ -1131,7 +1242,7 @@ extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, i
   a.window = window;
   a.scale_log2 = scale_log2;
   a.cap_log2 = softcap * kLog2e;
-  a.inv_cap = softcap > 0.f ? 1.f / a.cap_log2 : 0.f;
+  a.two_over_cap = softcap > 0.f ? 2.f / softcap : 0.f;
   a.v_factor = c->v_scale * kQ4ScaleFactor;
   a.wait_limit_ns = kWaitTimeoutNs;
 
@@ -1143,16 +1254,20 @@ extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, i
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-      for (const auto kernel : {q4_chunk_kernel<false>, q4_chunk_kernel<true>})
+      for (const auto kernel : {q4_chunk_kernel<kPlain>, q4_chunk_kernel<kSlope>, q4_chunk_kernel<kCap>}) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmTotal) != cudaSuccess)
           return ZF_ERR_CUDA;
+        // the warpgroups' shares are those of a launch with kRegs registers per thread
+        cudaFuncAttributes attr;
+        if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess) return ZF_ERR_CUDA;
+        if (attr.numRegs != kRegs) return ZF_ERR_UNSUPPORTED;
+      }
       ready[dev] = true;
     }
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool mod = softcap > 0.f || slopes != nullptr;
-  st = mod ? launch(q4_chunk_kernel<true>, dim3(p.grid), kThreads, kSmTotal, s, a)
-           : launch(q4_chunk_kernel<false>, dim3(p.grid), kThreads, kSmTotal, s, a);
+  const auto kernel = softcap > 0.f ? q4_chunk_kernel<kCap> : slopes ? q4_chunk_kernel<kSlope> : q4_chunk_kernel<kPlain>;
+  st = launch(kernel, dim3(p.grid), kThreads, kSmTotal, s, a);
   if (st != ZF_OK) return st;
   return launch(q4_chunk_join_kernel, dim3(p.grid, p.part_rows / kJoinRows), 512, 0, s, a, p.grid);
 }
