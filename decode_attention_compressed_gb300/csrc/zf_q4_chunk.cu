@@ -134,12 +134,11 @@ constexpr uint32_t kIdescO = kIdescS | (1u << 16);
 
 // Shared-memory descriptors without swizzle of [128][128] operands in core matrices (8 rows x 16 bytes, 128
 // contiguous bytes), rows' cores 2048 bytes apart, columns' 128.  K-major (columns along K): leading offset
-// 128, stride offset 2048.  MN-major (rows along K): leading offset (along K) 2048, stride offset (along N) 128.
-__device__ __forceinline__ uint64_t desc_k(const void* p) { return umma_desc_kmajor(p); }
-__device__ __forceinline__ uint64_t desc_mn(const void* p) {
-  return static_cast<uint64_t>((smem_addr(p) & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(2048 >> 4) << 16) |
-         (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
-}
+// 128, stride offset 2048.  MN-major (rows along K): leading offset (along K) 2048, stride offset (along N) 128.  The low
+// half holds the address and the leading offset (in units of 16 bytes), the high half the stride offset and the version.
+constexpr uint32_t kDescHighK = (2048 >> 4) | (1u << 14), kDescHighMn = (128 >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((128u >> 4) << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | ((2048u >> 4) << 16); }
 
 template <int kN>
 __device__ __forceinline__ void take_registers() {
@@ -152,38 +151,29 @@ __device__ __forceinline__ void give_registers() {
 
 // The MMA warp's issue forms (the whole warp calls, one lane issues: from a branch of one lane an instruction takes
 // about 120 cycles, more than the tensor cores need for it): S = Q K^T over 128 channels, O += P V over 128 tokens.
-__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b) {
-  asm volatile(
-      "{\n\t.reg .pred e, f, t;\n\t.reg .b64 x, y;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n\t"
-      "add.s64 x, %1, 16;\n\tadd.s64 y, %2, 16;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, %1, 32;\n\tadd.s64 y, %2, 32;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, %1, 48;\n\tadd.s64 y, %2, 48;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, %1, 64;\n\tadd.s64 y, %2, 64;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, %1, 80;\n\tadd.s64 y, %2, 80;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, %1, 96;\n\tadd.s64 y, %2, 96;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t"
-      "add.s64 x, %1, 112;\n\tadd.s64 y, %2, 112;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, t;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdescS)
-      : "memory");
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (uint32_t e = 0; e < 8; ++e)
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 x, y;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 x, {%1, %4};\n\tmov.b64 y, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a + 16 * e), "r"(b + 16 * e), "r"(kIdescS), "r"(kDescHighK), "r"(e > 0 ? 1u : 0u)
+        : "memory");
 }
-__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {
-  static_assert(2 * kCoreRow / 16 == 256, "descriptor steps");
-  asm volatile(
-      "{\n\t.reg .pred e, f, t;\n\t.reg .b64 y;\n\t.reg .b32 x;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
-      "add.u32 x, %1, 8;\n\tadd.s64 y, %2, 256;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
-      "add.u32 x, %1, 16;\n\tadd.s64 y, %2, 512;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
-      "add.u32 x, %1, 24;\n\tadd.s64 y, %2, 768;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
-      "add.u32 x, %1, 32;\n\tadd.s64 y, %2, 1024;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
-      "add.u32 x, %1, 40;\n\tadd.s64 y, %2, 1280;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
-      "add.u32 x, %1, 48;\n\tadd.s64 y, %2, 1536;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t"
-      "add.u32 x, %1, 56;\n\tadd.s64 y, %2, 1792;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], y, %3, t;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kIdescO), "r"(acc)
-      : "memory");
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t a, uint32_t b, uint32_t acc) {
+#pragma unroll
+  for (uint32_t e = 0; e < 8; ++e)
+    asm volatile(
+        "{\n\t.reg .pred e, p;\n\t.reg .b64 y;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 y, {%2, %4};\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a + 8 * e), "r"(b + 2 * kCoreRow / 16 * e), "r"(kIdescO), "r"(kDescHighMn), "r"(e > 0 ? 1u : acc)
+        : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile(
@@ -664,12 +654,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     uint32_t gs = 0, gj = 0;                      // steps and jobs before this piece
     uint32_t rows_seen = 0;                       // pieces whose query rows were waited for
     uint32_t fed = 0;                             // operands waited for
+    const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), sm = __shfl_sync(0xFFFFFFFFu, smem_addr(smem), 0);
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int buf = n & 1;
       if (!wait_warp(&bars[kBarPieceFull + buf], (n >> 1) & 1, abort_flag, a)) break;
-      const int pb = pieces[buf].b, steps = pieces[buf].steps;
-      const bool both = pieces[buf].rows > 128;
+      // (the shuffles tell the compiler that these are the same in all lanes: descriptors then stay in uniform registers)
+      const int pb = __shfl_sync(0xFFFFFFFFu, pieces[buf].b, 0), steps = __shfl_sync(0xFFFFFFFFu, pieces[buf].steps, 0);
+      const bool both = __shfl_sync(0xFFFFFFFFu, pieces[buf].rows, 0) > 128;
       if (pb < 0) break;
       if (steps > 0 && !wait_warp(&bars[kBarQFull], rows_seen++ & 1, abort_flag, a)) break;
       tcgen05_after_sync();
@@ -685,8 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         const uint32_t k = 2 * (gs + (both ? j >> 1 : j)), b = (gj + j) & 1;
         if (!operand(k)) return false;
         tcgen05_after_sync();
-        mma_scores(tmem + kTmemS + 128 * b, desc_k(smem + kSmQ + (both && (j & 1) ? kOperand : 0)),
-                   desc_k(smem + kSmRing + (k % kRing) * kOperand));
+        mma_scores(tm + kTmemS + 128 * b, desc_k(sm + kSmQ + (both && (j & 1) ? kOperand : 0)),
+                   desc_k(sm + kSmRing + (k % kRing) * kOperand));
         commit(&bars[kBarSFull + b]);
         if (!both || (j & 1)) commit(&bars[kBarOpEmpty + k % kRing]);
         return true;
@@ -696,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         if (!operand(k)) return false;
         if (!wait_warp(&bars[kBarPFull + b], ((gj + j) >> 1) & 1, abort_flag, a)) return false;
         tcgen05_after_sync();
-        mma_weights(tmem + kTmemO + (both && (j & 1) ? 128 : 0), tmem + kTmemS + 128 * b,
-                    desc_mn(smem + kSmRing + (k % kRing) * kOperand), j > (both ? 1 : 0));
+        mma_weights(tm + kTmemO + (both && (j & 1) ? 128 : 0), tm + kTmemS + 128 * b,
+                    desc_mn(sm + kSmRing + (k % kRing) * kOperand), j > (both ? 1 : 0));
         commit(&bars[kBarPvDone + b]);
         if (!both || (j & 1)) commit(&bars[kBarOpEmpty + k % kRing]);
         return true;
