@@ -420,6 +420,23 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// The columns 8 i + d (i < 16, d < 2) that are at most h, or all; bit 2 i + d.
+__device__ __forceinline__ uint32_t bits_to(int h) {
+  if (h < 0) return 0u;
+  const int n = 2 * (h >> 3) + min((h & 7) + 1, 2);
+  return n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+// Of them those that a row sees, whose position is at column hi: not more than `window` back (0: all), and of records
+// (16 columns, a byte each) that are not absent.
+__device__ __forceinline__ uint32_t seen_bits(int hi, int window, uint64_t absent) {
+  uint32_t m = bits_to(hi);
+  if (window > 0) m &= ~bits_to(hi - window);
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if ((absent >> (8 * r)) & 1u) m &= ~(0xFu << (4 * r));
+  return m;
+}
+
 // What becomes of the scores: nothing; slopes; a cap, and slopes if there are any.
 enum : int { kPlain = 0, kSlope = 1, kCap = 2 };
 
@@ -649,13 +666,34 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
   } else if (warp == kMmaWarp) {
     // ================================================================== products
     // Job j of a piece: the scores of a tile of 128 rows and a step, and the product of their weights.  More than 128
-    // rows: job j is tile j % 2 and step j / 2, else step j of the one tile.  The next job's scores are computed while
-    // the softmax has one job's, the one after it once the product that frees their buffer is issued.
-    uint32_t gs = 0, gj = 0;                      // steps and jobs before this piece
-    uint32_t rows_seen = 0;                       // pieces whose query rows were waited for
-    uint32_t fed = 0;                             // operands waited for
+    // rows: the tiles take turns, each with a buffer of its own; else the one tile's steps alternate between the
+    // buffers.  The next job's scores are computed while the softmax has one job's, the one after it once the product
+    // that frees their buffer is issued.  Nothing but issuing happens here: waits, commits and instructions cost this
+    // warp more cycles than the tensor cores take for a job if they are not few.
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), sm = __shfl_sync(0xFFFFFFFFu, smem_addr(smem), 0);
+    const uint32_t q0 = desc_k(sm + kSmQ), q1 = desc_k(sm + kSmQ + kOperand);
+    const uint32_t k0 = desc_k(sm + kSmRing), v0 = desc_mn(sm + kSmRing);
+    struct Next {                                 // the ring's next K or V: slot, and parity of its phase
+      int slot;
+      uint32_t turn;
+    } key{0, 0}, value{1, 0};
+    uint32_t phase = 0;                           // parity of the next weights in each buffer
+    uint32_t rows_seen = 0;                       // pieces whose query rows were waited for
     bool ok = true;
+    // Waits until the next K or V is decoded; at: its slot.  (K and V alternate in the ring, so each moves two on; the
+    // phase before was complete when the operand before it in the slot had been used.)
+    auto operand = [&](Next& next, int& at) {
+      at = next.slot;
+      const bool good = wait_warp(&bars[kBarOpFull + at], next.turn, abort_flag, a);
+      if (at > 0) next.turn ^= 1;
+      next.slot = at == 0 ? 2 : at - 1;
+      return good;
+    };
+    auto weights_ready = [&](int b) {
+      const bool good = wait_warp(&bars[kBarPFull + b], (phase >> b) & 1, abort_flag, a);
+      phase ^= 1u << b;
+      return good;
+    };
     for (int n = 0; ok; ++n) {
       const int buf = n & 1;
       if (!wait_warp(&bars[kBarPieceFull + buf], (n >> 1) & 1, abort_flag, a)) break;
@@ -664,40 +702,59 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       const bool both = __shfl_sync(0xFFFFFFFFu, pieces[buf].rows, 0) > 128;
       if (pb < 0) break;
       if (steps > 0 && !wait_warp(&bars[kBarQFull], rows_seen++ & 1, abort_flag, a)) break;
-      tcgen05_after_sync();
-      const int N = both ? 2 * steps : steps;
-      auto operand = [&](uint32_t k) -> bool {     // operand k of the ring (they come in order)
-        while (fed <= k) {
-          if (!wait_warp(&bars[kBarOpFull + fed % kRing], (fed / kRing) & 1, abort_flag, a)) return false;
-          ++fed;
+      int k = 0, v = 0;
+      if (steps > 0 && both) {
+        if (!(ok = operand(key, k))) break;
+        tcgen05_after_sync();
+        mma_scores(tm + kTmemS, q0, k0 + k * (kOperand / 16));
+        commit(&bars[kBarSFull]);
+        mma_scores(tm + kTmemS + 128, q1, k0 + k * (kOperand / 16));
+        commit(&bars[kBarSFull + 1]);
+        commit(&bars[kBarOpEmpty + k]);
+        for (int s = 0; s < steps; ++s) {
+          const bool more = s + 1 < steps;
+          if (!(ok = operand(value, v) && weights_ready(0))) break;
+          tcgen05_after_sync();
+          mma_weights(tm + kTmemO, tm + kTmemS, v0 + v * (kOperand / 16), s > 0);
+          if (more) {
+            if (!(ok = operand(key, k))) break;
+            tcgen05_after_sync();
+            mma_scores(tm + kTmemS, q0, k0 + k * (kOperand / 16));
+            commit(&bars[kBarSFull]);
+          }
+          if (!(ok = weights_ready(1))) break;
+          tcgen05_after_sync();
+          mma_weights(tm + kTmemO + 128, tm + kTmemS + 128, v0 + v * (kOperand / 16), s > 0);
+          commit(&bars[kBarOpEmpty + v]);
+          if (more) {
+            mma_scores(tm + kTmemS + 128, q1, k0 + k * (kOperand / 16));
+            commit(&bars[kBarSFull + 1]);
+            commit(&bars[kBarOpEmpty + k]);
+          }
         }
-        return true;
-      };
-      auto scores = [&](int j) -> bool {
-        const uint32_t k = 2 * (gs + (both ? j >> 1 : j)), b = (gj + j) & 1;
-        if (!operand(k)) return false;
-        tcgen05_after_sync();
-        mma_scores(tm + kTmemS + 128 * b, desc_k(sm + kSmQ + (both && (j & 1) ? kOperand : 0)),
-                   desc_k(sm + kSmRing + (k % kRing) * kOperand));
-        commit(&bars[kBarSFull + b]);
-        if (!both || (j & 1)) commit(&bars[kBarOpEmpty + k % kRing]);
-        return true;
-      };
-      auto product = [&](int j) -> bool {
-        const uint32_t k = 2 * (gs + (both ? j >> 1 : j)) + 1, b = (gj + j) & 1;
-        if (!operand(k)) return false;
-        if (!wait_warp(&bars[kBarPFull + b], ((gj + j) >> 1) & 1, abort_flag, a)) return false;
-        tcgen05_after_sync();
-        mma_weights(tm + kTmemO + (both && (j & 1) ? 128 : 0), tm + kTmemS + 128 * b,
-                    desc_mn(sm + kSmRing + (k % kRing) * kOperand), j > (both ? 1 : 0));
-        commit(&bars[kBarPvDone + b]);
-        if (!both || (j & 1)) commit(&bars[kBarOpEmpty + k % kRing]);
-        return true;
-      };
-      for (int j = 0; ok && j < min(N, 2); ++j) ok = scores(j);
-      for (int j = 0; ok && j < N; ++j) ok = product(j) && (j + 2 >= N || scores(j + 2));
-      gs += steps;
-      gj += N;
+        if (!ok) break;
+        commit(&bars[kBarPvDone]);
+      } else if (steps > 0) {
+        // (the keys of step s take the place of the values of step s - 2)
+        for (int s = 0; s < steps + 2; ++s) {
+          const int b = s & 1;
+          if (s >= 2) {
+            if (!(ok = operand(value, v) && weights_ready(b))) break;
+            tcgen05_after_sync();
+            mma_weights(tm + kTmemO, tm + kTmemS + 128 * b, v0 + v * (kOperand / 16), s > 2);
+            commit(&bars[kBarPvDone + b]);
+            commit(&bars[kBarOpEmpty + v]);
+          }
+          if (s < steps) {
+            if (!(ok = operand(key, k))) break;
+            tcgen05_after_sync();
+            mma_scores(tm + kTmemS + 128 * b, q0, k0 + k * (kOperand / 16));
+            commit(&bars[kBarSFull + b]);
+            commit(&bars[kBarOpEmpty + k]);
+          }
+        }
+        if (!ok) break;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarPieceEmpty + buf]);
     }
@@ -761,7 +818,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     float* factors = reinterpret_cast<float*>(smem + kSmScale);
     int* positions = reinterpret_cast<int*>(smem + kSmPos);
     float* slopes = reinterpret_cast<float*>(smem + kSmSlope);
-    uint32_t gs = 0, jobs = 0;                                // steps and jobs before
+    uint32_t gs = 0;                                          // steps before this piece
+    uint32_t phase = 0, done = 0;                             // parity of the next scores in a buffer; of the products' next end
     // The warp's 16 rows of tile t of the query operand: 4 KB that no other warp writes.
     auto my_q = [&](int t) { return smem + kSmQ + t * kOperand + (row16 >> 3) * kCoreRow; };
 
@@ -833,10 +891,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       const bool both = pieces[buf].rows > 128;
       const int steps = pieces[buf].steps, step0 = pieces[buf].step0, count = both ? 2 * steps : steps;
       Rows st{{-CUDART_INF_F, -CUDART_INF_F}, {0.f, 0.f}, {0.f, 0.f}, 0, 0}, other = st;
-      for (int j = 0; j < count; ++j, ++jobs) {
-        const uint32_t b = jobs & 1, ts = lanes + kTmemS + 128 * b;
+      for (int j = 0; j < count; ++j) {
+        const uint32_t b = j & 1, ts = lanes + kTmemS + 128 * b;
         const int t = both ? j & 1 : 0, s = both ? j >> 1 : j;
-        if (!(ok = wait_warp(&bars[kBarSFull + b], (jobs >> 1) & 1, abort_flag, a))) break;
+        if (!(ok = wait_warp(&bars[kBarSFull + b], (phase >> b) & 1, abort_flag, a))) break;
+        phase ^= 1u << b;
         tcgen05_after_sync();
         uint32_t v[2][32];
         tmem_ld_16x256b_x8(ts, v[0]);
@@ -849,8 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         }
         const float factor[2] = {factors[at], factors[at + 8]};
         const int t0 = (step0 + s) * kStep;
-        const uint64_t absent = *reinterpret_cast<volatile uint64_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8);
-        const bool whole = absent == 0 && t0 + kStep <= st.seen_end && t0 >= st.seen_begin;
+        const bool whole = *reinterpret_cast<volatile uint64_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8) == 0 && t0 + kStep <= st.seen_end && t0 >= st.seen_begin;
         float mul[2] = {kMode == kPlain ? factor[0] : 1.f, kMode == kPlain ? factor[1] : 1.f};      // scores are mul * v
         tmem_wait_ld();
         touch(v[0]);
@@ -881,20 +939,17 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           }
         }
         if (!whole) {
-          // column 64 k + 2 e + d + 2 quad (e a multiple of 4) against the row's ends; records of 16 that are absent
-          const int hi[2] = {pos[0] - t0 - 2 * quad, pos[1] - t0 - 2 * quad};
-          const int lo[2] = {a.window > 0 ? hi[0] + 1 - a.window : INT_MIN, a.window > 0 ? hi[1] + 1 - a.window : INT_MIN};
+          const uint64_t absent = *reinterpret_cast<volatile uint64_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
+          for (int r = 0; r < 2; ++r) {
+            const int hi = pos[r] - t0 - 2 * quad;
+            const uint32_t m = seen_bits(hi, a.window, absent);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const bool gone = (absent >> (8 * (4 * k + e / 8))) & 1u;
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int d = 0; d < 4; ++d) {
-                const int col = 64 * k + 2 * e + (d & 1), r = d >> 1;
-                if (gone || col > hi[r] || col < lo[r]) v[k][e + d] = 0xFF800000u;
-              }
-            }
+              for (int n = 0; n < 16; ++n)
+                if (!(m & (1u << (16 * k + n)))) v[k][4 * (n >> 1) + 2 * r + (n & 1)] = 0xFF800000u;
+          }
         }
         // ---- the rows' maxima, over the four lanes that share them
         float mx[2];
@@ -942,9 +997,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
             }
           if (s > 0 && __any_sync(0xFFFFFFFFu, raise[0] || raise[1])) {
             // the output so far in the new units, once the product before this one is in it (with two tiles it was when
-            // these scores were complete)
+            // these scores were complete; with one the product before that was, so its barrier is in this phase or past it)
             if (!both) {
-              if (!(ok = wait_warp(&bars[kBarPvDone + (b ^ 1)], ((jobs - 1) >> 1) & 1, abort_flag, a))) break;
+              if (!(ok = wait_warp(&bars[kBarPvDone + (b ^ 1)], ((done >> (b ^ 1)) & 1) ^ 1, abort_flag, a))) break;
               tcgen05_after_sync();
             }
 #pragma unroll 1
@@ -985,14 +1040,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           const Rows x = st;
           st = other;
           other = x;
+        } else {
+          done ^= 1u << b;
         }
       }
       if (!ok) break;
       // ---- the end of the piece: output rows, through the warp's part of the query operand (free once the products are
       // done) so that they go to memory in one piece: 16 bytes c of row r lie at c ^ (r & 7)
       if (steps > 0) {
-        // (the last product; the one two jobs before it was complete when its scores were)
-        if (!(ok = wait_warp(&bars[kBarPvDone + ((jobs - 1) & 1)], ((jobs - 1) >> 1) & 1, abort_flag, a))) break;
+        // (two tiles: announced once; one: for every step, and the one two before was complete when its scores were)
+        if (both) done ^= 1u;
+        const uint32_t b = both ? 0 : (count - 1) & 1;
+        if (!(ok = wait_warp(&bars[kBarPvDone + b], ((done >> b) & 1) ^ 1, abort_flag, a))) break;
         tcgen05_after_sync();
       }
       for (int t = 0; t < (both ? 2 : 1); ++t) {
