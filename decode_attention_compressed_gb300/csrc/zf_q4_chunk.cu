@@ -47,9 +47,15 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kDecodeWarp0 = 8, kDecodeWarps = 8;
 constexpr int kMmaWarp = 16, kWalkWarp = 17;       // (18 and 19 fill up a warpgroup)
-// Registers per thread: the launch's, and what the softmax, decode and other warpgroups (4 warps) make of them.
-constexpr int kRegs = 96, kRegsSoftmax = 128, kRegsDecode = 72, kRegsOther = 80;
-static_assert(2 * kRegsSoftmax + 2 * kRegsDecode + kRegsOther <= 5 * kRegs, "a larger sum would wait for registers forever");
+// Registers per thread: the launch's, and what the softmax, decode and other warpgroups (4 warps) make of them; a cap
+// takes a few more in the softmax (564 us instead of 624 for the workload with a window and a cap), where the others do
+// with fewer (a long context 3343 us with 144 / 56 / 80, 3385 with 128 / 72 / 80).
+constexpr int kRegs = 96, kRegsDecode = 56;
+constexpr int regs_softmax(int mode) { return mode & 2 ? 152 : 144; }
+constexpr int regs_other(int mode) { return mode & 2 ? 64 : 80; }
+static_assert(2 * regs_softmax(0) + 2 * kRegsDecode + regs_other(0) <= 5 * kRegs &&
+                  2 * regs_softmax(2) + 2 * kRegsDecode + regs_other(2) <= 5 * kRegs,
+              "a larger sum would wait for registers forever");
 constexpr int kStep = 128;                       // tokens per step: of the operands
 constexpr int kUnitRows = 256;                   // query rows per unit
 constexpr int kStages = 3;                       // steps of records in flight
@@ -119,7 +125,9 @@ constexpr int kSmRec = kSmQ + 2 * kOperand;
 constexpr int kSmScale = kSmRec + kStages * 8 * kQ4Record;     // [2][256] score factors of the rows
 constexpr int kSmPos = kSmScale + 2 * kUnitRows * 4;           // [2][256] their positions
 constexpr int kSmSlope = kSmPos + 2 * kUnitRows * 4;           // [2][256] their slopes
-constexpr int kSmPiece = kSmSlope + 2 * kUnitRows * 4;         // [2] Piece
+constexpr int kSmPlace = kSmSlope + 2 * kUnitRows * 4;         // [2][256] their places among the rows of q and out
+constexpr int kSmWhole = kSmPlace + 2 * kUnitRows * 4;         // [2][2][8] int2: steps that all rows of a warp see whole
+constexpr int kSmPiece = kSmWhole + 2 * 2 * 8 * 8;             // [2] Piece
 constexpr int kSmAbsent = kSmPiece + 2 * 48;                   // [8 steps][8 records] 1: no tokens there
 constexpr int kSmBars = kSmAbsent + 64;
 constexpr int kSmMisc = kSmBars + kNumBars * 8;                // abort flag, tensor-memory base, range
@@ -437,7 +445,7 @@ __device__ __forceinline__ uint32_t seen_bits(int hi, int window, uint64_t absen
   return m;
 }
 
-// What becomes of the scores: nothing; slopes; a cap, and slopes if there are any.
+// What becomes of the scores: nothing, or a cap, slopes, or both.
 enum : int { kPlain = 0, kSlope = 1, kCap = 2 };
 
 template <int kMode>
@@ -531,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
   Piece* pieces = reinterpret_cast<Piece*>(smem + kSmPiece);
   // (a warpgroup's warps run one setmaxnreg together, so it stands before their ways part)
   if (warp >= kMmaWarp) {
-  give_registers<kRegsOther>();
+  give_registers<regs_other(kMode)>();
   if (warp == kWalkWarp) {
     // ================================================================== walk and copies
     const uint64_t policy = l2_evict_first_policy();
@@ -809,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     }
   } else {
     // ================================================================== softmax
-    take_registers<kRegsSoftmax>();
+    take_registers<regs_softmax(kMode)>();
     // All eight warps work on the same job, 16 rows of its tile each (warps w and w + 4 share the lanes that they can
     // reach): a lane has rows lane / 4 and lane / 4 + 8 of them, and columns 8 i + 2 (lane % 4), + 1.
     const int row16 = 32 * (warp & 3) + 16 * (warp >> 2);     // the warp's first row in a tile
@@ -818,36 +826,59 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     float* factors = reinterpret_cast<float*>(smem + kSmScale);
     int* positions = reinterpret_cast<int*>(smem + kSmPos);
     float* slopes = reinterpret_cast<float*>(smem + kSmSlope);
+    int* places = reinterpret_cast<int*>(smem + kSmPlace);
+    auto whole_of = [&](int buf, int t) -> int2& { return reinterpret_cast<int2*>(smem + kSmWhole)[(buf * 2 + t) * 8 + warp]; };
     uint32_t gs = 0;                                          // steps before this piece
     uint32_t phase = 0, done = 0;                             // parity of the next scores in a buffer; of the products' next end
     // The warp's 16 rows of tile t of the query operand: 4 KB that no other warp writes.
     auto my_q = [&](int t) { return smem + kSmQ + t * kOperand + (row16 >> 3) * kCoreRow; };
 
-    // Query rows of a piece, 16 of each tile: lane (row lane % 8 of 8, chunks lane / 8 + 4 i of 16 bytes).
-    auto q_rows = [&](int buf) {
+    // Query rows of a piece, 16 of each tile: lane (row lane % 8 of 8, chunks lane / 8 + 4 i of 16 bytes).  They are read
+    // while the piece before ends.
+    uint4 qv[2][2][4];
+    auto q_load = [&](int buf) {
       const Piece& p = pieces[buf];
-      const bool negate = a.scale_log2 < 0.f;
       const int tiles = p.rows > 128 ? 2 : 1;
-      for (int t = 0; t < tiles; ++t) {
-        uint4 v[2][4];
-        int at[2], tok[2], h[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t >= tiles) break;
+        int low = INT_MAX, high = INT_MIN;
 #pragma unroll
         for (int r8 = 0; r8 < 2; ++r8) {
-          at[r8] = 128 * t + row16 + 8 * r8 + (lane & 7);
-          const bool in = at[r8] < p.rows;
-          const int row = p.row0 + min(at[r8], p.rows - 1);
-          tok[r8] = row / a.group;
-          h[r8] = p.g * a.group + (row - tok[r8] * a.group);
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(p.q0 + tok[r8]) * a.hq + h[r8]) * ZF_HEAD_DIM);
+          const int at = 128 * t + row16 + 8 * r8 + (lane & 7);
+          const bool in = at < p.rows;
+          const int row = p.row0 + min(at, p.rows - 1), tok = row / a.group, h = p.g * a.group + (row - tok * a.group);
+          const int place = (p.q0 + tok) * a.hq + h;
+          const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(place) * ZF_HEAD_DIM);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[r8][i] = in ? src[(lane >> 3) + 4 * i] : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i) qv[t][r8][i] = in ? src[(lane >> 3) + 4 * i] : make_uint4(0u, 0u, 0u, 0u);
+          low = min(low, p.pos0 + tok);
+          high = max(high, p.pos0 + tok);
+          if (lane < 8) {
+            positions[buf * kUnitRows + at] = p.pos0 + tok;
+            places[buf * kUnitRows + at] = place;
+            if (kMode & kSlope) slopes[buf * kUnitRows + at] = a.slopes[h] * kLog2e;
+          }
         }
+        // steps from the first that no row's window cuts to the one that ends at the first row's position or before
+        low = __reduce_min_sync(0xFFFFFFFFu, low);
+        high = __reduce_max_sync(0xFFFFFFFFu, high);
+        const int begin = a.window > 0 ? (max(high + 1 - a.window, 0) + kStep - 1) / kStep : 0;
+        if (lane == 0) whole_of(buf, t) = make_int2(begin, max((low + 1) / kStep - begin, 0));
+      }
+    };
+    auto q_store = [&](int buf) {
+      const int tiles = pieces[buf].rows > 128 ? 2 : 1;
+      const bool negate = a.scale_log2 < 0.f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (t >= tiles) break;
 #pragma unroll
         for (int r8 = 0; r8 < 2; ++r8) {
           uint32_t big = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint4 x = v[r8][i];
+            const uint4 x = qv[t][r8][i];
             const uint32_t m2 = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
             big = max(big, max(m2 & 0xFFFFu, m2 >> 16));
           }
@@ -857,14 +888,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           // the largest raw score has the largest score: a negative scale negates the row)
           const int k = min(138 - static_cast<int>(big >> 7), 126);
           const float f = __int_as_float(((127 + k) << 23) | (negate ? 0x80000000 : 0));
-          if (lane < 8) {
-            factors[buf * kUnitRows + at[r8]] = fmaxf(__int_as_float((127 - k) << 23) * fabsf(a.scale_log2), 1e-37f);
-            positions[buf * kUnitRows + at[r8]] = p.pos0 + tok[r8];
-            if (kMode != kPlain) slopes[buf * kUnitRows + at[r8]] = a.slopes ? a.slopes[h[r8]] * kLog2e : 0.f;
-          }
+          if (lane < 8)
+            factors[buf * kUnitRows + 128 * t + row16 + 8 * r8 + lane] =
+                fmaxf(__int_as_float((127 - k) << 23) * fabsf(a.scale_log2), 1e-37f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {v[r8][i].x, v[r8][i].y, v[r8][i].z, v[r8][i].w};
+            const uint32_t w[4] = {qv[t][r8][i].x, qv[t][r8][i].y, qv[t][r8][i].z, qv[t][r8][i].w};
             uint32_t y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = pack_f16(bf16lo_to_f32(w[e]) * f, bf16hi_to_f32(w[e]) * f);
@@ -880,17 +909,20 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
 
     // What a lane keeps of its two rows of a tile.
     struct Rows {
-      float top[2], c[2], sum[2];                             // maximum, -maximum + shift (log2 units), sum of weights
-      int seen_begin, seen_end;                               // positions that all rows of the warp see
+      float c[2], sum[2];                                     // shift - maximum (log2 units), sum of weights
     };
+    constexpr float kNone = 1e30f;                            // c before the first score that is seen
     bool ok = wait_warp(&bars[kBarPieceFull], 0, abort_flag, a);
-    if (ok && pieces[0].b >= 0 && pieces[0].steps > 0) q_rows(0);
+    if (ok && pieces[0].b >= 0) {
+      q_load(0);
+      if (pieces[0].steps > 0) q_store(0);
+    }
     for (int n = 0; ok && pieces[n & 1].b >= 0; ++n) {
       // (a piece is read from shared memory where it is needed: registers are short in the loop over its jobs)
       const int buf = n & 1;
       const bool both = pieces[buf].rows > 128;
       const int steps = pieces[buf].steps, step0 = pieces[buf].step0, count = both ? 2 * steps : steps;
-      Rows st{{-CUDART_INF_F, -CUDART_INF_F}, {0.f, 0.f}, {0.f, 0.f}, 0, 0}, other = st;
+      Rows st{{kNone, kNone}, {0.f, 0.f}}, other = st;
       for (int j = 0; j < count; ++j) {
         const uint32_t b = j & 1, ts = lanes + kTmemS + 128 * b;
         const int t = both ? j & 1 : 0, s = both ? j >> 1 : j;
@@ -901,19 +933,16 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         tmem_ld_16x256b_x8(ts, v[0]);
         tmem_ld_16x256b_x8(ts + 64, v[1]);
         const int at = buf * kUnitRows + 128 * t + own;
-        const int pos[2] = {positions[at], positions[at + 8]};
-        if (s == 0) {
-          st.seen_end = __reduce_min_sync(0xFFFFFFFFu, min(pos[0], pos[1])) + 1;
-          st.seen_begin = a.window > 0 ? __reduce_max_sync(0xFFFFFFFFu, max(pos[0], pos[1])) + 1 - a.window : INT_MIN;
-        }
         const float factor[2] = {factors[at], factors[at + 8]};
         const int t0 = (step0 + s) * kStep;
-        const bool whole = *reinterpret_cast<volatile uint64_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8) == 0 && t0 + kStep <= st.seen_end && t0 >= st.seen_begin;
+        const int2 range = whole_of(buf, t);
+        const bool whole = static_cast<uint32_t>(step0 + s - range.x) < static_cast<uint32_t>(range.y) &&
+                           *reinterpret_cast<volatile uint64_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8) == 0;
         float mul[2] = {kMode == kPlain ? factor[0] : 1.f, kMode == kPlain ? factor[1] : 1.f};      // scores are mul * v
         tmem_wait_ld();
         touch(v[0]);
         touch(v[1]);
-        if (kMode == kCap) {
+        if (kMode & kCap) {
           // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), off by some 2^-23 of the cap
           const float f[2] = {factor[0] * a.two_over_cap, factor[1] * a.two_over_cap}, two = -2.f * a.cap_log2;
 #pragma unroll
@@ -922,11 +951,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
             for (int e = 0; e < 32; ++e)
               v[k][e] = __float_as_uint(fmaf(fast_rcp(1.f + fast_exp2(__uint_as_float(v[k][e]) * f[(e >> 1) & 1])), two, a.cap_log2));
         }
-        if (kMode != kPlain) {
+        if (kMode & kSlope) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float slope = slopes[at + 8 * r], base = -slope * static_cast<float>(pos[r] - t0 - 2 * quad);
-            const float m = kMode == kCap ? 1.f : factor[r];
+            const float slope = slopes[at + 8 * r], base = -slope * static_cast<float>(positions[at + 8 * r] - t0 - 2 * quad);
+            const float m = kMode & kCap ? 1.f : factor[r];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -942,7 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           const uint64_t absent = *reinterpret_cast<volatile uint64_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int hi = pos[r] - t0 - 2 * quad;
+            const int hi = positions[at + 8 * r] - t0 - 2 * quad;
             const uint32_t m = seen_bits(hi, a.window, absent);
 #pragma unroll
             for (int k = 0; k < 2; ++k)
@@ -970,10 +999,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           mx[1] = fmaxf(mx[1], x1);
         }
         bool raise[2], big = false;
+        float nc[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           mx[r] *= mul[r];
-          raise[r] = mx[r] > st.top[r] + kRaise || (st.top[r] == -CUDART_INF_F && mx[r] > -CUDART_INF_F);
+          nc[r] = fabsf(mx[r]) < kBigScore ? kShift - mx[r] : -mx[r];
+          raise[r] = nc[r] < st.c[r] - kRaise;                // (-inf, a row that sees nothing here, raises nothing)
           big |= kMode == kPlain && fabsf(mx[r]) >= kBigScore;
         }
         if (__any_sync(0xFFFFFFFFu, raise[0] || raise[1] || big)) {
@@ -989,10 +1020,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
 #pragma unroll
           for (int r = 0; r < 2; ++r)
             if (raise[r]) {
-              const float nc = fabsf(mx[r]) < kBigScore ? kShift - mx[r] : -mx[r];
-              alpha[r] = st.top[r] == -CUDART_INF_F ? 0.f : fast_exp2(nc - st.c[r]);
-              st.top[r] = mx[r];
-              st.c[r] = nc;
+              alpha[r] = fast_exp2(nc[r] - st.c[r]);
+              st.c[r] = nc[r];
               st.sum[r] *= alpha[r];
             }
           if (s > 0 && __any_sync(0xFFFFFFFFu, raise[0] || raise[1])) {
@@ -1047,6 +1076,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       if (!ok) break;
       // ---- the end of the piece: output rows, through the warp's part of the query operand (free once the products are
       // done) so that they go to memory in one piece: 16 bytes c of row r lie at c ^ (r & 7)
+      if (!(ok = wait_warp(&bars[kBarPieceFull + (buf ^ 1)], ((n + 1) >> 1) & 1, abort_flag, a))) break;
+      if (pieces[buf ^ 1].b >= 0) q_load(buf ^ 1);
       if (steps > 0) {
         // (two tiles: announced once; one: for every step, and the one two before was complete when its scores were)
         if (both) done ^= 1u;
@@ -1060,11 +1091,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * a.part_rows;
         uint8_t* stage = my_q(t);
         float f[2];
-        long long to[2];                                      // this lane's rows' places in out and lse
+        int to[2];                                            // this lane's rows' places in out and lse
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const int row = p.row0 + min(first + (lane >> 2) + 8 * r, p.rows - 1), tok = row / a.group;
-          to[r] = static_cast<long long>(p.q0 + tok) * a.hq + p.g * a.group + (row - tok * a.group);
+          to[r] = places[buf * kUnitRows + first + (lane >> 2) + 8 * r];
           float sum = st.sum[r];
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
           sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
@@ -1075,48 +1105,48 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
             else a.part_ml[part + first + (lane >> 2) + 8 * r] = make_float2(none ? -CUDART_INF_F : -st.c[r], sum);
           }
         }
-        // 32 columns: rows lane / 4 (+ 8), columns 8 i + 2 quad (+ 1)
-        auto columns = [&](int k, uint32_t (&u)[16]) {
+        // 64 columns: rows lane / 4 (+ 8), columns 8 i + 2 quad (+ 1)
+        auto columns = [&](int k, uint32_t (&u)[32]) {
           if (steps > 0) {
-            tmem_ld_16x256b_x4(lanes + kTmemO + 128 * t + 32 * k, u);
+            tmem_ld_16x256b_x8(lanes + kTmemO + 128 * t + 64 * k, u);
             tmem_wait_ld();
             touch(u);
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) u[e] = steps > 0 ? __float_as_uint(__uint_as_float(u[e]) * f[(e >> 1) & 1]) : 0u;
+          for (int e = 0; e < 32; ++e) u[e] = steps > 0 ? __float_as_uint(__uint_as_float(u[e]) * f[(e >> 1) & 1]) : 0u;
         };
         if (slot < 0) {
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t u[16];
+          for (int k = 0; k < 2; ++k) {
+            uint32_t u[32];
             columns(k, u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
               for (int r = 0; r < 2; ++r)
-                *reinterpret_cast<uint32_t*>(stage + ((lane >> 2) + 8 * r) * 256 + (((4 * k + i) ^ (lane >> 2)) * 16) + quad * 4) =
+                *reinterpret_cast<uint32_t*>(stage + ((lane >> 2) + 8 * r) * 256 + (((8 * k + i) ^ (lane >> 2)) * 16) + quad * 4) =
                     pack_bf16x2(__uint_as_float(u[4 * i + 2 * r]), __uint_as_float(u[4 * i + 2 * r + 1]));
           }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int row = 2 * i + (lane >> 4);
-            const long long place = __shfl_sync(0xFFFFFFFFu, to[i >> 2], (row & 7) * 4);
+            const int place = __shfl_sync(0xFFFFFFFFu, to[i >> 2], (row & 7) * 4);
             if (row < live)
-              reinterpret_cast<uint4*>(a.out + place * ZF_HEAD_DIM)[lane & 15] =
+              reinterpret_cast<uint4*>(a.out + static_cast<size_t>(place) * ZF_HEAD_DIM)[lane & 15] =
                   *reinterpret_cast<const uint4*>(stage + row * 256 + (((lane & 15) ^ (row & 7)) * 16));
           }
         } else {
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t u[16];
+          for (int k = 0; k < 2; ++k) {
+            uint32_t u[32];
             columns(k, u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
               for (int r = 0; r < 2; ++r)
                 if ((lane >> 2) + 8 * r < live)
-                  *reinterpret_cast<uint2*>(a.part_o + (part + first + (lane >> 2) + 8 * r) * ZF_HEAD_DIM + 32 * k + 8 * i + 2 * quad) =
+                  *reinterpret_cast<uint2*>(a.part_o + (part + first + (lane >> 2) + 8 * r) * ZF_HEAD_DIM + 64 * k + 8 * i + 2 * quad) =
                       make_uint2(u[4 * i + 2 * r], u[4 * i + 2 * r + 1]);
           }
         }
@@ -1125,9 +1155,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       tcgen05_before_sync();
       gs += steps;
       // ---- the next piece
-      if (!(ok = wait_warp(&bars[kBarPieceFull + (buf ^ 1)], ((n + 1) >> 1) & 1, abort_flag, a))) break;
+      __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarPieceEmpty + buf]);
-      if (pieces[buf ^ 1].b >= 0 && pieces[buf ^ 1].steps > 0) q_rows(buf ^ 1);
+      if (pieces[buf ^ 1].b >= 0 && pieces[buf ^ 1].steps > 0) q_store(buf ^ 1);
     }
   }
 
@@ -1199,9 +1229,9 @@ ChunkPlan chunk_plan(int rows, int group, int sms) {
 bool chunk_shape_ok(int batch, int rows, int hq, int hkv, int page_size, int max_pages) {
   if (batch < 0 || batch > ZF_MAX_BATCH || rows < 0 || hkv < 1 || hq < hkv || hq % hkv != 0 || max_pages < 1) return false;
   if (page_size < ZF_BLOCK_TOKENS || page_size % ZF_BLOCK_TOKENS || page_size > ZF_MAX_PAGE_SIZE) return false;
-  // positions, and the rows of a request and kv head, are counted with 32 bits
+  // positions and rows (of all heads) are counted with 32 bits
   return static_cast<long long>(max_pages) * page_size < INT_MAX - 16 * kStep &&
-         static_cast<long long>(rows) * (hq / hkv) < INT_MAX - 2 * kUnitRows;
+         static_cast<long long>(rows) * hq < INT_MAX - 2 * kUnitRows;
 }
 
 zf_status sm_count(int* sms) {
@@ -1305,7 +1335,7 @@ extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, i
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-      for (const auto kernel : {q4_chunk_kernel<kPlain>, q4_chunk_kernel<kSlope>, q4_chunk_kernel<kCap>}) {
+      for (const auto kernel : {q4_chunk_kernel<kPlain>, q4_chunk_kernel<kSlope>, q4_chunk_kernel<kCap>, q4_chunk_kernel<kCap | kSlope>}) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmTotal) != cudaSuccess)
           return ZF_ERR_CUDA;
         // the warpgroups' shares are those of a launch with kRegs registers per thread
@@ -1317,7 +1347,8 @@ extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, i
     }
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const auto kernel = softcap > 0.f ? q4_chunk_kernel<kCap> : slopes ? q4_chunk_kernel<kSlope> : q4_chunk_kernel<kPlain>;
+  const auto kernel = softcap > 0.f ? (slopes ? q4_chunk_kernel<kCap | kSlope> : q4_chunk_kernel<kCap>)
+                                    : (slopes ? q4_chunk_kernel<kSlope> : q4_chunk_kernel<kPlain>);
   st = launch(kernel, dim3(p.grid), kThreads, kSmTotal, s, a);
   if (st != ZF_OK) return st;
   return launch(q4_chunk_join_kernel, dim3(p.grid, p.part_rows / kJoinRows), 512, 0, s, a, p.grid);
