@@ -959,13 +959,11 @@ def _list_1d(t, name):
     return t.shape
 
 
-def _outputs(kind, out, shapes, dev):
-    """The int32 outputs of a call as `kind`: made here (in one allocation), or `out` checked."""
+def _outputs(kind, out, sizes, dev):
+    """The one-dimensional int32 outputs of a call as `kind`: made here (in one allocation), or `out` checked."""
     if out is not None:
-        return kind(*(_tensor(t, "out." + name, _I32, dev, s, write=True) for t, name, s in zip(out, kind._fields, shapes)))
-    sizes = [math.prod(s) for s in shapes]
-    return kind(*(t.view(s) for t, s in zip(torch.empty(sum(sizes), dtype=torch.int32, device=dev)
-                                            .unsafe_split_with_sizes(sizes), shapes)))
+        return kind(*[_tensor(t, "out." + name, _I32, dev, (n,), write=True) for t, name, n in zip(out, kind._fields, sizes)])
+    return kind._make(torch.empty(sum(sizes), dtype=torch.int32, device=dev).unsafe_split_with_sizes(sizes))
 
 
 def _status_ptr(status, dev):
@@ -998,7 +996,7 @@ def fork_requests(page_table, seq_lens, pages_held, src, dst, free_pages, free_p
     free_pos = _tensor(free_pos, "free_pos", _I32, dev, (1,))
     word = _status_ptr(status, dev)
     s = _launch_stream(dev)
-    out = _outputs(Fork, out, ((B,), (B,), (1,), (n,), (n,)), dev)
+    out = _outputs(Fork, out, (B, B, 1, n, n), dev)
     code = lib().zf_fork_requests(B, page_size, max_pages, seq_lens.data_ptr(), pages_held.data_ptr(), src.data_ptr(),
                                   dst.data_ptr(), n, page_table.data_ptr(), free_pages.data_ptr(), free_pages.shape[0],
                                   free_pos.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(),
@@ -1037,7 +1035,7 @@ def release_requests(page_table, seq_lens, pages_held, release, free_pages, free
     free_pos = _tensor(free_pos, "free_pos", _I32, dev, (1,))
     word = _status_ptr(status, dev)
     s = _launch_stream(dev)
-    out = _outputs(Release, out, ((B,), (B,), (1,)), dev)
+    out = _outputs(Release, out, (B, B, 1), dev)
     workspace = _workspace(workspace, release_workspace_size(num_pages), dev)
     code = lib().zf_release_requests(B, max_pages, num_pages, page_table.data_ptr(), seq_lens.data_ptr(),
                                      pages_held.data_ptr(), release.data_ptr(), free_pages.data_ptr(),
@@ -1062,7 +1060,13 @@ def compact_pages(page_table, pages_held, num_pages, out=None, status=None, work
         raise ValueError("num_pages must not be negative")
     word = _status_ptr(status, dev)
     s = _launch_stream(dev)
-    out = _outputs(Compaction, out, ((B, max_pages), (num_pages,), (1,), (num_pages // 2,), (num_pages // 2,)), dev)
+    sizes = (B * max_pages, num_pages, 1, num_pages // 2, num_pages // 2)
+    if out is None:
+        table, *lists = torch.empty(sum(sizes), dtype=torch.int32, device=dev).unsafe_split_with_sizes(sizes)
+        out = Compaction(table.view(B, max_pages), *lists)
+    else:
+        out = Compaction(*[_tensor(t, "out." + name, _I32, dev, (n,) if i else (B, max_pages), write=True)
+                           for i, (t, name, n) in enumerate(zip(out, Compaction._fields, sizes))])
     workspace = _workspace(workspace, compact_workspace_size(num_pages), dev)
     code = lib().zf_compact_pages(B, max_pages, num_pages, page_table.data_ptr(), pages_held.data_ptr(), out[0].data_ptr(),
                                   out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), word,
