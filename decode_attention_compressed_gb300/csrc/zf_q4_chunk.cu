@@ -13,14 +13,16 @@
 // One CTA, 20 warps:
 //  * warps 0-7, softmax: all on the same job, which is a tile of 128 rows and a step, 16 rows a warp, so that a job's
 //    chain from scores to weights is short.  Two tiles of up to 256 rows take turns; up to 128 rows, one tile takes
-//    one step after the other.  Scores (fp32, 128 x 128) come out of tensor memory once; the weights go back over
-//    them as fp16, the A operand of the second product.  A row's maximum is raised only when a score exceeds it
-//    by 2^8 (the output in tensor memory is then rescaled in place).  These warps also stage query rows as fp16, each
-//    row times a power of two (exact down to 2^-28 of its largest value).
+//    one step after the other; up to 16 rows, every warp has them all and one record of the step.  Scores (fp32,
+//    128 x 128) come out of tensor memory once; the weights go back over them as fp16, the A operand of the second
+//    product.  A row's maximum is raised only when a score exceeds it by 2^8 (the output in tensor memory is then
+//    rescaled in place).  These warps also stage query rows as fp16, each row times a power of two (exact down to
+//    2^-28 of its largest value).
 //  * warps 8-15 decode: warp r takes the 16 tokens of record r of each step from shared memory to the fp16
 //    operands.  A code is e2m1 and a scale e4m3, so their product is exact in fp16; K is K-major, V is stored the
 //    same way (a token's 8 channels are one row of a core matrix) and read as an MN-major operand.  The operands
-//    go round three buffers of 32 KB.
+//    go round three buffers of 32 KB, or four in units of one tile, where the second query tile's place is free (with
+//    three, keys wait for the product two steps before: 64 single tokens 184 us instead of 163).
 //  * warp 16 issues the products: S = Q K^T (8 x M128 N128 K16 from shared memory) and O += P V (P from tensor
 //    memory).
 //  * warp 17 finds the CTA's range, walks its pieces, resolves pages and starts the records' bulk copies, three
@@ -58,8 +60,10 @@ static_assert(2 * regs_softmax(0) + 2 * kRegsDecode + regs_other(0) <= 5 * kRegs
               "a larger sum would wait for registers forever");
 constexpr int kStep = 128;                       // tokens per step: of the operands
 constexpr int kUnitRows = 256;                   // query rows per unit
+constexpr int kFewRows = 16;                     // units of up to so many rows: each warp has them all, and a record of the step
 constexpr int kStages = 3;                       // steps of records in flight
-constexpr int kRing = 3;                         // operand buffers
+constexpr int kRing = 4;                         // operand buffers; the last is the second query tile's in units of two tiles,
+                                                 // whose operands go round the first three
 constexpr int kOperand = kStep * ZF_HEAD_DIM * 2;
 constexpr int kCoreRow = 2048;                   // 8 rows x 128 elements of 16 bits
 constexpr int kUnitCost = 2;                     // a unit's start and end in steps
@@ -114,20 +118,23 @@ enum : int {
   kBarPFull = kBarSFull + 2,                   // [2] its weights
   kBarPvDone = kBarPFull + 2,                  // [2] its product with the values (commit)
   kBarQFull = kBarPvDone + 2,                  // query rows of a piece
-  kBarDrain = kBarQFull + 1,
+  kBarFew = kBarQFull + 1,                     // the softmax warps meet
+  kBarDrain = kBarFew + 1,
   kNumBars = kBarDrain + 1,
 };
 
 // Shared memory.  The operand ring comes first: the plan's sums lie over it before the walk begins.
 constexpr int kSmRing = 0;
-constexpr int kSmQ = kSmRing + kRing * kOperand;
-constexpr int kSmRec = kSmQ + 2 * kOperand;
+constexpr int kSmQ1 = kSmRing + (kRing - 1) * kOperand;
+constexpr int kSmQ0 = kSmQ1 + kOperand;
+constexpr int kSmRec = kSmQ0 + kOperand;
 constexpr int kSmScale = kSmRec + kStages * 8 * kQ4Record;     // [2][256] score factors of the rows
 constexpr int kSmPos = kSmScale + 2 * kUnitRows * 4;           // [2][256] their positions
 constexpr int kSmSlope = kSmPos + 2 * kUnitRows * 4;           // [2][256] their slopes
 constexpr int kSmPlace = kSmSlope + 2 * kUnitRows * 4;         // [2][256] their places among the rows of q and out
 constexpr int kSmWhole = kSmPlace + 2 * kUnitRows * 4;         // [2][2][8] int2: steps that all rows of a warp see whole
-constexpr int kSmPiece = kSmWhole + 2 * 2 * 8 * 8;             // [2] Piece
+constexpr int kSmFew = kSmWhole + 2 * 2 * 8 * 8;               // [8 warps][16 rows] float2: c and sum
+constexpr int kSmPiece = kSmFew + 8 * kFewRows * 8;             // [2] Piece
 constexpr int kSmAbsent = kSmPiece + 2 * 48;                   // [8 steps][8 records] 1: no tokens there
 constexpr int kSmBars = kSmAbsent + 64;
 constexpr int kSmMisc = kSmBars + kNumBars * 8;                // abort flag, tensor-memory base, range
@@ -448,6 +455,14 @@ __device__ __forceinline__ uint32_t seen_bits(int hi, int window, uint64_t absen
 // What becomes of the scores: nothing, or a cap, slopes, or both.
 enum : int { kPlain = 0, kSlope = 1, kCap = 2 };
 
+// The s-th step that a piece of so many takes.  With slopes the last one first: positive slopes raise the scores with the
+// position, so going up a row's maximum would be raised, and its output rescaled, in almost every step (64 single
+// tokens: 201 us up, 184 us down).
+template <int kMode>
+__device__ __forceinline__ int order(int s, int steps) {
+  return kMode & kSlope ? steps - 1 - s : s;
+}
+
 template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -473,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       mbar_init(&bars[kBarOpEmpty + i], 1);
     }
     mbar_init(&bars[kBarQFull], 8);
+    mbar_init(&bars[kBarFew], 8);
     mbar_init(&bars[kBarDrain], 1);
     *abort_flag = 0;
   }
@@ -609,15 +625,18 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           if (tile * 16 >= p.last) return -1;
           return row[tile * 16 / a.page_size];
         };
-        int next = page_of(p.step0 * 8 + lane);
+        auto tile_of = [&](int s) {              // lane's tile of the steps from the s-th
+          const int o = order<kMode>(s + (lane >> 3), p.steps);
+          return o < 0 ? 1 << 26 : (p.step0 + o) * 8 + (lane & 7);       // (behind every context)
+        };
+        int next = page_of(tile_of(0));
         for (int s = 0; s < p.steps && ok; s += 4) {
           int cur = next;
-          const int tile0 = (p.step0 + s) * 8;
-          if ((tile0 + lane) * 16 < p.last && (cur < 0 || cur >= a.num_pages)) {
+          if (tile_of(s) * 16 < p.last && (cur < 0 || cur >= a.num_pages)) {
             report(a.status, ZF_DEV_BAD_PAGE_ID);
             cur = -1;
           }
-          next = page_of(tile0 + 32 + lane);
+          next = page_of(tile_of(s + 4));
           for (int k = 0; k < 4 && s + k < p.steps; ++k, ++gs) {
             const int page = __shfl_sync(0xFFFFFFFFu, cur, 8 * k + (lane & 7));
             const int stage = gs % kStages;
@@ -629,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
                 uint64_t* bar = &bars[kBarRecFull + stage * 8 + lane];
                 smem[kSmAbsent + (gs & 7) * 8 + lane] = page < 0;
                 if (page >= 0) {
-                  const int in = ((tile0 + 8 * k + lane) * 16 % a.page_size) >> 4;
+                  const int in = (((p.step0 + order<kMode>(s + k, p.steps)) * 8 + lane) * 16 % a.page_size) >> 4;
                   const uint8_t* src =
                       a.records + ((static_cast<size_t>(page) * a.hkv + p.g) * (a.page_size >> 4) + in) * kQ4Record;
                   mbar_arrive_expect_tx(bar, kQ4Record);
@@ -679,24 +698,21 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     // that frees their buffer is issued.  Nothing but issuing happens here: waits, commits and instructions cost this
     // warp more cycles than the tensor cores take for a job if they are not few.
     const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0), sm = __shfl_sync(0xFFFFFFFFu, smem_addr(smem), 0);
-    const uint32_t q0 = desc_k(sm + kSmQ), q1 = desc_k(sm + kSmQ + kOperand);
+    const uint32_t q0 = desc_k(sm + kSmQ0), q1 = desc_k(sm + kSmQ1);
     const uint32_t k0 = desc_k(sm + kSmRing), v0 = desc_mn(sm + kSmRing);
-    struct Next {                                 // the ring's next K or V: slot, and parity of its phase
-      int slot;
-      uint32_t turn;
-    } key{0, 0}, value{1, 0};
+    uint32_t slot = 0, turn = 0;                  // the ring's next operand; parities of the slots' phases
     uint32_t phase = 0;                           // parity of the next weights in each buffer
     uint32_t rows_seen = 0;                       // pieces whose query rows were waited for
     bool ok = true;
-    // Waits until the next K or V is decoded; at: its slot.  (K and V alternate in the ring, so each moves two on; the
-    // phase before was complete when the operand before it in the slot had been used.)
-    auto operand = [&](Next& next, int& at) {
-      at = next.slot;
-      const bool good = wait_warp(&bars[kBarOpFull + at], next.turn, abort_flag, a);
-      if (at > 0) next.turn ^= 1;
-      next.slot = at == 0 ? 2 : at - 1;
-      return good;
+    // The next operand's slot (K and V alternate), with the parity of its phase in bit 8.  (The phase before was complete
+    // when the operand before it in the slot had been used.)
+    auto next = [&](bool both) {
+      const uint32_t at = slot | ((turn >> slot) & 1) << 8;
+      turn ^= 1u << slot;
+      slot = slot + 1 == (both ? kRing - 1 : kRing) ? 0 : slot + 1;
+      return at;
     };
+    auto decoded = [&](uint32_t at) { return wait_warp(&bars[kBarOpFull + (at & 255)], at >> 8, abort_flag, a); };
     auto weights_ready = [&](int b) {
       const bool good = wait_warp(&bars[kBarPFull + b], (phase >> b) & 1, abort_flag, a);
       phase ^= 1u << b;
@@ -710,9 +726,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       const bool both = __shfl_sync(0xFFFFFFFFu, pieces[buf].rows, 0) > 128;
       if (pb < 0) break;
       if (steps > 0 && !wait_warp(&bars[kBarQFull], rows_seen++ & 1, abort_flag, a)) break;
-      int k = 0, v = 0;
+      uint32_t k = 0, v = 0;
       if (steps > 0 && both) {
-        if (!(ok = operand(key, k))) break;
+        if (slot == kRing - 1) slot = 0;
+        if (!(ok = decoded(k = next(true)))) break;
+        k &= 255;
         tcgen05_after_sync();
         mma_scores(tm + kTmemS, q0, k0 + k * (kOperand / 16));
         commit(&bars[kBarSFull]);
@@ -721,11 +739,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         commit(&bars[kBarOpEmpty + k]);
         for (int s = 0; s < steps; ++s) {
           const bool more = s + 1 < steps;
-          if (!(ok = operand(value, v) && weights_ready(0))) break;
+          if (!(ok = decoded(v = next(true)) && weights_ready(0))) break;
+          v &= 255;
           tcgen05_after_sync();
           mma_weights(tm + kTmemO, tm + kTmemS, v0 + v * (kOperand / 16), s > 0);
           if (more) {
-            if (!(ok = operand(key, k))) break;
+            if (!(ok = decoded(k = next(true)))) break;
+            k &= 255;
             tcgen05_after_sync();
             mma_scores(tm + kTmemS, q0, k0 + k * (kOperand / 16));
             commit(&bars[kBarSFull]);
@@ -742,19 +762,24 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         }
         if (!ok) break;
         commit(&bars[kBarPvDone]);
+        commit(&bars[kBarOpEmpty + kRing - 1]);   // (the second tile's place is free)
       } else if (steps > 0) {
-        // (the keys of step s take the place of the values of step s - 2)
+        uint32_t values[2];                       // places of the values of the steps whose scores are under way
         for (int s = 0; s < steps + 2; ++s) {
           const int b = s & 1;
           if (s >= 2) {
-            if (!(ok = operand(value, v) && weights_ready(b))) break;
+            v = b ? values[1] : values[0];
+            if (!(ok = decoded(v) && weights_ready(b))) break;
+            v &= 255;
             tcgen05_after_sync();
             mma_weights(tm + kTmemO, tm + kTmemS + 128 * b, v0 + v * (kOperand / 16), s > 2);
             commit(&bars[kBarPvDone + b]);
             commit(&bars[kBarOpEmpty + v]);
           }
           if (s < steps) {
-            if (!(ok = operand(key, k))) break;
+            if (!(ok = decoded(k = next(false)))) break;
+            k &= 255;
+            values[b] = next(false);
             tcgen05_after_sync();
             mma_scores(tm + kTmemS + 128 * b, q0, k0 + k * (kOperand / 16));
             commit(&bars[kBarSFull + b]);
@@ -776,12 +801,19 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     constexpr int kPerWarp = 8 / kDecodeWarps;       // records of a step
     const int r = warp - kDecodeWarp0;
     uint32_t gs = 0;
+    uint32_t slot = 0, turn = 0;                     // the next operand's; parities of the slots' uses
     bool ok = true;
     for (int n = 0; ok; ++n) {
       const int buf = n & 1;
       if (!wait_warp(&bars[kBarPieceFull + buf], (n >> 1) & 1, abort_flag, a)) break;
       const int pb = pieces[buf].b, steps = pieces[buf].steps;
       if (pb < 0) break;
+      const uint32_t last = pieces[buf].rows > 128 ? kRing - 1 : kRing;
+      if (steps > 0 && last < kRing) {
+        // the second tile is a use of the last slot (every piece before the last one is done, so no phase is passed over)
+        if (slot == last) slot = 0;
+        turn ^= 1u << last;
+      }
       for (int s = 0; s < steps; ++s, ++gs) {
         const int stage = gs % kStages;
         bool absent[kPerWarp];
@@ -794,9 +826,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         if (!ok) break;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-          const uint32_t k = 2 * gs + v;
-          if (k >= kRing && !(ok = wait_warp(&bars[kBarOpEmpty + k % kRing], (k / kRing - 1) & 1, abort_flag, a))) break;
-          uint8_t* op = smem + kSmRing + (k % kRing) * kOperand;
+          const uint32_t k = slot;
+          // (before the first use: of the phase before the first, which counts as complete)
+          if (!(ok = wait_warp(&bars[kBarOpEmpty + k], ((turn >> k) & 1) ^ 1, abort_flag, a))) break;
+          turn ^= 1u << k;
+          slot = slot + 1 == last ? 0 : slot + 1;
+          uint8_t* op = smem + kSmRing + k * kOperand;
 #pragma unroll
           for (int i = 0; i < kPerWarp; ++i) {
             const int rec = r + i * kDecodeWarps;
@@ -807,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kBarOpFull + k % kRing]);
+          if (lane == 0) mbar_arrive(&bars[kBarOpFull + k]);
         }
         if (!ok) break;
         if (lane < kPerWarp) mbar_arrive(&bars[kBarRecEmpty + stage * 8 + r + lane * kDecodeWarps]);
@@ -831,14 +866,14 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     uint32_t gs = 0;                                          // steps before this piece
     uint32_t phase = 0, done = 0;                             // parity of the next scores in a buffer; of the products' next end
     // The warp's 16 rows of tile t of the query operand: 4 KB that no other warp writes.
-    auto my_q = [&](int t) { return smem + kSmQ + t * kOperand + (row16 >> 3) * kCoreRow; };
+    auto my_q = [&](int t) { return smem + (t ? kSmQ1 : kSmQ0) + (row16 >> 3) * kCoreRow; };
 
     // Query rows of a piece, 16 of each tile: lane (row lane % 8 of 8, chunks lane / 8 + 4 i of 16 bytes).  They are read
-    // while the piece before ends.
+    // while the piece before ends.  Up to 16 rows: every warp has the same.
     uint4 qv[2][2][4];
     auto q_load = [&](int buf) {
       const Piece& p = pieces[buf];
-      const int tiles = p.rows > 128 ? 2 : 1;
+      const int tiles = p.rows > 128 ? 2 : 1, copy = p.rows <= kFewRows ? row16 : 0;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (t >= tiles) break;
@@ -846,8 +881,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
 #pragma unroll
         for (int r8 = 0; r8 < 2; ++r8) {
           const int at = 128 * t + row16 + 8 * r8 + (lane & 7);
-          const bool in = at < p.rows;
-          const int row = p.row0 + min(at, p.rows - 1), tok = row / a.group, h = p.g * a.group + (row - tok * a.group);
+          const bool in = at - copy < p.rows;
+          const int row = p.row0 + min(at - copy, p.rows - 1), tok = row / a.group, h = p.g * a.group + (row - tok * a.group);
           const int place = (p.q0 + tok) * a.hq + h;
           const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(place) * ZF_HEAD_DIM);
 #pragma unroll
@@ -912,6 +947,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       float c[2], sum[2];                                     // shift - maximum (log2 units), sum of weights
     };
     constexpr float kNone = 1e30f;                            // c before the first score that is seen
+    uint32_t met = 0;
+    auto meet = [&]() {                                       // all softmax warps
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarFew]);
+      return wait_warp(&bars[kBarFew], met++ & 1, abort_flag, a);
+    };
     bool ok = wait_warp(&bars[kBarPieceFull], 0, abort_flag, a);
     if (ok && pieces[0].b >= 0) {
       q_load(0);
@@ -923,7 +964,121 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       const bool both = pieces[buf].rows > 128;
       const int steps = pieces[buf].steps, step0 = pieces[buf].step0, count = both ? 2 * steps : steps;
       Rows st{{kNone, kNone}, {0.f, 0.f}}, other = st;
-      for (int j = 0; j < count; ++j) {
+      const bool few = pieces[buf].rows <= kFewRows && steps > 0;
+      if (few) {
+        // ---- up to 16 rows.  Every warp has a copy of them and of the tile's 128 rows its 16, and takes the scores of one
+        // record, 16 tokens, with a maximum of its own; its weights of the other tokens are 0, so the product leaves
+        // its part of the output in its rows, and the parts are summed at the end.  A job's chain from scores to
+        // weights, which bounds units of one tile, is half as long (64 single tokens with slopes: 228 -> 201 us).
+        const int mine = buf * kUnitRows + own, col0 = 16 * warp + 2 * quad;
+        const float factor[2] = {factors[mine], factors[mine + 8]};
+        const int pos[2] = {positions[mine], positions[mine + 8]};
+        float slope[2] = {0.f, 0.f};
+        if (kMode & kSlope) {
+          slope[0] = slopes[mine];
+          slope[1] = slopes[mine + 8];
+        }
+        for (int s = 0; s < steps; ++s) {
+          const uint32_t b = s & 1, ts = lanes + kTmemS + 128 * b;
+          if (!(ok = wait_warp(&bars[kBarSFull + b], (phase >> b) & 1, abort_flag, a))) break;
+          phase ^= 1u << b;
+          tcgen05_after_sync();
+          uint32_t v[8];
+          tmem_ld_16x256b_x2(ts + 16 * warp, v);
+          const int t0 = (step0 + order<kMode>(s, steps)) * kStep + col0;
+          const bool absent = *reinterpret_cast<volatile uint8_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8 + warp) != 0;
+          float mul[2] = {kMode == kPlain ? factor[0] : 1.f, kMode == kPlain ? factor[1] : 1.f};
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) asm volatile("" : "+r"(v[e]));
+          float mx[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int hi = pos[r] - t0;
+            const float base = -slope[r] * static_cast<float>(hi);
+            mx[r] = -CUDART_INF_F;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int col = 8 * (e >> 1) + (e & 1);
+              uint32_t& at_e = v[4 * (e >> 1) + 2 * r + (e & 1)];
+              float x = __uint_as_float(at_e);
+              if (kMode & kCap) x = fmaf(fast_rcp(1.f + fast_exp2(x * (factor[r] * a.two_over_cap))), -2.f * a.cap_log2, a.cap_log2);
+              if (kMode & kSlope) x = fmaf(x, kMode & kCap ? 1.f : factor[r], fmaf(slope[r], static_cast<float>(col), base));
+              if (absent || col > hi || (a.window > 0 && col <= hi - a.window)) x = -CUDART_INF_F;
+              at_e = __float_as_uint(x);
+              mx[r] = fmaxf(mx[r], x);
+            }
+          }
+#pragma unroll
+          for (int d = 1; d < 4; d <<= 1) {
+            const float x0 = __shfl_xor_sync(0xFFFFFFFFu, mx[0], d), x1 = __shfl_xor_sync(0xFFFFFFFFu, mx[1], d);
+            mx[0] = fmaxf(mx[0], x0);
+            mx[1] = fmaxf(mx[1], x1);
+          }
+          bool raise[2];
+          float nc[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            mx[r] *= mul[r];
+            nc[r] = fabsf(mx[r]) < kBigScore ? kShift - mx[r] : -mx[r];
+            raise[r] = nc[r] < st.c[r] - kRaise;
+            if (kMode == kPlain && fabsf(mx[r]) >= kBigScore) {       // (multiplied out, see below)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t& at_e = v[4 * (e >> 1) + 2 * r + (e & 1)];
+                at_e = __float_as_uint(__uint_as_float(at_e) * mul[r]);
+              }
+              mul[r] = 1.f;
+            }
+          }
+          if (__any_sync(0xFFFFFFFFu, raise[0] || raise[1])) {
+            float alpha[2] = {1.f, 1.f};
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (raise[r]) {
+                alpha[r] = fast_exp2(nc[r] - st.c[r]);
+                st.c[r] = nc[r];
+                st.sum[r] *= alpha[r];
+              }
+            if (s > 0) {
+              if (!(ok = wait_warp(&bars[kBarPvDone + (b ^ 1)], ((done >> (b ^ 1)) & 1) ^ 1, abort_flag, a))) break;
+              tcgen05_after_sync();
+#pragma unroll 1
+              for (int k = 0; k < 4; ++k) {
+                uint32_t u[16];
+                tmem_ld_16x256b_x4(lanes + kTmemO + 32 * k, u);
+                tmem_wait_ld();
+                touch(u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha[(e >> 1) & 1]);
+                tmem_st_16x256b_x4(lanes + kTmemO + 32 * k, u);
+              }
+            }
+          }
+          uint32_t y[4];                                      // [8 i tokens][row]
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int r = e & 1;
+            const float y0 = fast_exp2(fmaf(__uint_as_float(v[2 * e]), mul[r], st.c[r])),
+                        y1 = fast_exp2(fmaf(__uint_as_float(v[2 * e + 1]), mul[r], st.c[r]));
+            st.sum[r] += y0 + y1;
+            y[e] = pack_f16(y0, y1);
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = 4 * k + (e >> 2) == warp ? y[e & 3] : 0u;
+            tmem_st_16x128b_x8(ts + 32 * k, w);
+          }
+          tmem_wait_st();
+          tcgen05_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarPFull + b]);
+          done ^= 1u << b;
+        }
+      }
+      for (int j = few ? count : 0; j < count; ++j) {
         const uint32_t b = j & 1, ts = lanes + kTmemS + 128 * b;
         const int t = both ? j & 1 : 0, s = both ? j >> 1 : j;
         if (!(ok = wait_warp(&bars[kBarSFull + b], (phase >> b) & 1, abort_flag, a))) break;
@@ -934,9 +1089,9 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         tmem_ld_16x256b_x8(ts + 64, v[1]);
         const int at = buf * kUnitRows + 128 * t + own;
         const float factor[2] = {factors[at], factors[at + 8]};
-        const int t0 = (step0 + s) * kStep;
+        const int step = step0 + order<kMode>(s, steps), t0 = step * kStep;
         const int2 range = whole_of(buf, t);
-        const bool whole = static_cast<uint32_t>(step0 + s - range.x) < static_cast<uint32_t>(range.y) &&
+        const bool whole = static_cast<uint32_t>(step - range.x) < static_cast<uint32_t>(range.y) &&
                            *reinterpret_cast<volatile uint64_t*>(smem + kSmAbsent + ((gs + s) & 7) * 8) == 0;
         float mul[2] = {kMode == kPlain ? factor[0] : 1.f, kMode == kPlain ? factor[1] : 1.f};      // scores are mul * v
         tmem_wait_ld();
@@ -1085,11 +1240,74 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         if (!(ok = wait_warp(&bars[kBarPvDone + b], ((done >> b) & 1) ^ 1, abort_flag, a))) break;
         tcgen05_after_sync();
       }
-      for (int t = 0; t < (both ? 2 : 1); ++t) {
+      if (few) {
+        // the parts of the output, through the query operand (32 KB, free now) in two halves of 64 channels:
+        // [warp][row][64], 8 channels c of row r at c ^ 8 (r & 7)
+        float2* rows = reinterpret_cast<float2*>(smem + kSmFew);
+        float* parts = reinterpret_cast<float*>(smem + kSmQ0);
+        const Piece& p = pieces[buf];
+        const int slot = p.slot, live = p.rows;
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * a.part_rows;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          st.sum[r] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[r], 1);
+          st.sum[r] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[r], 2);
+          if (quad == 0) rows[warp * kFewRows + (lane >> 2) + 8 * r] = make_float2(st.c[r], st.sum[r]);
+        }
+        if (!(ok = meet())) break;
+        float f[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = (lane >> 2) + 8 * r;
+          float c = kNone, sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < 8; ++w) c = fminf(c, rows[w * kFewRows + row].x);
+#pragma unroll
+          for (int w = 0; w < 8; ++w) sum += rows[w * kFewRows + row].y * fast_exp2(c - rows[w * kFewRows + row].x);
+          const bool none = sum == 0.f;
+          f[r] = none ? 0.f : fast_exp2(c - st.c[r]) * (slot >= 0 ? 1.f : a.v_factor / sum);
+          if (warp == 0 && quad == 0 && row < live) {
+            if (slot < 0) a.lse[places[buf * kUnitRows + row]] = none ? -CUDART_INF_F : (log2f(sum) - c) * kLn2f;
+            else a.part_ml[part + row] = make_float2(none ? -CUDART_INF_F : -c, sum);
+          }
+        }
+        const int row = threadIdx.x >> 4, four = threadIdx.x & 15;
+#pragma unroll 1
+        for (int k = 0; k < 2 && ok; ++k) {
+          uint32_t u[32];
+          tmem_ld_16x256b_x8(lanes + kTmemO + 64 * k, u);
+          tmem_wait_ld();
+          touch(u);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if ((lane >> 2) + 8 * r < live)
+                *reinterpret_cast<float2*>(parts + (warp * kFewRows + (lane >> 2) + 8 * r) * 64 + ((8 * i) ^ (8 * (lane >> 2))) + 2 * quad) =
+                    make_float2(__uint_as_float(u[4 * i + 2 * r]) * f[r], __uint_as_float(u[4 * i + 2 * r + 1]) * f[r]);
+          if (!(ok = meet())) break;
+          if (row < live) {
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const float4 x = *reinterpret_cast<const float4*>(parts + (w * kFewRows + row) * 64 + ((4 * four) ^ (8 * (row & 7))));
+              o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+            }
+            if (slot < 0)
+              *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(places[buf * kUnitRows + row]) * ZF_HEAD_DIM + 64 * k + 4 * four) =
+                  make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+            else
+              *reinterpret_cast<float4*>(a.part_o + (part + row) * ZF_HEAD_DIM + 64 * k + 4 * four) = o;
+          }
+          ok = meet();
+        }
+        if (!ok) break;
+      }
+      for (int t = few ? 2 : 0; t < (both ? 2 : 1); ++t) {
         const Piece& p = pieces[buf];
         const int slot = p.slot, first = 128 * t + row16, live = min(16, p.rows - first);      // rows of this warp
         const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * a.part_rows;
-        uint8_t* stage = my_q(t);
+        uint8_t* stage = my_q(0);                             // (the second tile's place may have the next piece's keys)
         float f[2];
         int to[2];                                            // this lane's rows' places in out and lse
 #pragma unroll
@@ -1151,6 +1369,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           }
         }
         st = other;
+        __syncwarp();
       }
       tcgen05_before_sync();
       gs += steps;
