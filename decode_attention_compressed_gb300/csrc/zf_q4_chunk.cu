@@ -307,19 +307,19 @@ __device__ __forceinline__ Request request(const ChunkArgs& a, int b) {
 __device__ __forceinline__ int unit_count(const ChunkArgs& a, const Request& r) {
   return (r.tokens * a.group + kUnitRows - 1) / kUnitRows;
 }
-// Steps [lo, hi) and tokens seen of unit i.
-__device__ __forceinline__ void unit_steps(const ChunkArgs& a, const Request& r, int i, int& lo, int& hi, int& last) {
+// Steps [lo, hi) of unit i, and the tokens [first, last) that its rows see.
+__device__ __forceinline__ void unit_steps(const ChunkArgs& a, const Request& r, int i, int& lo, int& hi, int& first, int& last) {
   const int rows = r.tokens * a.group;
   const int t0 = i * kUnitRows / a.group, t1 = (min(rows, (i + 1) * kUnitRows) - 1) / a.group;
   const int p0 = r.len - r.tokens + t0;
   last = max(r.len - r.tokens + t1 + 1, 0);
   hi = (last + kStep - 1) / kStep;
-  lo = a.window > 0 ? max(0, p0 + 1 - a.window) / kStep : 0;
-  lo = min(lo, hi);
+  first = a.window > 0 ? max(0, p0 + 1 - a.window) : 0;
+  lo = min(first / kStep, hi);
 }
 __device__ __forceinline__ int unit_cost(const ChunkArgs& a, const Request& r, int i) {
-  int lo, hi, last;
-  unit_steps(a, r, i, lo, hi, last);
+  int lo, hi, first, last;
+  unit_steps(a, r, i, lo, hi, first, last);
   return hi - lo + kUnitCost;
 }
 
@@ -355,9 +355,9 @@ __device__ __forceinline__ Place find_place(const ChunkArgs& a, const int* sums,
     if (above) {
       const int k = __ffs(above) - 1;
       const int before = k > 0 ? __shfl_sync(0xFFFFFFFFu, in, k - 1) : 0;
-      int slo, shi, last;
+      int slo, shi, first, last;
       p.i = base + k;
-      unit_steps(a, r, p.i, slo, shi, last);
+      unit_steps(a, r, p.i, slo, shi, first, last);
       const int steps = shi - slo;
       int s = min(max(rest - before - kUnitCost, 0), steps);
       if (s < kSnap) s = 0;
@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       const bool final_unit = at.b == to.b && at.g == to.g && at.i == to.i;
       if (at.b >= a.batch || at.b > to.b || (final_unit && to.s == 0)) break;
       Piece p;
-      int lo, hi;
-      unit_steps(a, r, at.i, lo, hi, p.last);
+      int lo, hi, from;
+      unit_steps(a, r, at.i, lo, hi, from, p.last);
       const int s0 = first ? at.s : 0, s1 = final_unit ? to.s : hi - lo;
       first = false;
       if (s0 < s1 || hi == lo) {
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         // its records: lane l resolves the page of tile l of every 4 steps, lanes 0-7 start the copies
         const int32_t* row = a.page_table + static_cast<size_t>(p.b) * a.max_pages;
         auto page_of = [&](int tile) {           // tile: 16 tokens of the context; -1: none there
-          if (tile * 16 >= p.last) return -1;
+          if (tile * 16 >= p.last || tile * 16 + 16 <= from) return -1;
           return row[tile * 16 / a.page_size];
         };
         auto tile_of = [&](int s) {              // lane's tile of the steps from the s-th
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         int next = page_of(tile_of(0));
         for (int s = 0; s < p.steps && ok; s += 4) {
           int cur = next;
-          if (tile_of(s) * 16 < p.last && (cur < 0 || cur >= a.num_pages)) {
+          if (tile_of(s) * 16 < p.last && tile_of(s) * 16 + 16 > from && (cur < 0 || cur >= a.num_pages)) {
             report(a.status, ZF_DEV_BAD_PAGE_ID);
             cur = -1;
           }

@@ -511,6 +511,7 @@ size_t zf_q4_chunk_attn_workspace_size(int32_t batch, int32_t rows, int32_t num_
  *   A token_start entry that decreases or passes rows leaves that request out, a seq_len out of range is clamped;
  *   both set ZF_DEV_BAD_SEQ_LEN.  A page id out of range sets ZF_DEV_BAD_PAGE_ID and its tokens are not seen.
  *   A wait that takes 2 s gives up: it sets ZF_DEV_TIMEOUT, and out and lse of that call mean nothing.
+ *   With a window, pages that lie before the windows of all new tokens of a request need not be there.
  *   batch <= ZF_MAX_BATCH.  rows == 0 or batch == 0 is a no-op.  Two kernels (attention, then the joining of units
  *   split over CTAs), launched with programmatic stream serialisation; results are deterministic (no atomics).
  */

@@ -127,6 +127,50 @@ def test_large_scores_keep_their_weights(zf):
                     assert (np.abs(f64(out[t, h]) - want) <= 2.0 ** -7 * np.abs(want) + 1e-12).all()
 
 
+@pytest.mark.parametrize("group,tokens", [(1, 1), (1, 16), (1, 17), (4, 4), (4, 5), (16, 1), (15, 1), (7, 2), (17, 1)])
+@pytest.mark.parametrize("mod", [{}, dict(steep=1.0), dict(steep=-1.0, window=200), dict(softcap=3.0, steep=0.5), dict(window=1)])
+def test_up_to_sixteen_rows_and_a_few_more(zf, group, tokens, mod):
+    """Units whose rows every warp has, at every end of a context, and slopes that raise the maximum in every step."""
+    lens = [tokens + n for n in (0, 1, 15, 16, 17, 111, 112, 127, 128, 129, 700)]
+    c = Case(zf, 16, 2, group, lens, [tokens] * len(lens), seed=group + tokens)
+    c.table[10, 40] = -1                                             # a page that is not there
+    seen = [np.ones(L, bool) for L in lens]
+    seen[10][640:656] = False
+    mod = dict(mod)
+    steep = mod.pop("steep", None)
+    kw = dict(mod)
+    if steep is not None:
+        mod["slopes"] = np.float32(steep) * np.linspace(0.01, 1, c.hq, dtype=np.float32)
+        kw["slopes"] = torch.from_numpy(mod["slopes"]).cuda()
+    out, lse = zf.q4_chunk_attn(*c.args(), **kw)
+    c.check(out, lse, seen=seen, **mod)
+    assert c.cache.status_word() == (zf.DEV_BAD_PAGE_ID if mod.get("window", 999) > 700 - 656 else 0)       # (no window reaches it)
+
+
+@pytest.mark.parametrize("window,new", [(1, 1), (40, 3), (100, 70), (129, 200)])
+def test_pages_behind_the_window_may_be_gone(zf, window, new):
+    c = Case(zf, 16, 2, 4, [900, 333], [new, new], seed=window)
+    for b, L in enumerate(c.lens):
+        c.table[b, :max(0, L - new + 1 - window) // 16] = -1
+    out, lse = zf.q4_chunk_attn(*c.args(), window=window)
+    c.check(out, lse, window=window)
+    assert c.cache.status_word() == 0
+
+
+@pytest.mark.parametrize("slopes", [False, True])
+def test_units_of_all_sizes_on_one_sm(zf, slopes):
+    """Many requests of few, some and many rows: each CTA goes from units of two tiles to units of one and back."""
+    rng = np.random.default_rng(3)
+    new = rng.choice([0, 1, 2, 4, 5, 20, 32, 33, 70], 150).tolist()
+    lens = [n + int(rng.choice([0, 1, 40, 200, 600])) for n in new]
+    c = Case(zf, 16, 3, 4, lens, new, seed=21)
+    slope = np.float32(2.0) ** -np.linspace(1, 8, c.hq, dtype=np.float32) if slopes else None
+    kw = dict(slopes=torch.from_numpy(slope).cuda()) if slopes else {}
+    out, lse = zf.q4_chunk_attn(*c.args(), **kw)
+    c.check(out, lse, slopes=slope)
+    assert c.cache.status_word() == 0
+
+
 def test_rows_of_no_request_are_left_alone(zf):
     c = Case(zf, 16, 2, 4, [50, 200], [5, 40], seed=2, lead=3, behind=6)
     out = torch.full((c.rows, c.hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
