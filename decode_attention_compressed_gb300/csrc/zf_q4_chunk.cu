@@ -95,6 +95,7 @@ struct ChunkArgs {
   float cap_log2, two_over_cap;  // cap * log2(e), 2 / cap (kCap: scores in log2 units to twice the tanh's argument in them)
   float v_factor;
   uint64_t wait_limit_ns;
+  int32_t hold;                  // tests: no piece is published before a wait for one has given up
 };
 
 struct Piece {
@@ -563,6 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       write_part(a, 0, nullptr, false);
       write_part(a, 1, nullptr, false);
     }
+    if (a.hold) {
+      const uint64_t t0 = global_timer_ns();
+      while (!*abort_flag && global_timer_ns() - t0 < 4 * a.wait_limit_ns) __nanosleep(1000);
+    }
     int n = 0;                     // pieces published
     uint32_t gs = 0;               // steps copied
     uint32_t started = 0, phase = 0;       // this lane's copies: stages used, parity of each one's last
@@ -627,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         };
         auto tile_of = [&](int s) {              // lane's tile of the steps from the s-th
           const int o = order<kMode>(s + (lane >> 3), p.steps);
-          return o < 0 ? 1 << 26 : (p.step0 + o) * 8 + (lane & 7);       // (behind every context)
+          return o < 0 ? INT_MAX / 16 - 1 : (p.step0 + o) * 8 + (lane & 7);       // (behind every context)
         };
         int next = page_of(tile_of(0));
         for (int s = 0; s < p.steps && ok; s += 4) {
@@ -1488,11 +1493,11 @@ extern "C" size_t zf_q4_chunk_attn_workspace_size(int32_t batch, int32_t rows, i
   return chunk_plan(rows, num_q_heads / num_kv_heads, sms).bytes();
 }
 
-extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, int32_t rows, int32_t batch,
-                                      int32_t num_q_heads, const int32_t* token_start, const int32_t* page_table,
-                                      int32_t max_pages, const int32_t* seq_lens, float softmax_scale, int32_t window,
-                                      float softcap, const float* slopes, uint16_t* out, float* lse, void* workspace,
-                                      size_t workspace_bytes, void* stream) {
+static zf_status q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, int32_t rows, int32_t batch, int32_t num_q_heads,
+                               const int32_t* token_start, const int32_t* page_table, int32_t max_pages,
+                               const int32_t* seq_lens, float softmax_scale, int32_t window, float softcap,
+                               const float* slopes, uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                               void* stream, uint64_t wait_limit_ns = kWaitTimeoutNs, bool hold = false) {
   zf_status st = check_q4_cache(c);
   if (st != ZF_OK) return st;
   if (!chunk_shape_ok(batch, rows, num_q_heads, c->num_kv_heads, c->page_size, max_pages)) return ZF_ERR_INVALID_ARGUMENT;
@@ -1544,7 +1549,8 @@ extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, i
   a.cap_log2 = softcap * kLog2e;
   a.two_over_cap = softcap > 0.f ? 2.f / softcap : 0.f;
   a.v_factor = c->v_scale * kQ4ScaleFactor;
-  a.wait_limit_ns = kWaitTimeoutNs;
+  a.wait_limit_ns = wait_limit_ns;
+  a.hold = hold;
 
   static std::mutex mu;
   static bool ready[64] = {};
@@ -1571,4 +1577,24 @@ extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, i
   st = launch(kernel, dim3(p.grid), kThreads, kSmTotal, s, a);
   if (st != ZF_OK) return st;
   return launch(q4_chunk_join_kernel, dim3(p.grid, p.part_rows / kJoinRows), 512, 0, s, a, p.grid);
+}
+
+extern "C" zf_status zf_q4_chunk_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t rows, int32_t batch,
+                                      int32_t num_q_heads, const int32_t* token_start, const int32_t* page_table,
+                                      int32_t max_pages, const int32_t* seq_lens, float softmax_scale, int32_t window,
+                                      float softcap, const float* slopes, uint16_t* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  return q4_chunk_attn(cache, q, rows, batch, num_q_heads, token_start, page_table, max_pages, seq_lens, softmax_scale, window,
+                       softcap, slopes, out, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" zf_status zf_q4_chunk_attn_wait_test(const zf_q4_cache* cache, const uint16_t* q, int32_t rows, int32_t batch,
+                                                int32_t num_q_heads, const int32_t* token_start,
+                                                const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                                float softmax_scale, int32_t window, float softcap, const float* slopes,
+                                                uint16_t* out, float* lse, void* workspace, size_t workspace_bytes,
+                                                uint64_t wait_limit_ns, void* stream) {
+  if (wait_limit_ns < 1000 || wait_limit_ns > kWaitTimeoutNs) return ZF_ERR_INVALID_ARGUMENT;
+  return q4_chunk_attn(cache, q, rows, batch, num_q_heads, token_start, page_table, max_pages, seq_lens, softmax_scale, window,
+                       softcap, slopes, out, lse, workspace, workspace_bytes, stream, wait_limit_ns, true);
 }

@@ -108,6 +108,10 @@ SIGNATURES = {
     "zf_q4_chunk_attn": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_int32, _c_int32, _c_int32, _c_void_p,
                                     _c_void_p, _c_int32, _c_void_p, _c_float, _c_int32, _c_float, _c_void_p, _c_void_p,
                                     _c_void_p, _c_void_p, _c_size_t, _c_void_p]),
+    "zf_q4_chunk_attn_wait_test": (_c_int32, [ctypes.POINTER(ZfQ4CacheDesc), _c_void_p, _c_int32, _c_int32, _c_int32,
+                                              _c_void_p, _c_void_p, _c_int32, _c_void_p, _c_float, _c_int32, _c_float,
+                                              _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_size_t, ctypes.c_uint64,
+                                              _c_void_p]),
     "zf_map_tokens": (_c_int32, [_c_int32, _c_int32, _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_int32, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                  _c_void_p, _c_int32, _c_void_p, _c_void_p]),
@@ -756,6 +760,29 @@ def q4_chunk_attn(cache: Q4Cache, q, page_table, seq_lens, token_start, scale=No
                                   workspace.nbytes, s)
     if code:
         _check("zf_q4_chunk_attn", code)
+    return out, lse
+
+
+@_on_stream
+def q4_chunk_attn_wait_test(cache: Q4Cache, q, page_table, seq_lens, token_start, wait_limit_ns=1000000):
+    """zf_q4_chunk_attn_wait_test (tests of the failure path): q4_chunk_attn whose warps' first wait for work runs out
+    after wait_limit_ns.  Returns (out, lse), which are not meaningful; the cache's status word gets DEV_TIMEOUT."""
+    dev = cache._device
+    N, Hq = q.shape[:2]
+    q = _tensor(q, "q", _BITS16, dev, (N, Hq, HEAD_DIM))
+    token_start = _tensor(token_start, "token_start", _I32, dev, token_start.shape)
+    B = token_start.shape[0] - 1
+    page_table, seq_lens = _tables(page_table, seq_lens, dev, B)
+    max_pages = page_table.shape[1]
+    s = _launch_stream(dev)
+    out = torch.empty((N, Hq, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
+    workspace = new_workspace(q4_chunk_workspace_size(B, N, Hq, cache._sizes[1], cache._sizes[2], max_pages), dev)
+    _check("zf_q4_chunk_attn_wait_test",
+           lib().zf_q4_chunk_attn_wait_test(cache._ref, q.data_ptr(), N, B, Hq, token_start.data_ptr(), page_table.data_ptr(),
+                                            max_pages, seq_lens.data_ptr(), 1.0 / math.sqrt(HEAD_DIM), 0, 0.0, None,
+                                            out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                            int(wait_limit_ns), s))
     return out, lse
 
 

@@ -512,7 +512,9 @@ size_t zf_q4_chunk_attn_workspace_size(int32_t batch, int32_t rows, int32_t num_
  *   both set ZF_DEV_BAD_SEQ_LEN.  A page id out of range sets ZF_DEV_BAD_PAGE_ID and its tokens are not seen.
  *   A wait that takes 2 s gives up: it sets ZF_DEV_TIMEOUT, and out and lse of that call mean nothing.
  *   With a window, pages that lie before the windows of all new tokens of a request need not be there.
- *   batch <= ZF_MAX_BATCH.  rows == 0 or batch == 0 is a no-op.  Two kernels (attention, then the joining of units
+ *   batch <= ZF_MAX_BATCH, rows * num_q_heads < 2^31; ZF_ERR_UNSUPPORTED when all units (kv heads times the requests and
+ *   the 256-row parts of the rows) times the steps of the longest context (128 tokens) would pass 2^31.  rows == 0 or
+ *   batch == 0 is a no-op.  Two kernels (attention, then the joining of units
  *   split over CTAs), launched with programmatic stream serialisation; results are deterministic (no atomics).
  */
 zf_status zf_q4_chunk_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t rows, int32_t batch,
@@ -520,6 +522,18 @@ zf_status zf_q4_chunk_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t 
                            int32_t max_pages_per_req, const int32_t* seq_lens, float softmax_scale, int32_t window,
                            float softcap, const float* slopes, uint16_t* out, float* lse, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/*
+ * zf_q4_chunk_attn_wait_test — for tests of the failure path: zf_q4_chunk_attn whose warps' first wait for work runs
+ * out on purpose after wait_limit_ns (1 us .. 2 s).  ZF_DEV_TIMEOUT is then set, copies in flight land, out and lse mean
+ * nothing, and the context and the stream stay usable for the next call.  No fault, trap or endless wait is involved.
+ * ZF_ERR_INVALID_ARGUMENT for a limit out of range; other arguments as for zf_q4_chunk_attn.
+ */
+zf_status zf_q4_chunk_attn_wait_test(const zf_q4_cache* cache, const uint16_t* q, int32_t rows, int32_t batch,
+                                     int32_t num_q_heads, const int32_t* token_start, const int32_t* page_table,
+                                     int32_t max_pages_per_req, const int32_t* seq_lens, float softmax_scale,
+                                     int32_t window, float softcap, const float* slopes, uint16_t* out, float* lse,
+                                     void* workspace, size_t workspace_bytes, uint64_t wait_limit_ns, void* stream);
 
 /*
  * zf_map_tokens — block tables and slot maps on the GPU: gives every request's new tokens their

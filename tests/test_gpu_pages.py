@@ -314,3 +314,70 @@ def test_a_serving_loop(zf, graph):
     consistent()
     place([1, 1, 33, 2, 1, 7])
     consistent()
+
+
+def test_behind_a_late_writer(zf):
+    """The kernel ahead lets the next one start and then writes what that one reads."""
+    late = H.late_writer()
+    p = Pool(40, 50, 16, 31, empty=0.3)
+    share(p)
+    s = torch.cuda.current_stream().cuda_stream
+    table, lens, held = dev(p.table), dev(p.lens), dev(p.held)
+    src = [b for b in range(40) if p.held[b]][:6]
+    dst = [b for b in range(40) if not p.held[b]][:6]
+    n = min(len(src), len(dst))
+    src, dst = src[:n], dst[:n]
+    free, pos = dev(p.free), dev([p.pos])
+    gone = dev([b % 2 for b in range(40)])
+
+    def behind(small, big, call):
+        d_small, d_big = torch.zeros_like(small), torch.zeros_like(big)
+        torch.cuda.synchronize()
+        assert late(small.data_ptr(), d_small.data_ptr(), small.numel(), big.data_ptr(), d_big.data_ptr(), big.numel(), 300000, s) == 0
+        out = call(d_small, d_big)
+        torch.cuda.synchronize()
+        return out
+
+    want = R.fork(p.table, p.lens, p.held, src, dst, p.free, p.pos, 16)
+    f = behind(dev(src), table, lambda a, t: (zf.fork_requests(t, lens, held, a, dev(dst), free, pos, 16), t))
+    assert (f[1].cpu().numpy() == want[0]).all() and f[0].copy_src.tolist() == want[4] and f[0].seq_lens.tolist() == want[1]
+    wl, wh, wf, wp, _ = R.release(p.table, p.lens, p.held, gone.tolist(), p.free, p.pos, p.pool)
+    ws = torch.empty(zf.release_workspace_size(p.pool), dtype=torch.uint8, device="cuda")
+    r = behind(gone, table, lambda a, t: zf.release_requests(t, lens, held, a, free, pos, p.pool, workspace=ws))
+    assert r.seq_lens.tolist() == wl and free.tolist() == wf and r.free_pos.tolist() == [wp]
+    want = R.compact(p.table, p.held, p.pool)
+    wc = torch.empty(zf.compact_workspace_size(p.pool), dtype=torch.uint8, device="cuda")
+    c = behind(held, table, lambda h, t: zf.compact_pages(t, h, p.pool, workspace=wc))
+    assert (c.page_table.cpu().numpy() == want[0]).all() and c.copy_src.tolist() == want[3]
+    cache = zf.Q4Cache(8, 1, 16)
+    cache.records.copy_(torch.randint(0, 255, cache.records.shape, dtype=torch.uint8, device="cuda"))
+    before = cache.records.clone().view(8, -1)
+    behind(dev([5, 2]), dev([0, 7]), lambda a, b: zf.q4_copy_pages(cache, a, b))
+    after = cache.records.view(8, -1)
+    assert torch.equal(after[0], before[5]) and torch.equal(after[7], before[2]) and torch.equal(after[1:7], before[1:7])
+
+
+def test_two_streams_at_once(zf):
+    """The same calls on two streams, each with its own workspace and outputs."""
+    p = Pool(200, 300, 16, 33, empty=0.2)
+    share(p)
+    table, lens, held, gone = dev(p.table), dev(p.lens), dev(p.held), dev([b % 3 == 0 for b in range(200)])
+    want = R.release(p.table, p.lens, p.held, gone.tolist(), p.free, p.pos, p.pool)
+    packed = R.compact(p.table, p.held, p.pool)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ws = [torch.empty(zf.release_workspace_size(p.pool), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    wc = [torch.empty(zf.compact_workspace_size(p.pool), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    lists = [[dev(p.free) for _ in range(4)] for _ in range(2)]
+    pos = dev([p.pos])
+    torch.cuda.synchronize()
+    done = [[], []]
+    for k in range(4):
+        for i, s in enumerate(streams):
+            done[i].append((zf.release_requests(table, lens, held, gone, lists[i][k], pos, p.pool, workspace=ws[i], stream=s),
+                            zf.compact_pages(table, held, p.pool, workspace=wc[i], stream=s)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for k in range(4):
+            r, c = done[i][k]
+            assert r.pages_held.tolist() == want[1] and lists[i][k].tolist() == want[2] and r.free_pos.tolist() == [want[3]]
+            assert (c.page_table.cpu().numpy() == packed[0]).all() and c.free_pages.tolist() == packed[1]

@@ -386,3 +386,22 @@ def test_behind_a_late_writer(zf):
     zf.q4_chunk_attn(cache, d_q, table, d_lens, d_start, out=out, lse=lse, workspace=ws)
     torch.cuda.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_wait_that_runs_out_reports_timeout_and_the_next_call_is_right(zf):
+    """The first wait of every CTA's warps is made to run out: the call reports it and ends, and the next one, right
+    behind it on the same stream, gives what it gave before."""
+    c = Case(zf, 16, 2, 4, [900, 37, 129, 400], [200, 1, 4, 40], seed=14)
+    args = c.args()
+    want = zf.q4_chunk_attn(*args)
+    for limit in (1000, 200_000):
+        zf.q4_chunk_attn_wait_test(*args, wait_limit_ns=limit)
+        got = zf.q4_chunk_attn(*args)
+        torch.cuda.synchronize()
+        assert c.cache.status_word() == zf.DEV_TIMEOUT
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        c.cache.status.zero_()
+    for limit in (0, 999, 2_000_000_001):
+        with pytest.raises(zf.ZfError, match="invalid argument"):
+            zf.q4_chunk_attn_wait_test(*args, wait_limit_ns=limit)
+    assert c.cache.status_word() == 0

@@ -174,3 +174,35 @@ def test_probabilities_alone_and_captured(zf):
     again = zf.sample_tokens(x, u, top_p=p, stream=s)
     s.synchronize()
     assert torch.equal(again, want)
+
+
+def test_behind_a_late_writer(zf):
+    """The kernel ahead lets the next one start and then writes the logits and the top-k."""
+    late = H.late_writer()
+    x, k = logits_of(20, 50000, 11, torch.bfloat16).cuda(), torch.arange(20, dtype=torch.int32, device="cuda") * 30
+    u, p = torch.rand(20, device="cuda"), torch.full((20,), 0.8, device="cuda")
+    want = zf.sample_tokens(x, u, top_k=k, top_p=p)
+    d_x, d_k = torch.zeros_like(x), torch.zeros_like(k)
+    out = torch.empty_like(want)
+    torch.cuda.synchronize()
+    s = torch.cuda.current_stream().cuda_stream
+    assert late(k.data_ptr(), d_k.data_ptr(), 20, x.data_ptr(), d_x.data_ptr(), x.numel() // 2, 300000, s) == 0
+    zf.sample_tokens(d_x, u, top_k=d_k, top_p=p, tokens=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_few_and_many_candidates(zf, dtype):
+    """Around the number of candidates that are listed at once, by top-k and by min-p, with ties across the border."""
+    V = 20000
+    g = torch.Generator().manual_seed(12)
+    x = (torch.randn(8, V, generator=g) * 3).to(dtype)
+    tied = (torch.randn(8, V, generator=g) * 3).round().to(dtype)
+    u = torch.rand(8, generator=g).numpy()
+    for y in (x, tied):
+        check(zf, y, u, top_k=[1, 2, 500, 511, 512, 513, 600, 1024])
+        check(zf, y, u, top_k=[1, 2, 500, 511, 512, 513, 600, 1024], top_p=[0.0, 0.3, 0.9, 0.999, 0.5, 0.99, 0.7, 0.2])
+        check(zf, y, u, min_p=[1.0, 0.9, 0.5, 0.2, 0.1, 0.05, 0.01, 1e-30], top_p=[0.9, 0.0, 0.5, 0.7, 0.9, 0.95, 0.99, 0.3])
+        check(zf, y, u, top_k=[3, 9, 40, 100, 300, 505, 30, 20], min_p=[1.0, 0.9, 0.5, 0.2, 0.1, 0.05, 0.01, 1e-30],
+              top_p=[0.9, 0.0, 0.5, 0.7, 0.9, 0.95, 0.99, 0.3], temperature=[0.1, 0.5, 1.0, 2.0, 5.0, 1.5, 0.01, 1.0])
