@@ -29,8 +29,8 @@
 // Bound: a row's bytes once from memory are 1.7 to 4 us of the 22 to 40 that a cluster is busy.  The histogram's
 // atomics (128000 entries on four CTAs, two CTAs per SM: 7.6 us) and the exponentials of steps 5 and 6 (10 and 7 us for
 // 50001 entries), about 55 instructions each, more than half of them on integers, are the rest, with a chain of 8 to 12
-// cluster barriers and exchanges of 1 to 2.5 us each.  64 rows of 128000 BF16 logits: 38 us; 320 rows of 50001 FP32
-// logits with their probabilities written: 190 us (4.2 rounds of the CTAs that fit).
+// cluster barriers and exchanges of 1 to 2.5 us each.  64 rows of 128000 BF16 logits: 37 us; 320 rows of 50001 FP32
+// logits with their probabilities written: 182 us (4.2 rounds of the CTAs that fit).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -260,6 +260,21 @@ struct Shared {
 };
 // (both are read and written 16 bytes at a time)
 static_assert(offsetof(Shared, list) % 16 == 0 && offsetof(Shared, bins) % 16 == 0 && sizeof(Shared) % 16 == 0, "layout");
+
+// Whether an entry's weight is min-p's or more, to 32 bits of the weight.  (Few entries are so close: not inlined, as the
+// kernel's passes are short and wait for their instructions: 320 x 50001 with probabilities 190 -> 182 us.)
+__device__ __noinline__ bool min_keeps(Scale s, float x, float p_min, const uint32_t* table) {
+  Weight w = weight(s, x, table);
+  if (w.m < 0x80000000u) {
+    w.m <<= 1;
+    w.shift -= 1;
+  }
+  int e;
+  const float m = frexpf(p_min, &e);               // p_min = m 2^e, m in [0.5, 1)
+  const unsigned long long want = static_cast<unsigned long long>(m * 16777216.f) << 8;   // m 2^32
+  const int d = w.shift + 1 - e;                   // w = (m_w / 2^32) 2^(shift + 1)
+  return d == 0 ? static_cast<unsigned long long>(w.m) >= want : d > 0;
+}
 
 template <typename T, bool kVec>
 struct Row {
@@ -700,18 +715,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     sure = __fsub_ru(s.max, gap * 0.99999f);
     out = __fsub_rd(s.max, gap * 1.00001f);
   }
-  auto above_min = [&](float x) {                  // to 32 bits of the weight
-    Weight w = weight(s, x, sh.table);
-    if (w.m < 0x80000000u) {
-      w.m <<= 1;
-      w.shift -= 1;
-    }
-    int e;
-    const float m = frexpf(p_min, &e);             // p_min = m 2^e, m in [0.5, 1)
-    const unsigned long long want = static_cast<unsigned long long>(m * 16777216.f) << 8;   // m 2^32
-    const int d = w.shift + 1 - e;                 // w = (m_w / 2^32) 2^(shift + 1)
-    return d == 0 ? static_cast<unsigned long long>(w.m) >= want : d > 0;
-  };
+  auto above_min = [&](float x) { return min_keeps(s, x, p_min, sh.table); };
   auto bound = [&](unsigned long long last) {      // nothing behind this place is kept
     if (last >= limit) return;
     limit = last;
