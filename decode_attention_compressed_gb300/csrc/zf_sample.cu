@@ -1068,14 +1068,19 @@ extern "C" zf_status zf_sample_tokens(int32_t rows, int32_t vocab, const void* l
   a.row_stride = row_stride;
   a.rows = rows;
   a.vocab = vocab;
-  // CTAs per row: a power of two, as long as all rows' CTAs run at once (two per SM) and each has 4096 entries, and so many
-  // that a slice is no more than 72 KB (two CTAs' fit an SM then); slices are kept whole up to 160 KB, and read again
-  // from L2 beyond.
+  // CTAs per row: a power of two, as long as all rows' CTAs run at once (two per SM; clusters of 16 find room for about
+  // one per SM) and each has 2560 entries; and so many that a slice is no more than 72 KB (two CTAs' fit an SM then),
+  // where eight are enough for slices of 160 KB, which are still kept whole (beyond, they are read again from L2).
+  // Measured with top-p, us for 1, 2, 4, 8, 16 CTAs: 32000 BF16, 8 rows 42, 29, 22, 19, 23, 64 rows 45, 37, 29, 44, 100,
+  // 256 rows 60, 72, 96, 155, 360; 8192, 32 rows 18, 17, 18, 20, 55; 128000, 1 row -, 80, 47, 31, 28, 64 rows -, 84, 75, 92,
+  // 151; 256000 FP32, 128 rows 423 with 8 (slices of 128 KB), 486 with 16.
   const size_t fixed_smem = (sizeof(Shared) + 15) & ~static_cast<size_t>(15);
   int ctas = 1;
-  while (ctas < kMaxCluster && ((vocab / (2 * ctas) >= 4096 && static_cast<long long>(rows) * 2 * ctas <= 304) ||
-                                static_cast<long long>(vocab) * size / ctas > 73728))
+  while (ctas < kMaxCluster) {
+    const long long all = static_cast<long long>(rows) * 2 * ctas, bytes = static_cast<long long>(vocab) * size / ctas;
+    if (!(vocab / (2 * ctas) >= 2560 && all <= (2 * ctas == kMaxCluster ? 152 : 304)) && bytes <= (ctas < 8 ? 73728 : 163840)) break;
     ctas *= 2;
+  }
   a.slice = ((vocab + ctas - 1) / ctas + 7) & ~7;
   const size_t bytes = static_cast<size_t>(a.slice) * size;
   a.cached = bytes <= 163840;
