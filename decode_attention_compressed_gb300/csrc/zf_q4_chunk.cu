@@ -94,7 +94,7 @@ struct ChunkArgs {
   float scale_log2;              // softmax scale * log2(e) * the decoding's factors
   float cap_log2, two_over_cap;  // cap * log2(e), 2 / cap (kCap: scores in log2 units to twice the tanh's argument in them)
   float v_factor;
-  uint64_t wait_limit_ns;
+  uint32_t wait_limit_ns;        // at most 2 s
   int32_t hold;                  // tests: no piece is published before a wait for one has given up
 };
 
@@ -264,15 +264,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// A bounded wait that also ends when another warp's has given up (abort_flag).
+// A bounded wait that also ends when another warp's has given up (abort_flag; reported when the CTA ends).  Waits stand in
+// some thirty places, so they are short.
+__device__ __forceinline__ uint32_t timer_ns() {
+  uint32_t t;
+  asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+  return t;
+}
 __device__ __forceinline__ bool wait_longer(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const ChunkArgs& a) {
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t i = 0; i < (1u << 30) && !*abort_flag; ++i) {
+  const uint32_t t0 = timer_ns();
+  while (!*abort_flag) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (global_timer_ns() - t0 > a.wait_limit_ns) break;
+    if (timer_ns() - t0 > a.wait_limit_ns) *abort_flag = 1;
   }
-  if (!*abort_flag) report(a.status, ZF_DEV_TIMEOUT);
-  *abort_flag = 1;
   return false;
 }
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const ChunkArgs& a) {
@@ -369,6 +373,20 @@ __device__ __forceinline__ Place find_place(const ChunkArgs& a, const int* sums,
     rest -= __shfl_sync(0xFFFFFFFFu, in, 31);
   }
   return p;                                          // (not reached: rest < head)
+}
+
+// Lane q of each four has column q of a 4 x 4 matrix and gets row q.
+__device__ __forceinline__ void transpose4(uint32_t (&w)[4], int q) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, q & 1 ? w[i] : w[i + 1], 1);
+    if (q & 1) w[i] = x; else w[i + 1] = x;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t x = __shfl_xor_sync(0xFFFFFFFFu, q & 2 ? w[i] : w[i + 2], 2);
+    if (q & 2) w[i] = x; else w[i + 2] = x;
+  }
 }
 
 // Which rows a partial belongs to: {valid, q0, row0, rows}, {kv head, whether the unit ends here, 0, 0}.
@@ -546,8 +564,11 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     const int ctas = min(static_cast<int>(gridDim.x), (total + kMinCost - 1) / kMinCost), at = blockIdx.x;
     if (at < ctas) {
       const int each = total / ctas, more = total - each * ctas;       // the first `more` CTAs take one more
-      from = find_place(a, sums, each * at + min(at, more), lane);
-      to = find_place(a, sums, each * (at + 1) + min(at + 1, more), lane);
+#pragma unroll 1
+      for (int k = at; k <= at + 1; ++k) {             // (one place in the code)
+        from = to;
+        to = find_place(a, sums, each * k + min(k, more), lane);
+      }
     }
   }
   tcgen05_after_sync();
@@ -566,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     }
     if (a.hold) {
       const uint64_t t0 = global_timer_ns();
-      while (!*abort_flag && global_timer_ns() - t0 < 4 * a.wait_limit_ns) __nanosleep(1000);
+      while (!*abort_flag && global_timer_ns() - t0 < 4ull * a.wait_limit_ns) __nanosleep(1000);
     }
     int n = 0;                     // pieces published
     uint32_t gs = 0;               // steps copied
@@ -635,6 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           return o < 0 ? INT_MAX / 16 - 1 : (p.step0 + o) * 8 + (lane & 7);       // (behind every context)
         };
         int next = page_of(tile_of(0));
+        // its query rows, for the softmax warps
+        for (int i = lane; i < p.rows; i += 32) {
+          const int tok = (p.row0 + i) / a.group, h = p.g * a.group + (p.row0 + i - tok * a.group);
+          const uint16_t* at_q = a.q + (static_cast<size_t>(p.q0 + tok) * a.hq + h) * ZF_HEAD_DIM;
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(at_q));
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(at_q + 64));
+        }
         for (int s = 0; s < p.steps && ok; s += 4) {
           int cur = next;
           if (tile_of(s) * 16 < p.last && tile_of(s) * 16 + 16 > from && (cur < 0 || cur >= a.num_pages)) {
@@ -873,15 +901,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     // The warp's 16 rows of tile t of the query operand: 4 KB that no other warp writes.
     auto my_q = [&](int t) { return smem + (t ? kSmQ1 : kSmQ0) + (row16 >> 3) * kCoreRow; };
 
-    // Query rows of a piece, 16 of each tile: lane (row lane % 8 of 8, chunks lane / 8 + 4 i of 16 bytes).  They are read
-    // while the piece before ends.  Up to 16 rows: every warp has the same.
-    uint4 qv[2][2][4];
-    auto q_load = [&](int buf) {
+    // Query rows of a piece, 16 of each tile: lane (row lane % 8 of 8, chunks lane / 8 + 4 i of 16 bytes).  (The walk has
+    // brought them to L2.)  Up to 16 rows: every warp has the same.
+    auto q_rows = [&](int buf) {
       const Piece& p = pieces[buf];
       const int tiles = p.rows > 128 ? 2 : 1, copy = p.rows <= kFewRows ? row16 : 0;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t >= tiles) break;
+      const bool negate = a.scale_log2 < 0.f, wanted = p.steps > 0;
+#pragma unroll 1
+      for (int t = 0; t < tiles; ++t) {
+        uint4 qv[2][4];
         int low = INT_MAX, high = INT_MIN;
 #pragma unroll
         for (int r8 = 0; r8 < 2; ++r8) {
@@ -891,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           const int place = (p.q0 + tok) * a.hq + h;
           const uint4* src = reinterpret_cast<const uint4*>(a.q + static_cast<size_t>(place) * ZF_HEAD_DIM);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qv[t][r8][i] = in ? src[(lane >> 3) + 4 * i] : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i) qv[r8][i] = in ? src[(lane >> 3) + 4 * i] : make_uint4(0u, 0u, 0u, 0u);
           low = min(low, p.pos0 + tok);
           high = max(high, p.pos0 + tok);
           if (lane < 8) {
@@ -905,21 +933,15 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         high = __reduce_max_sync(0xFFFFFFFFu, high);
         const int begin = a.window > 0 ? (max(high + 1 - a.window, 0) + kStep - 1) / kStep : 0;
         if (lane == 0) whole_of(buf, t) = make_int2(begin, max((low + 1) / kStep - begin, 0));
-      }
-    };
-    auto q_store = [&](int buf) {
-      const int tiles = pieces[buf].rows > 128 ? 2 : 1;
-      const bool negate = a.scale_log2 < 0.f;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t >= tiles) break;
+        if (!wanted) continue;
 #pragma unroll
         for (int r8 = 0; r8 < 2; ++r8) {
           uint32_t big = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint4 x = qv[t][r8][i];
-            const uint32_t m2 = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+            const uint4 x = qv[r8][i];
+            const uint32_t m2 = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu),
+                                         __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
             big = max(big, max(m2 & 0xFFFFu, m2 >> 16));
           }
           big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 8));
@@ -933,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
                 fmaxf(__int_as_float((127 - k) << 23) * fabsf(a.scale_log2), 1e-37f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t w[4] = {qv[t][r8][i].x, qv[t][r8][i].y, qv[t][r8][i].z, qv[t][r8][i].w};
+            const uint32_t w[4] = {qv[r8][i].x, qv[r8][i].y, qv[r8][i].z, qv[r8][i].w};
             uint32_t y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = pack_f16(bf16lo_to_f32(w[e]) * f, bf16hi_to_f32(w[e]) * f);
@@ -942,6 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
           }
         }
       }
+      if (!wanted) return;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarQFull]);
@@ -958,16 +981,151 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
       if (lane == 0) mbar_arrive(&bars[kBarFew]);
       return wait_warp(&bars[kBarFew], met++ & 1, abort_flag, a);
     };
-    bool ok = wait_warp(&bars[kBarPieceFull], 0, abort_flag, a);
-    if (ok && pieces[0].b >= 0) {
-      q_load(0);
-      if (pieces[0].steps > 0) q_store(0);
-    }
-    for (int n = 0; ok && pieces[n & 1].b >= 0; ++n) {
+    bool ok = true;
+    // The end of a piece of up to 16 rows.
+    auto finish_few = [&](int buf, Rows& st) {
+      // the parts of the output, through the query operand (32 KB, free now) in two halves of 64 channels:
+      // [warp][row][64], 8 channels c of row r at c ^ 8 (r & 7)
+      float2* rows = reinterpret_cast<float2*>(smem + kSmFew);
+      float* parts = reinterpret_cast<float*>(smem + kSmQ0);
+      const Piece& p = pieces[buf];
+      const int slot = p.slot, live = p.rows;
+      const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * a.part_rows;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        st.sum[r] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[r], 1);
+        st.sum[r] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[r], 2);
+        if (quad == 0) rows[warp * kFewRows + (lane >> 2) + 8 * r] = make_float2(st.c[r], st.sum[r]);
+      }
+      if (!(ok = meet())) return;
+      float f[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = (lane >> 2) + 8 * r;
+        const float2 p0 = rows[2 * quad * kFewRows + row], p1 = rows[(2 * quad + 1) * kFewRows + row];
+        float c = fminf(p0.x, p1.x);
+        c = fminf(c, __shfl_xor_sync(0xFFFFFFFFu, c, 1));
+        c = fminf(c, __shfl_xor_sync(0xFFFFFFFFu, c, 2));
+        float sum = p0.y * fast_exp2(c - p0.x) + p1.y * fast_exp2(c - p1.x);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        const bool none = sum == 0.f;
+        f[r] = none ? 0.f : fast_exp2(c - st.c[r]) * (slot >= 0 ? 1.f : a.v_factor / sum);
+        if (warp == 0 && quad == 0 && row < live) {
+          if (slot < 0) a.lse[places[buf * kUnitRows + row]] = none ? -CUDART_INF_F : (log2f(sum) - c) * kLn2f;
+          else a.part_ml[part + row] = make_float2(none ? -CUDART_INF_F : -c, sum);
+        }
+      }
+      const int row = threadIdx.x >> 4, four = threadIdx.x & 15;
+#pragma unroll 1
+      for (int k = 0; k < 2 && ok; ++k) {
+        uint32_t u[32];
+        tmem_ld_16x256b_x8(lanes + kTmemO + 64 * k, u);
+        tmem_wait_ld();
+        touch(u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if ((lane >> 2) + 8 * r < live)
+              *reinterpret_cast<float2*>(parts + (warp * kFewRows + (lane >> 2) + 8 * r) * 64 + ((8 * i) ^ (8 * (lane >> 2))) + 2 * quad) =
+                  make_float2(__uint_as_float(u[4 * i + 2 * r]) * f[r], __uint_as_float(u[4 * i + 2 * r + 1]) * f[r]);
+        if (!(ok = meet())) return;
+        if (row < live) {
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(parts + (w * kFewRows + row) * 64 + ((4 * four) ^ (8 * (row & 7))));
+            o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
+          }
+          if (slot < 0)
+            *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(places[buf * kUnitRows + row]) * ZF_HEAD_DIM + 64 * k + 4 * four) =
+                make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+          else
+            *reinterpret_cast<float4*>(a.part_o + (part + row) * ZF_HEAD_DIM + 64 * k + 4 * four) = o;
+        }
+        ok = meet();
+      }
+    };
+    // The end of any other piece.
+    auto finish = [&](int buf, Rows& st, const Rows& other) {
+      const Piece& p = pieces[buf];
+      const bool both = p.rows > 128;
+      const int steps = p.steps;
+#pragma unroll 1
+      for (int t = 0; t < (both ? 2 : 1); ++t) {
+        const int slot = p.slot, first = 128 * t + row16, live = min(16, p.rows - first);      // rows of this warp
+        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * a.part_rows;
+        float f[2];
+        int to[2];                                            // this lane's rows' places in out and lse
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          to[r] = places[buf * kUnitRows + first + (lane >> 2) + 8 * r];
+          float sum = st.sum[r];
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+          const bool none = sum == 0.f;
+          f[r] = slot >= 0 ? 1.f : none ? 0.f : a.v_factor / sum;
+          if (quad == 0 && (lane >> 2) + 8 * r < live) {
+            if (slot < 0) a.lse[to[r]] = none ? -CUDART_INF_F : (log2f(sum) - st.c[r]) * kLn2f;
+            else a.part_ml[part + first + (lane >> 2) + 8 * r] = make_float2(none ? -CUDART_INF_F : -st.c[r], sum);
+          }
+        }
+        // 64 columns: rows lane / 4 (+ 8), columns 8 i + 2 quad (+ 1)
+        auto columns = [&](int k, uint32_t (&u)[32]) {
+          if (steps > 0) {
+            tmem_ld_16x256b_x8(lanes + kTmemO + 128 * t + 64 * k, u);
+            tmem_wait_ld();
+            touch(u);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) u[e] = steps > 0 ? __float_as_uint(__uint_as_float(u[e]) * f[(e >> 1) & 1]) : 0u;
+        };
+        if (slot < 0) {
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) {
+            uint32_t u[32];
+            columns(k, u);
+            // lane q of the four with a row has words q of its 16-byte chunks: it gets chunks q and q + 4
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  w[i] = pack_bf16x2(__uint_as_float(u[4 * (4 * h + i) + 2 * r]), __uint_as_float(u[4 * (4 * h + i) + 2 * r + 1]));
+                transpose4(w, quad);
+                if ((lane >> 2) + 8 * r < live)
+                  reinterpret_cast<uint4*>(a.out + static_cast<size_t>(to[r]) * ZF_HEAD_DIM)[8 * k + 4 * h + quad] =
+                      make_uint4(w[0], w[1], w[2], w[3]);
+              }
+          }
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) {
+            uint32_t u[32];
+            columns(k, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r)
+                if ((lane >> 2) + 8 * r < live)
+                  *reinterpret_cast<uint2*>(a.part_o + (part + first + (lane >> 2) + 8 * r) * ZF_HEAD_DIM + 64 * k + 8 * i + 2 * quad) =
+                      make_uint2(u[4 * i + 2 * r], u[4 * i + 2 * r + 1]);
+          }
+        }
+        st = other;
+      }
+    };
+
+    // (from -1: the first piece's query rows are read where the next one's are, as instructions that run once wait for
+    // themselves longer than for anything else)
+    for (int n = -1;; ++n) {
       // (a piece is read from shared memory where it is needed: registers are short in the loop over its jobs)
       const int buf = n & 1;
-      const bool both = pieces[buf].rows > 128;
-      const int steps = pieces[buf].steps, step0 = pieces[buf].step0, count = both ? 2 * steps : steps;
+      const bool both = n >= 0 && pieces[buf].rows > 128;
+      const int steps = n >= 0 ? pieces[buf].steps : 0, step0 = pieces[buf].step0, count = both ? 2 * steps : steps;
       Rows st{{kNone, kNone}, {0.f, 0.f}}, other = st;
       const bool few = pieces[buf].rows <= kFewRows && steps > 0;
       if (few) {
@@ -1234,10 +1392,10 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         }
       }
       if (!ok) break;
-      // ---- the end of the piece: output rows, through the warp's part of the query operand (free once the products are
-      // done) so that they go to memory in one piece: 16 bytes c of row r lie at c ^ (r & 7)
+      // ---- the end of the piece.  The next one's query rows come first, so that its first scores are computed while the
+      // output goes out (of up to 16 rows: through the query operand, so before)
       if (!(ok = wait_warp(&bars[kBarPieceFull + (buf ^ 1)], ((n + 1) >> 1) & 1, abort_flag, a))) break;
-      if (pieces[buf ^ 1].b >= 0) q_load(buf ^ 1);
+      const bool more = pieces[buf ^ 1].b >= 0;
       if (steps > 0) {
         // (two tiles: announced once; one: for every step, and the one two before was complete when its scores were)
         if (both) done ^= 1u;
@@ -1245,148 +1403,31 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         if (!(ok = wait_warp(&bars[kBarPvDone + b], ((done >> b) & 1) ^ 1, abort_flag, a))) break;
         tcgen05_after_sync();
       }
-      if (few) {
-        // the parts of the output, through the query operand (32 KB, free now) in two halves of 64 channels:
-        // [warp][row][64], 8 channels c of row r at c ^ 8 (r & 7)
-        float2* rows = reinterpret_cast<float2*>(smem + kSmFew);
-        float* parts = reinterpret_cast<float*>(smem + kSmQ0);
-        const Piece& p = pieces[buf];
-        const int slot = p.slot, live = p.rows;
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * a.part_rows;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          st.sum[r] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[r], 1);
-          st.sum[r] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[r], 2);
-          if (quad == 0) rows[warp * kFewRows + (lane >> 2) + 8 * r] = make_float2(st.c[r], st.sum[r]);
-        }
-        if (!(ok = meet())) break;
-        float f[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = (lane >> 2) + 8 * r;
-          float c = kNone, sum = 0.f;
-#pragma unroll
-          for (int w = 0; w < 8; ++w) c = fminf(c, rows[w * kFewRows + row].x);
-#pragma unroll
-          for (int w = 0; w < 8; ++w) sum += rows[w * kFewRows + row].y * fast_exp2(c - rows[w * kFewRows + row].x);
-          const bool none = sum == 0.f;
-          f[r] = none ? 0.f : fast_exp2(c - st.c[r]) * (slot >= 0 ? 1.f : a.v_factor / sum);
-          if (warp == 0 && quad == 0 && row < live) {
-            if (slot < 0) a.lse[places[buf * kUnitRows + row]] = none ? -CUDART_INF_F : (log2f(sum) - c) * kLn2f;
-            else a.part_ml[part + row] = make_float2(none ? -CUDART_INF_F : -c, sum);
-          }
-        }
-        const int row = threadIdx.x >> 4, four = threadIdx.x & 15;
 #pragma unroll 1
-        for (int k = 0; k < 2 && ok; ++k) {
-          uint32_t u[32];
-          tmem_ld_16x256b_x8(lanes + kTmemO + 64 * k, u);
-          tmem_wait_ld();
-          touch(u);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if ((lane >> 2) + 8 * r < live)
-                *reinterpret_cast<float2*>(parts + (warp * kFewRows + (lane >> 2) + 8 * r) * 64 + ((8 * i) ^ (8 * (lane >> 2))) + 2 * quad) =
-                    make_float2(__uint_as_float(u[4 * i + 2 * r]) * f[r], __uint_as_float(u[4 * i + 2 * r + 1]) * f[r]);
-          if (!(ok = meet())) break;
-          if (row < live) {
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-              const float4 x = *reinterpret_cast<const float4*>(parts + (w * kFewRows + row) * 64 + ((4 * four) ^ (8 * (row & 7))));
-              o = make_float4(o.x + x.x, o.y + x.y, o.z + x.z, o.w + x.w);
-            }
-            if (slot < 0)
-              *reinterpret_cast<uint2*>(a.out + static_cast<size_t>(places[buf * kUnitRows + row]) * ZF_HEAD_DIM + 64 * k + 4 * four) =
-                  make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
-            else
-              *reinterpret_cast<float4*>(a.part_o + (part + row) * ZF_HEAD_DIM + 64 * k + 4 * four) = o;
-          }
-          ok = meet();
+      for (int turn = 0; turn < 2 && ok; ++turn) {            // (each once in the code)
+        if (turn == static_cast<int>(few)) {
+          if (more) q_rows(buf ^ 1);
+          continue;
         }
-        if (!ok) break;
+        if (few) {
+          finish_few(buf, st);
+        } else if (n >= 0) {
+          finish(buf, st, other);
+        }
       }
-      for (int t = few ? 2 : 0; t < (both ? 2 : 1); ++t) {
-        const Piece& p = pieces[buf];
-        const int slot = p.slot, first = 128 * t + row16, live = min(16, p.rows - first);      // rows of this warp
-        const size_t part = (static_cast<size_t>(blockIdx.x) * 2 + max(slot, 0)) * a.part_rows;
-        uint8_t* stage = my_q(0);                             // (the second tile's place may have the next piece's keys)
-        float f[2];
-        int to[2];                                            // this lane's rows' places in out and lse
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          to[r] = places[buf * kUnitRows + first + (lane >> 2) + 8 * r];
-          float sum = st.sum[r];
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-          sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-          const bool none = sum == 0.f;
-          f[r] = slot >= 0 ? 1.f : none ? 0.f : a.v_factor / sum;
-          if (quad == 0 && (lane >> 2) + 8 * r < live) {
-            if (slot < 0) a.lse[to[r]] = none ? -CUDART_INF_F : (log2f(sum) - st.c[r]) * kLn2f;
-            else a.part_ml[part + first + (lane >> 2) + 8 * r] = make_float2(none ? -CUDART_INF_F : -st.c[r], sum);
-          }
-        }
-        // 64 columns: rows lane / 4 (+ 8), columns 8 i + 2 quad (+ 1)
-        auto columns = [&](int k, uint32_t (&u)[32]) {
-          if (steps > 0) {
-            tmem_ld_16x256b_x8(lanes + kTmemO + 128 * t + 64 * k, u);
-            tmem_wait_ld();
-            touch(u);
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) u[e] = steps > 0 ? __float_as_uint(__uint_as_float(u[e]) * f[(e >> 1) & 1]) : 0u;
-        };
-        if (slot < 0) {
-#pragma unroll 1
-          for (int k = 0; k < 2; ++k) {
-            uint32_t u[32];
-            columns(k, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-                *reinterpret_cast<uint32_t*>(stage + ((lane >> 2) + 8 * r) * 256 + (((8 * k + i) ^ (lane >> 2)) * 16) + quad * 4) =
-                    pack_bf16x2(__uint_as_float(u[4 * i + 2 * r]), __uint_as_float(u[4 * i + 2 * r + 1]));
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 2 * i + (lane >> 4);
-            const int place = __shfl_sync(0xFFFFFFFFu, to[i >> 2], (row & 7) * 4);
-            if (row < live)
-              reinterpret_cast<uint4*>(a.out + static_cast<size_t>(place) * ZF_HEAD_DIM)[lane & 15] =
-                  *reinterpret_cast<const uint4*>(stage + row * 256 + (((lane & 15) ^ (row & 7)) * 16));
-          }
-        } else {
-#pragma unroll 1
-          for (int k = 0; k < 2; ++k) {
-            uint32_t u[32];
-            columns(k, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-              for (int r = 0; r < 2; ++r)
-                if ((lane >> 2) + 8 * r < live)
-                  *reinterpret_cast<uint2*>(a.part_o + (part + first + (lane >> 2) + 8 * r) * ZF_HEAD_DIM + 64 * k + 8 * i + 2 * quad) =
-                      make_uint2(u[4 * i + 2 * r], u[4 * i + 2 * r + 1]);
-          }
-        }
-        st = other;
-        __syncwarp();
-      }
+      if (!ok) break;
       tcgen05_before_sync();
       gs += steps;
       // ---- the next piece
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarPieceEmpty + buf]);
-      if (pieces[buf ^ 1].b >= 0 && pieces[buf ^ 1].steps > 0) q_store(buf ^ 1);
+      if (n >= 0 && lane == 0) mbar_arrive(&bars[kBarPieceEmpty + buf]);
+      if (!more) break;
     }
   }
 
   tcgen05_before_sync();
   __syncthreads();
+  if (tid == 0 && *abort_flag) report(a.status, ZF_DEV_TIMEOUT);
   if (warp == kMmaWarp) {
     tcgen05_after_sync();
     tmem_dealloc(tmem, kTmemCols);
@@ -1549,7 +1590,7 @@ static zf_status q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, int32_t 
   a.cap_log2 = softcap * kLog2e;
   a.two_over_cap = softcap > 0.f ? 2.f / softcap : 0.f;
   a.v_factor = c->v_scale * kQ4ScaleFactor;
-  a.wait_limit_ns = wait_limit_ns;
+  a.wait_limit_ns = static_cast<uint32_t>(wait_limit_ns);
   a.hold = hold;
 
   static std::mutex mu;
