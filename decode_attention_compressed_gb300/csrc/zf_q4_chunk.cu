@@ -6,7 +6,7 @@
 //
 // Split.  A unit is a request, a kv head and up to 256 of its query rows (token-major: row r is token r / G, query
 // head r % G of the kv head's G), which take the head's records in steps of 128 tokens.  The steps of all units,
-// each unit charged kUnitCost more for its start and end, are dealt in equal contiguous ranges to one CTA per SM,
+// each unit charged more for its start and end, are dealt in equal contiguous ranges to one CTA per SM,
 // so ragged batches and long contexts fill the GPU alike; a unit that a border cuts leaves its parts in the
 // workspace, which a second kernel joins.
 //
@@ -66,8 +66,12 @@ constexpr int kRing = 4;                         // operand buffers; the last is
                                                  // whose operands go round the first three
 constexpr int kOperand = kStep * ZF_HEAD_DIM * 2;
 constexpr int kCoreRow = 2048;                   // 8 rows x 128 elements of 16 bits
-constexpr int kUnitCost = 2;                     // a unit's start and end in steps
-constexpr int kMinCost = 6;                      // a CTA's least share of the steps
+// What steps, and a unit's start and end, cost with two tiles and with one: a step takes 1.87 us with two tiles and 1.03 with
+// one (plain scores, 512 units of 4096 to 16384 tokens); the units' cost was chosen by measurement (mixed batch, prompt: 385,
+// 496 us with steps counted alike and two of them per unit; 366, 497 with 14 and 10; 320, 479 with 24 and 18; 312, 475 with 35
+// and 20 or 25; 315, 479 with 45 and 30).
+constexpr int kStepCost = 7, kStepCost1 = 4, kUnitCost = 35, kUnitCost1 = 20;
+constexpr int kMinCost = 29;                     // a CTA's least share (one token over 4000: 20.6 us, with 36 21.8, with 42 22.5)
 constexpr int kSnap = 2;                         // no unit is cut this close to its ends
 constexpr float kShift = 7.f;                    // weights are 2^7 times their usual size
 constexpr float kBigScore = 1048576.f;           // scores (log2 units) from which differences are taken first
@@ -322,10 +326,15 @@ __device__ __forceinline__ void unit_steps(const ChunkArgs& a, const Request& r,
   first = a.window > 0 ? max(0, p0 + 1 - a.window) : 0;
   lo = min(first / kStep, hi);
 }
+// Whether unit i has one tile of rows.
+__device__ __forceinline__ bool one_tile(const ChunkArgs& a, const Request& r, int i) {
+  return r.tokens * a.group - i * kUnitRows <= 128;
+}
 __device__ __forceinline__ int unit_cost(const ChunkArgs& a, const Request& r, int i) {
   int lo, hi, first, last;
   unit_steps(a, r, i, lo, hi, first, last);
-  return hi - lo + kUnitCost;
+  const int one = one_tile(a, r, i);
+  return (hi - lo) * (one ? kStepCost1 : kStepCost) + (one ? kUnitCost1 : kUnitCost);
 }
 
 // A place in the order of all steps: unit (b, g, i) and steps of it before the place.
@@ -364,7 +373,8 @@ __device__ __forceinline__ Place find_place(const ChunkArgs& a, const int* sums,
       p.i = base + k;
       unit_steps(a, r, p.i, slo, shi, first, last);
       const int steps = shi - slo;
-      int s = min(max(rest - before - kUnitCost, 0), steps);
+      const bool one = one_tile(a, r, p.i);
+      int s = min(max(rest - before - (one ? kUnitCost1 : kUnitCost), 0) / (one ? kStepCost1 : kStepCost), steps);
       if (s < kSnap) s = 0;
       else if (steps - s < kSnap) s = steps;
       p.s = s;
@@ -587,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     }
     if (a.hold) {
       const uint64_t t0 = global_timer_ns();
-      while (!*abort_flag && global_timer_ns() - t0 < 4ull * a.wait_limit_ns) __nanosleep(1000);
+      while (!*abort_flag && global_timer_ns() - t0 < 2ull * a.wait_limit_ns + 20000000) __nanosleep(1000);
     }
     int n = 0;                     // pieces published
     uint32_t gs = 0;               // steps copied
@@ -1558,7 +1568,7 @@ static zf_status q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, int32_t 
   // the steps of all units, and what a unit is charged besides, are counted with 32 bits
   const long long units = static_cast<long long>(rows) * (num_q_heads / c->num_kv_heads) / kUnitRows + batch;
   if (units * c->num_kv_heads >= INT_MAX ||
-      units * c->num_kv_heads * (static_cast<long long>(max_pages) * c->page_size / kStep + 1 + kUnitCost) >= INT_MAX)
+      units * c->num_kv_heads * ((static_cast<long long>(max_pages) * c->page_size / kStep + 1) * kStepCost + kUnitCost) >= INT_MAX)
     return ZF_ERR_UNSUPPORTED;
   if (workspace_bytes < p.bytes()) return ZF_ERR_WORKSPACE_TOO_SMALL;
 
