@@ -336,7 +336,7 @@ __device__ __forceinline__ void unit_steps(const ChunkArgs& a, const Request& r,
   const int p0 = r.len - r.tokens + t0;
   last = max(r.len - r.tokens + t1 + 1, 0);
   hi = (last + kStep - 1) / kStep;
-  first = a.window > 0 ? max(0, p0 + 1 - a.window) : 0;
+  first = a.window > 0 && p0 >= a.window ? p0 + 1 - a.window : 0;       // (p0 may be far below 0)
   lo = min(first / kStep, hi);
 }
 // Whether unit i has one tile of rows.
@@ -954,7 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         // steps from the first that no row's window cuts to the one that ends at the first row's position or before
         low = __reduce_min_sync(0xFFFFFFFFu, low);
         high = __reduce_max_sync(0xFFFFFFFFu, high);
-        const int begin = a.window > 0 ? (max(high + 1 - a.window, 0) + kStep - 1) / kStep : 0;
+        const int begin = a.window > 0 && high >= a.window ? (high + 1 - a.window + kStep - 1) / kStep : 0;
         if (lane == 0) whole_of(buf, t) = make_int2(begin, max((low + 1) / kStep - begin, 0));
         if (!wanted) continue;
 #pragma unroll

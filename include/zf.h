@@ -513,7 +513,8 @@ size_t zf_q4_chunk_attn_workspace_size(int32_t batch, int32_t rows, int32_t num_
  *   A wait that takes 2 s gives up: it sets ZF_DEV_TIMEOUT, and out and lse of that call mean nothing.
  *   With a window, pages that lie before the windows of all new tokens of a request need not be there.
  *   batch <= ZF_MAX_BATCH, rows * num_q_heads < 2^31; ZF_ERR_UNSUPPORTED when all units (kv heads times the requests and
- *   the 256-row parts of the rows) times the steps of the longest context (128 tokens) would pass 2^31.  rows == 0 or
+ *   the 256-row parts of the rows) times the steps (128 tokens) of the longest context that the page table has room for
+ *   would pass 2^28.  rows == 0 or
  *   batch == 0 is a no-op.  Two kernels (attention, then the joining of units
  *   split over CTAs), launched with programmatic stream serialisation; results are deterministic (no atomics).
  */

@@ -157,6 +157,16 @@ def test_pages_behind_the_window_may_be_gone(zf, window, new):
     assert c.cache.status_word() == 0
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 200, 1000])
+def test_windows_beyond_the_context(zf, window):
+    """A window that reaches past the context cuts nothing, also where the first new tokens see nothing."""
+    c = Case(zf, 16, 2, 4, [5, 3, 140, 300], [9, 4, 150, 20], seed=15)
+    want = zf.q4_chunk_attn(*c.args())
+    got = zf.q4_chunk_attn(*c.args(), window=window)
+    c.check(*got)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 @pytest.mark.parametrize("slopes", [False, True])
 def test_units_of_all_sizes_on_one_sm(zf, slopes):
     """Many requests of few, some and many rows: each CTA goes from units of two tiles to units of one and back."""
