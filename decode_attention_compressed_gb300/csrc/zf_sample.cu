@@ -341,6 +341,7 @@ struct Ctx {
   Shared* sh;
   uint32_t rank, ranks;
   int flip;                                        // which part[] the next exchange uses
+  int index_bits;                                  // of the vocabulary
 };
 
 // The largest of all threads' values.
@@ -517,7 +518,9 @@ __device__ __forceinline__ unsigned long long settle(Ctx& c, const Row<T, kVec>&
                                                      uint32_t n, int turn, int which, unsigned long long target, unsigned long long& before,
                                                      int& listed, bool complete, In&& in, Val&& value) {
   Shared& sh = *c.sh;
-  unsigned long long lo = 0, hi = ~0ull;           // places
+  // an interval of places, the index moved up to the gap: dividing it by bits then comes to the index sooner
+  unsigned long long lo = 0, hi = ~0ull;
+  auto close = [&](int i, float x) { return static_cast<unsigned long long>(top - order_of(x)) << c.index_bits | static_cast<uint32_t>(i); };
   const float g0 = static_cast<float>(b), g1 = static_cast<float>(b + 1);
   auto in_bin = [&](float x) {
     const float g = bin_at(s, x);
@@ -530,7 +533,7 @@ __device__ __forceinline__ unsigned long long settle(Ctx& c, const Row<T, kVec>&
     unsigned long long mn = ~0ull, mx = 0;
     for_row(row, [&](int i, float x) {
       if (in_bin(x) && in(i, x)) {
-        const unsigned long long p = place(top, x, i);
+        const unsigned long long p = close(i, x);
         mn = min(mn, p);
         mx = max(mx, p);
       }
@@ -562,7 +565,7 @@ __device__ __forceinline__ unsigned long long settle(Ctx& c, const Row<T, kVec>&
       __syncthreads();
       for_row(row, [&](int i, float x) {
         if (!in_bin(x) || !in(i, x)) return;
-        const unsigned long long p = place(top, x, i);
+        const unsigned long long p = close(i, x);
         if (p < lo || p > hi) return;
         const int k = static_cast<int>((p - lo) >> shift);
         atomicAdd(&sh.bins[k], 1u);
@@ -582,13 +585,13 @@ __device__ __forceinline__ unsigned long long settle(Ctx& c, const Row<T, kVec>&
       lo += static_cast<unsigned long long>(k) << shift;
       hi = min(hi, lo + ((1ull << shift) - 1));
     }
-    if (lo >= hi) return lo;
+    if (lo >= hi) return (lo >> c.index_bits) << 32 | (lo & ((1ull << c.index_bits) - 1));
     cluster_sync();                                // (the list lies over the parts)
   }
   if (!complete) {
     for_row(row, [&](int i, float x) {
       if (!in_bin(x) || !in(i, x)) return;
-      const unsigned long long p = place(top, x, i);
+      const unsigned long long p = close(i, x);
       if (p >= lo && p <= hi) append(c, turn, which, i - row.first);
     });
     cluster_sync();
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   Shared& sh = *reinterpret_cast<Shared*>(raw);
   T* cache = reinterpret_cast<T*>(raw + ((sizeof(Shared) + 15) & ~static_cast<size_t>(15)));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Ctx c{&sh, cluster_rank(), cluster_size(), 0};
+  Ctx c{&sh, cluster_rank(), cluster_size(), 0, 32 - __clz(a.vocab)};
   const int r = blockIdx.x / c.ranks, V = a.vocab;
   for (int k = tid; k < 1024; k += kThreads) sh.table[k] = kExp2.v[k];
   if (tid < (kTurns + 1) * 3) sh.listed[tid / 3][tid % 3] = 0;
@@ -744,7 +747,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
   if (by_k && few_entries == 0) {
     // settle() overwrites the bins when it divides: what top-p needs of them is kept only if it does not
     int listed;
-    bound(settle(c, row, s, top, b_k, n_k, kTurns, 0, static_cast<unsigned long long>(k_top), before_k, listed, false,
+    unsigned long long before = before_k;
+    bound(settle(c, row, s, top, b_k, n_k, kTurns, 0, static_cast<unsigned long long>(k_top), before, listed, false,
                  [&](int, float) { return true; }, [](float) { return 1ull; }));
   }
   auto kept = [&](int i, float x) {                // (a NaN is not, its weight is 0)
