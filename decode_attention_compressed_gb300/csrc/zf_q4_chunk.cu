@@ -31,9 +31,9 @@
 //
 // Bound.  A product of M128 N128 K16 holds the tensor cores for 64 cycles whatever else runs, so a step's products are
 // 2048 cycles with two tiles and 1024 with one; steps take 1.87 and 1.03 us, some 3500 and 2000 cycles.  (One context of
-// 131072 tokens and 2048 new ones: 3.11 ms, 72 % of the products' time at the measured BF16 rate.)  The rest is the chain
+// 131072 tokens and 2048 new ones: 3.09 ms, where its products take 72 % at the measured BF16 rate.)  The rest is the chain
 // of a job through the softmax warps (450 cycles until the scores are there, 480 for the maxima, 750 for the weights, with
-// 430 of waiting) beside the decoding warps' and the issuing warp's instructions: 0.53 instructions per scheduler and
+// 430 of waiting) beside the decoding warps' and the issuing warp's instructions: 0.55 instructions per scheduler and
 // cycle.  Without any softmax arithmetic a step would take 8 % less, without decoding as long.  Starting and ending a
 // unit costs some 6 us, where instructions that run once wait for themselves, so code is kept short there (query rows
 // and output in one place each: mixed batch 447 -> 385 us).
@@ -62,15 +62,11 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kDecodeWarp0 = 8, kDecodeWarps = 8;
 constexpr int kMmaWarp = 16, kWalkWarp = 17;       // (18 and 19 fill up a warpgroup)
-// Registers per thread: the launch's, and what the softmax, decode and other warpgroups (4 warps) make of them; a cap
-// takes a few more in the softmax (564 us instead of 624 for the workload with a window and a cap), where the others do
-// with fewer (a long context 3343 us with 144 / 56 / 80, 3385 with 128 / 72 / 80).
-constexpr int kRegs = 96, kRegsDecode = 56;
-constexpr int regs_softmax(int mode) { return mode & 2 ? 152 : 144; }
-constexpr int regs_other(int mode) { return mode & 2 ? 64 : 80; }
-static_assert(2 * regs_softmax(0) + 2 * kRegsDecode + regs_other(0) <= 5 * kRegs &&
-                  2 * regs_softmax(2) + 2 * kRegsDecode + regs_other(2) <= 5 * kRegs,
-              "a larger sum would wait for registers forever");
+// Registers per thread: the launch's, and what the softmax, decode and other warpgroups (4 warps) make of them (long
+// context, prompt: 3094, 469 us with 136 / 64 / 80, 3116, 474 with 144 / 56 / 80, 3090, 469 with 160 / 48 / 64, but then
+// 514 instead of 503 with a window and a cap).
+constexpr int kRegs = 96, kRegsSoftmax = 136, kRegsDecode = 64, kRegsOther = 80;
+static_assert(2 * kRegsSoftmax + 2 * kRegsDecode + kRegsOther <= 5 * kRegs, "a larger sum would wait for registers forever");
 constexpr int kStep = 128;                       // tokens per step: of the operands
 constexpr int kUnitRows = 256;                   // query rows per unit
 constexpr int kFewRows = 16;                     // units of up to so many rows: each warp has them all, and a record of the step
@@ -600,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
   Piece* pieces = reinterpret_cast<Piece*>(smem + kSmPiece);
   // (a warpgroup's warps run one setmaxnreg together, so it stands before their ways part)
   if (warp >= kMmaWarp) {
-  give_registers<regs_other(kMode)>();
+  give_registers<kRegsOther>();
   if (warp == kWalkWarp) {
     // ================================================================== walk and copies
     const uint64_t policy = l2_evict_first_policy();
@@ -908,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
     }
   } else {
     // ================================================================== softmax
-    take_registers<regs_softmax(kMode)>();
+    take_registers<kRegsSoftmax>();
     // All eight warps work on the same job, 16 rows of its tile each (warps w and w + 4 share the lanes that they can
     // reach): a lane has rows lane / 4 and lane / 4 + 8 of them, and columns 8 i + 2 (lane % 4), + 1.
     const int row16 = 32 * (warp & 3) + 16 * (warp >> 2);     // the warp's first row in a tile
