@@ -398,6 +398,29 @@ def test_behind_a_late_writer(zf):
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+def test_more_steps_than_are_counted_are_refused(zf):
+    """A page table with room for 2^30 tokens: one request of few heads is right, two of many are refused."""
+    page, room = 16, 1 << 26
+    for batch, hkv, ok in ((1, 1, True), (2, 32, False)):
+        cache = zf.Q4Cache(4, hkv, page)
+        table = torch.zeros((batch, room), dtype=torch.int32, device="cuda")
+        table[:, 1] = 1
+        k = torch.ones(40, hkv, 128, dtype=torch.bfloat16, device="cuda")
+        at = torch.arange(20, dtype=torch.int32, device="cuda").repeat(2)
+        zf.q4_write_tokens(cache, k, k, at // page, at % page)
+        lens = torch.full((batch,), 20, dtype=torch.int32, device="cuda")
+        start = torch.arange(batch + 1, dtype=torch.int32, device="cuda") * 3
+        q = torch.ones(3 * batch, hkv, 128, dtype=torch.bfloat16, device="cuda")
+        if ok:
+            out, _ = zf.q4_chunk_attn(cache, q, table, lens, start)
+            # (a block of ones is stored as codes of 6 and the e4m3 scale next to 1 / 6, 11 / 64: 1.03125, a BF16 value)
+            assert (out == 1.03125).all()
+        else:
+            with pytest.raises(zf.ZfError, match="unsupported"):
+                zf.q4_chunk_attn(cache, q, table, lens, start)
+        assert cache.status_word() == 0
+
+
 def test_a_wait_that_runs_out_reports_timeout_and_the_next_call_is_right(zf):
     """The first wait of every CTA's warps is made to run out: the call reports it and ends, and the next one, right
     behind it on the same stream, gives what it gave before."""
