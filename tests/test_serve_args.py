@@ -52,6 +52,20 @@ def test_chunk_attention_refuses(zf):
         assert size(*args) == 0, args
 
 
+def test_chunk_wait_test_refuses(zf):
+    d = _desc(zf)
+    names = ["cache", "q", "rows", "batch", "hq", "start", "table", "max_pages", "lens", "scale", "window", "cap", "slopes",
+             "out", "lse", "ws", "ws_bytes", "limit", "stream"]
+    call = _caller(zf.lib().zf_q4_chunk_attn_wait_test, names, [ctypes.byref(d), 0x10000, 5, 2, 8, 0x20000, 0x30000, 4, 0x40000,
+                                                               0.1, 0, 0.0, None, 0x50000, 0x60000, 0x70000, 1 << 30, 1000000, None])
+    for kw, code in BAD_CACHES:
+        assert call(cache=ctypes.byref(_desc(zf, **kw))) == code, kw
+    for kw in (dict(limit=0), dict(limit=999), dict(limit=2_000_000_001), dict(limit=2 ** 64 - 1), dict(batch=-1), dict(hq=7),
+               dict(q=None), dict(ws=None), dict(scale=float("nan")), dict(window=-1), dict(batch=0, limit=999)):
+        assert call(**kw) == -1, kw
+    assert call(batch=0) == 0 and call(rows=0) == 0
+
+
 def test_sampling_refuses(zf):
     names = ["rows", "vocab", "logits", "type", "stride", "uniform", "temp", "k", "p", "min_p", "tokens", "probs", "status",
              "stream"]
