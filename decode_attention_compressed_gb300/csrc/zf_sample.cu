@@ -501,7 +501,9 @@ __device__ __forceinline__ unsigned long long rank_list(Ctx& c, int n, unsigned 
   }
   __syncthreads();
   before = sh.found[1];
-  return sh.found[0];
+  const unsigned long long at = sh.found[0];
+  __syncthreads();                                 // (the words are used again, by the guess of top-p's bin too)
+  return at;
 }
 // One more entry that is to be listed.
 __device__ __forceinline__ void append(Ctx& c, int turn, int which, int at) {

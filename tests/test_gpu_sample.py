@@ -206,3 +206,25 @@ def test_few_and_many_candidates(zf, dtype):
         check(zf, y, u, min_p=[1.0, 0.9, 0.5, 0.2, 0.1, 0.05, 0.01, 1e-30], top_p=[0.9, 0.0, 0.5, 0.7, 0.9, 0.95, 0.99, 0.3])
         check(zf, y, u, top_k=[3, 9, 40, 100, 300, 505, 30, 20], min_p=[1.0, 0.9, 0.5, 0.2, 0.1, 0.05, 0.01, 1e-30],
               top_p=[0.9, 0.0, 0.5, 0.7, 0.9, 0.95, 0.99, 0.3], temperature=[0.1, 0.5, 1.0, 2.0, 5.0, 1.5, 0.01, 1.0])
+
+
+@pytest.mark.parametrize("rows", [1, 12, 64])
+def test_top_k_border_is_the_same_for_all_warps(zf, rows):
+    """Top-k past the listed candidates, its border among many equal logits, and top-p behind it: every warp has to work
+    with the same border, so tokens and distributions are the same bits in every call."""
+    V = 128000
+    g = torch.Generator().manual_seed(21)
+    x = (3 * torch.randn(rows, V, generator=g)).to(torch.bfloat16)   # (some 140 equal ones at the thousandth place)
+    u = torch.rand(rows, generator=g).numpy()
+    k = np.array([600, 700, 999, 1000, 1001, 1500, 2000, 2500, 3001, 4000, 4500, 5000])[np.arange(rows) % 12]
+    p = np.array([0.9, 0.99, 0.5, 0.7, 0.999])[np.arange(rows) % 5].astype(np.float32)
+    if rows <= 12:
+        check(zf, x, u, top_k=k, top_p=p)
+    kw = dict(top_k=torch.as_tensor(k, dtype=torch.int32).cuda(), top_p=torch.from_numpy(p).cuda())
+    x, u = x.cuda(), torch.from_numpy(u).cuda()
+    first = torch.empty(rows, V, device="cuda")
+    want = zf.sample_tokens(x, u, probs=first, **kw)
+    again = torch.empty_like(first)
+    for _ in range(30):
+        tokens = zf.sample_tokens(x, u, probs=again, **kw)
+        assert torch.equal(tokens, want) and torch.equal(again, first)
