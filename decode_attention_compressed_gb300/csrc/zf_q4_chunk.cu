@@ -85,6 +85,7 @@ constexpr int kSnap = 2;                         // no unit is cut this close to
 constexpr float kShift = 7.f;                    // weights are 2^7 times their usual size
 constexpr float kBigScore = 1048576.f;           // scores (log2 units) from which differences are taken first
 constexpr float kRaise = 8.f;
+constexpr float kMostCap = 128.f;                // caps up to this: by an exponential (see cap_wide)
 constexpr float kLog2e = 1.4426950408889634f, kLn2f = 0.6931471805599453f;
 
 // Tensor memory: two buffers of scores (weights go over them), outputs of the two tiles.
@@ -106,6 +107,7 @@ struct ChunkArgs {
   int32_t batch, rows, hq, hkv, group, page_size, num_pages, max_pages, part_rows, window;
   float scale_log2;              // softmax scale * log2(e) * the decoding's factors
   float cap_log2, two_over_cap;  // cap * log2(e), 2 / cap (kCap: scores in log2 units to twice the tanh's argument in them)
+  float over_cap;                // 1 / (cap * log2(e)) (kWide: scores in log2 units to the tanh's argument)
   float v_factor;
   uint32_t wait_limit_ns;        // at most 2 s
   int32_t hold;                  // tests: no piece is published before a wait for one has given up
@@ -272,6 +274,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   asm("{\n\t.reg .b64 x, y, w;\n\t"
       "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
       "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
@@ -473,6 +485,28 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// cap tanh(z) for a pair of z, of any cap: z P(z^2) / Q(z^2) up to |z| = 8.4, where tanh is 1 - 2^-23.  The quotient, a
+// minimax fit of tanh(z) / z made for this (least squares, reweighted by the errors), is off by 2^-26.5; its steps round some
+// twelve times to 2^-24, so a score is off by at most 2^-20 of itself.  The kernel's other form, cap - 2 cap / (1 + e^(2 z)),
+// is off by some 2^-22 of the cap whatever the score: 2^-15 at a cap of 128, which the weights' fp16 hides (2^-11), but 0.09
+// at 10^6.  It takes fewer instructions (window and cap: 499 us, with the quotient 599), so it has the caps up to kMostCap.
+__device__ __forceinline__ float2 cap_wide(float2 z, float cap) {
+  constexpr float kP[] = {0.99999998949508034f, 0.13419579348100072f, 3.541616941987837e-3f, 2.1379765429157377e-5f,
+                          1.4457840450921928e-8f};
+  constexpr float kQ[] = {1.f, 0.4675290317888972f, 2.6051437834478844e-2f, 3.3614264344577566e-4f, 8.2199561599768221e-7f};
+  constexpr float kEnd = 8.4f;
+  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(z.x) : "f"(kEnd));      // (a NaN stays one)
+  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(z.y) : "f"(kEnd));
+  const float2 u = mul2(z, z);
+  float2 p = make_float2(kP[4], kP[4]), q = make_float2(kQ[4], kQ[4]);
+#pragma unroll
+  for (int i = 3; i >= 0; --i) {
+    p = fma2(p, u, make_float2(kP[i], kP[i]));
+    q = fma2(q, u, make_float2(kQ[i], kQ[i]));
+  }
+  return mul2(mul2(mul2(z, make_float2(cap, cap)), p), make_float2(fast_rcp(q.x), fast_rcp(q.y)));
+}
+
 // The columns 8 i + d (i < 16, d < 2) that are at most h, or all; bit 2 i + d.
 __device__ __forceinline__ uint32_t bits_to(int h) {
   if (h < 0) return 0u;
@@ -490,8 +524,8 @@ __device__ __forceinline__ uint32_t seen_bits(int hi, int window, uint64_t absen
   return m;
 }
 
-// What becomes of the scores: nothing, or a cap, slopes, or both.
-enum : int { kPlain = 0, kSlope = 1, kCap = 2 };
+// What becomes of the scores: nothing, or a cap (kWide: one above kMostCap), slopes, or both.
+enum : int { kPlain = 0, kSlope = 1, kCap = 2, kWide = 4 };
 
 // The s-th step that a piece of so many takes.  With slopes the last one first: positive slopes raise the scores with the
 // position, so going up a row's maximum would be raised, and its output rescaled, in almost every step (64 single
@@ -1184,7 +1218,12 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
               const int col = 8 * (e >> 1) + (e & 1);
               uint32_t& at_e = v[4 * (e >> 1) + 2 * r + (e & 1)];
               float x = __uint_as_float(at_e);
-              if (kMode & kCap) x = fmaf(fast_rcp(1.f + fast_exp2(x * (factor[r] * a.two_over_cap))), -2.f * a.cap_log2, a.cap_log2);
+              if (kMode & kWide) {
+                x *= factor[r] * a.over_cap;
+                x = cap_wide(make_float2(x, x), a.cap_log2).x;
+              } else if (kMode & kCap) {
+                x = fmaf(fast_rcp(1.f + fast_exp2(x * (factor[r] * a.two_over_cap))), -2.f * a.cap_log2, a.cap_log2);
+              }
               if (kMode & kSlope) x = fmaf(x, kMode & kCap ? 1.f : factor[r], fmaf(slope[r], static_cast<float>(col), base));
               if (absent || col > hi || (a.window > 0 && col <= hi - a.window)) x = -CUDART_INF_F;
               at_e = __float_as_uint(x);
@@ -1279,8 +1318,19 @@ __global__ void __launch_bounds__(kThreads, 1) q4_chunk_kernel(const ChunkArgs a
         tmem_wait_ld();
         touch(v[0]);
         touch(v[1]);
-        if (kMode & kCap) {
-          // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), off by some 2^-23 of the cap
+        if (kMode & kWide) {
+          const float f[2] = {factor[0] * a.over_cap, factor[1] * a.over_cap};
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float g = f[(e >> 1) & 1];
+              const float2 x = cap_wide(mul2(make_float2(__uint_as_float(v[k][e]), __uint_as_float(v[k][e + 1])), make_float2(g, g)), a.cap_log2);
+              v[k][e] = __float_as_uint(x.x);
+              v[k][e + 1] = __float_as_uint(x.y);
+            }
+        } else if (kMode & kCap) {
+          // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
           const float f[2] = {factor[0] * a.two_over_cap, factor[1] * a.two_over_cap}, two = -2.f * a.cap_log2;
 #pragma unroll
           for (int k = 0; k < 2; ++k)
@@ -1608,6 +1658,7 @@ static zf_status q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, int32_t 
   a.scale_log2 = scale_log2;
   a.cap_log2 = softcap * kLog2e;
   a.two_over_cap = softcap > 0.f ? 2.f / softcap : 0.f;
+  a.over_cap = softcap > 0.f ? 1.f / a.cap_log2 : 0.f;
   a.v_factor = c->v_scale * kQ4ScaleFactor;
   a.wait_limit_ns = static_cast<uint32_t>(wait_limit_ns);
   a.hold = hold;
@@ -1620,7 +1671,8 @@ static zf_status q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, int32_t 
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!ready[dev]) {
-      for (const auto kernel : {q4_chunk_kernel<kPlain>, q4_chunk_kernel<kSlope>, q4_chunk_kernel<kCap>, q4_chunk_kernel<kCap | kSlope>}) {
+      for (const auto kernel : {q4_chunk_kernel<kPlain>, q4_chunk_kernel<kSlope>, q4_chunk_kernel<kCap>, q4_chunk_kernel<kCap | kSlope>,
+                                q4_chunk_kernel<kCap | kWide>, q4_chunk_kernel<kCap | kWide | kSlope>}) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmTotal) != cudaSuccess)
           return ZF_ERR_CUDA;
         // the warpgroups' shares are those of a launch with kRegs registers per thread
@@ -1632,7 +1684,8 @@ static zf_status q4_chunk_attn(const zf_q4_cache* c, const uint16_t* q, int32_t 
     }
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const auto kernel = softcap > 0.f ? (slopes ? q4_chunk_kernel<kCap | kSlope> : q4_chunk_kernel<kCap>)
+  const auto kernel = softcap > kMostCap ? (slopes ? q4_chunk_kernel<kCap | kWide | kSlope> : q4_chunk_kernel<kCap | kWide>)
+                      : softcap > 0.f ? (slopes ? q4_chunk_kernel<kCap | kSlope> : q4_chunk_kernel<kCap>)
                                     : (slopes ? q4_chunk_kernel<kSlope> : q4_chunk_kernel<kPlain>);
   st = launch(kernel, dim3(p.grid), kThreads, kSmTotal, s, a);
   if (st != ZF_OK) return st;

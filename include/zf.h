@@ -505,7 +505,8 @@ size_t zf_q4_chunk_attn_workspace_size(int32_t batch, int32_t rows, int32_t num_
  *   out [rows][num_q_heads][128] BF16, lse [rows][num_q_heads] float32: the logarithm of the sum of exp(scores).  A
  *   row that sees nothing (a request with fewer tokens than new ones) gets out = 0 and lse = -inf.
  *   K and V are multiplied as the exact stored values; a query row's values enter as for zf_q4_decode_attn; scores
- *   and sums are float32; the softmax weights enter the product as fp16 (off by at most 2^-11 of the weight, or
+ *   and sums are float32 (with a softcap up to 128 a score is off by some 2^-22 of the cap besides, with a larger one by at most
+ *   2^-20 of itself); the softmax weights enter the product as fp16 (off by at most 2^-11 of the weight, or
  *   2^-32 of the row's largest one); the result is rounded once more, to BF16.  A NaN or an infinity in a query row
  *   stays in that row.
  *   A token_start entry that decreases or passes rows leaves that request out, a seq_len out of range is clamped;

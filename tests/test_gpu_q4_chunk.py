@@ -438,3 +438,50 @@ def test_a_wait_that_runs_out_reports_timeout_and_the_next_call_is_right(zf):
         with pytest.raises(zf.ZfError, match="invalid argument"):
             zf.q4_chunk_attn_wait_test(*args, wait_limit_ns=limit)
     assert c.cache.status_word() == 0
+
+
+@pytest.mark.parametrize("tokens,sizes", [(3, (-12, 13)), (70, (-12, 13)), (70, (-2, -1)), (70, (0, 1)), (70, (3, 4))])
+@pytest.mark.parametrize("softcap", [1e-3, 0.1, 3.0, 50.0, 128.0, 128.01, 1e3, 1e4, 1e5, 1e6])
+def test_caps_over_their_whole_range(zf, softcap, tokens, sizes):
+    """The error of a capped score does not grow with the cap: rows of sizes from 2^-12 to 2^12, and rows alike, whose scores
+    are all on one side of a cap or on both."""
+    c = Case(zf, 16, 2, 4, [tokens + 200, tokens, tokens + 40], [tokens] * 3, seed=31)
+    f = torch.exp2(torch.randint(*sizes, (c.rows, c.hq, 1), generator=torch.Generator().manual_seed(2)).float())
+    c.q = (c.q.float() * f).to(torch.bfloat16)
+    for window in (1, 0):
+        out, lse = zf.q4_chunk_attn(*c.args(), softcap=softcap, window=window)
+        out, lse = f64(out), lse.double().cpu().numpy()
+        for b, L in enumerate(c.lens):
+            a, e = c.start[b], c.start[b + 1]
+            want, wl, wv, sv, mag = R.chunk_attention(f64(c.q[a:e]), c.k[b], c.v[b], L - tokens, 1 / math.sqrt(128), window, softcap)
+            # a score before the cap: off by 2^-16 of its products' magnitudes (see check), which the cap does not raise;
+            # after it 2^-20 of itself, or with a cap up to 128 2^-21 of that (cap - 2 cap / (1 + e), with e off by 2^-22,
+            # 1 + e by 2^-24, the reciprocal by 2^-23, the result by 2^-24 of the cap); and a few roundings more in log2
+            # units and back
+            cap = 2.0 ** -21 * softcap if softcap <= 128 else 0.0
+            off = mag * 2.0 ** -16 + 2.0 ** -20 * np.minimum(mag, softcap) + 2.0 ** -20 + cap
+            tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2 * off + 2.0 ** -18)[..., None] * wv + 2.0 ** -32 * sv + 1e-30
+            assert (np.abs(out[a:e] - want) <= tol).all(), (b, window, (np.abs(out[a:e] - want) / tol).max())
+            tol = off + 2.0 ** -20 * (1 + np.abs(wl))                    # (window 1: lse is the score of the row's own token)
+            assert (np.abs(lse[a:e] - wl) <= tol).all(), (b, window, (np.abs(lse[a:e] - wl) / tol).max())
+    assert c.cache.status_word() == 0
+
+
+@pytest.mark.parametrize("page,hkv,group,lens,new", SHAPES)
+def test_wide_caps_against_the_oracle(zf, page, hkv, group, lens, new):
+    """Caps above 128 have kernels of their own, with slopes and without."""
+    c = Case(zf, page, hkv, group, lens, new, seed=len(lens) + hkv)
+    slope = np.float32(2.0) ** -np.linspace(1, 8, c.hq, dtype=np.float32)
+    for mod in (dict(softcap=200.0), dict(softcap=1000.0, window=64, slopes=slope)):
+        kw = {**mod, "slopes": torch.from_numpy(slope).cuda()} if "slopes" in mod else mod
+        out, lse = zf.q4_chunk_attn(*c.args(), **kw)
+        c.check(out, lse, **mod)
+    q = c.q.clone()
+    q[-1, 0, 5] = float("nan")
+    got = zf.q4_chunk_attn(c.cache, q.cuda(), *c.args()[2:], softcap=200.0)
+    want = zf.q4_chunk_attn(*c.args(), softcap=200.0)
+    hit = torch.zeros(c.rows, c.hq, dtype=torch.bool)
+    hit[-1, 0] = True
+    assert torch.isnan(got[0].cpu()[hit]).all() and torch.isnan(got[1].cpu()[hit]).all()
+    assert torch.equal(got[0].cpu()[~hit], want[0].cpu()[~hit]) and torch.equal(got[1].cpu()[~hit], want[1].cpu()[~hit])
+    assert c.cache.status_word() == 0
