@@ -619,6 +619,8 @@ extern "C" zf_status zf_compact_pages(int32_t batch, int32_t max_pages, int32_t 
                                       int32_t* free_pos, int32_t* copy_src, int32_t* copy_dst, int32_t* status,
                                       void* workspace, size_t workspace_bytes, void* stream) {
   if (!table_ok(batch, max_pages) || !pool_ok(num_pages)) return ZF_ERR_INVALID_ARGUMENT;
+  // a row's entries are counted with 32 bits, and in pieces of kPiece
+  if (max_pages > (1 << 30)) return ZF_ERR_UNSUPPORTED;
   if (!words_ok({free_pos}, {status})) return ZF_ERR_INVALID_ARGUMENT;
   if (batch > 0 && !words_ok({page_table, pages_held, new_page_table})) return ZF_ERR_INVALID_ARGUMENT;
   if (num_pages > 0 && (!words_ok({free_pages}) || !workspace || !aligned16(workspace))) return ZF_ERR_INVALID_ARGUMENT;

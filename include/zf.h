@@ -634,7 +634,7 @@ zf_status zf_release_requests(int32_t batch, int32_t max_pages_per_req, int32_t 
  *   i is i from n on, -1 before; free_pos [1]: n; copy_src, copy_dst [num_pages / 2]: the moves, then -1.
  *   A page id out of range sets ZF_DEV_BAD_PAGE_ID and stays as it is; a pages_held out of range is clamped and sets
  *   ZF_DEV_BAD_SEQ_LEN.  status: optional device word.  workspace: any contents, 16-byte aligned.  batch <=
- *   ZF_MAX_BATCH.  One kernel, launched with programmatic stream serialisation.
+ *   ZF_MAX_BATCH, max_pages_per_req <= 2^30.  One kernel, launched with programmatic stream serialisation.
  */
 size_t zf_compact_pages_workspace_size(int32_t num_pages);
 zf_status zf_compact_pages(int32_t batch, int32_t max_pages_per_req, int32_t num_pages, const int32_t* page_table,

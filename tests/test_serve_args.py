@@ -121,6 +121,13 @@ def test_release_and_compact_refuse(zf):
     assert zf.lib().zf_release_requests_workspace_size(-1) == 0 and zf.lib().zf_compact_pages_workspace_size(-1) == 0
 
 
+def test_compaction_refuses_rows_that_32_bits_do_not_count(zf):
+    """With the last few entries below 2^31 a row's pieces would be counted as negative, and its pages taken as unused."""
+    f = zf.lib().zf_compact_pages
+    for max_pages in ((1 << 30) + 1, 2 ** 31 - 256, 2 ** 31 - 255, 2 ** 31 - 1):
+        assert f(1, max_pages, 100, 0x1000, 0x1100, 0x1200, 0x1300, 0x1400, 0x1500, 0x1600, None, 0x2000, 1 << 20, None) == -2
+
+
 def test_copy_refuses(zf):
     f = zf.lib().zf_q4_copy_pages
     for kw, code in BAD_CACHES:
