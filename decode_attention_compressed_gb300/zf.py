@@ -903,8 +903,8 @@ _LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 def sample_tokens(logits, uniform=None, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, tokens=None,
                   status=None):
     """zf_sample_tokens: logits [R][V] float32, bfloat16 or float16 (rows may be a stride apart); uniform [R] float32 in
-    [0, 1); temperature, top_p, min_p [R] float32 and top_k [R] int32, each None for none.  Returns tokens [R] int32
-    (None when uniform is None).  probs [R][V] float32 is filled with the distribution sampled from; uniform may be
+    [0, 1); temperature, top_p, min_p [R] float32 and top_k [R] int32, each None for none (min_p: 0 or less too).
+    Returns tokens [R] int32 (None when uniform is None).  probs [R][V] float32 is filled with the distribution sampled from; uniform may be
     None when only that is wanted.  tokens: a tensor to write into; status: an int32 device word."""
     if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
         raise ValueError("logits must be a [rows][vocab] tensor")

@@ -649,16 +649,16 @@ zf_status zf_compact_pages(int32_t batch, int32_t max_pages_per_req, int32_t num
  *                 counts as -inf.
  *   temperature, top_k, top_p, min_p [rows], each NULL for none.  w_i = exp((x_i - max) / temperature); a temperature
  *                 below 1e-6 takes the largest logit, the first of equal ones.  In the order of (x descending, index
- *                 ascending) these are kept: the first top_k (0: all), of them those with w_i >= min_p (in [0, 1]),
- *                 of them the shortest run from the front whose sum reaches top_p (1 or more: all) times theirs; at
- *                 least the first.
+ *                 ascending) these are kept: the first top_k (0: all), of them those with w_i >= min_p (0 or less:
+ *                 all; at most 1), of them the shortest run from the front whose sum reaches top_p (1 or more: all)
+ *                 times theirs; at least the first.
  *   uniform [rows] in [0, 1), tokens [rows] (both or neither): the first index, in index order, at which the running
  *                 sum of kept weights is above uniform times their sum.
  *   probs [rows][vocab] float32 or NULL: kept weights over their sum, 0 elsewhere.  (tokens or probs or both.)
  *   Weights are taken as integers times 2^-42, off by at most 2^-30 of themselves or 2^-43, and summed exactly, so
  *   neither a choice nor a probability depends on how the work is split.
- *   A row without a finite largest logit, or with a parameter that is NaN, negative or (temperature) infinite, a
- *   min_p above 1 or a uniform outside [0, 1) gives token -1 and probabilities 0 and sets ZF_DEV_BAD_PROBS.
+ *   A row without a finite largest logit, or with a parameter that is NaN, negative (but for min_p) or (temperature)
+ *   infinite, a min_p above 1 or a uniform outside [0, 1) gives token -1 and probabilities 0 and sets ZF_DEV_BAD_PROBS.
  *   status: optional device word.  rows <= ZF_MAX_SAMPLE_ROWS, vocab <= ZF_MAX_SAMPLE_VOCAB.  One kernel, launched
  *   with programmatic stream serialisation.
  */

@@ -228,3 +228,12 @@ def test_top_k_border_is_the_same_for_all_warps(zf, rows):
     for _ in range(30):
         tokens = zf.sample_tokens(x, u, probs=again, **kw)
         assert torch.equal(tokens, want) and torch.equal(again, first)
+
+
+def test_a_negative_min_p_is_none(zf):
+    """No weight is below it, so it keeps all, like 0; NaN and what is above 1 are refused."""
+    x, u = logits_of(6, 3000, 14), np.linspace(0, 0.99, 6)
+    m = np.array([-1.0, -1e-30, -0.0, -np.inf, -3e38, -0.5], np.float32)
+    tokens = check(zf, x, u, min_p=m, top_p=[0.9] * 6)
+    assert tokens.tolist() == check(zf, x, u, top_p=[0.9] * 6).tolist()
+    assert check(zf, x[:2], u[:2], min_p=[np.nan, 1.5]).tolist() == [-1, -1]
