@@ -646,7 +646,7 @@ zf_status zf_compact_pages(int32_t batch, int32_t max_pages_per_req, int32_t num
  * zf_sample_tokens — a token per row of logits, and the distribution it is drawn from (what zf_verify_drafts takes as
  * target_probs and draft_probs).
  *   logits [rows][vocab], row r at entry r * row_stride (>= vocab); logits_type ZF_F32, ZF_BF16 or ZF_F16.  A NaN
- *                 counts as -inf.
+ *                 counts as -inf, and so does a logit that lies more than FLT_MAX below the row's largest one.
  *   temperature, top_k, top_p, min_p [rows], each NULL for none.  w_i = exp((x_i - max) / temperature); a temperature
  *                 below 1e-6 takes the largest logit, the first of equal ones.  In the order of (x descending, index
  *                 ascending) these are kept: the first top_k (0: all), of them those with w_i >= min_p (0 or less:

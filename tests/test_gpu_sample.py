@@ -237,3 +237,30 @@ def test_a_negative_min_p_is_none(zf):
     tokens = check(zf, x, u, min_p=m, top_p=[0.9] * 6)
     assert tokens.tolist() == check(zf, x, u, top_p=[0.9] * 6).tolist()
     assert check(zf, x[:2], u[:2], min_p=[np.nan, 1.5]).tolist() == [-1, -1]
+
+
+def test_the_flattest_temperatures_and_the_farthest_logits(zf):
+    """Temperatures up to the largest float, where the histogram's one bin has every logit; differences beyond it."""
+    x, u = logits_of(4, 5000, 15), [0.1, 0.4, 0.7, 0.99]
+    t = np.array([1e36, 1.5e37, 1e38, 3.4e38], np.float32)
+    check(zf, x, u, temperature=t, top_p=[0.3, 0.5, 0.9, 1.0])
+    k, p, m = np.array([1, 600, 3000, 0]), np.array([0.9, 0.9, 0.5, 0.999]), np.array([0.5, 1.0, 0.0, 1e-30])
+    some = [0, 2, 3]
+    check(zf, x[some], np.array(u)[some], temperature=t[some], top_k=k[some], top_p=p[some], min_p=m[some])
+    # min_p 1: exp(-d / t) is 1 - d / t, d / t some 10^-36, for all but the largest: only that one is kept (the oracle's
+    # float64 rounds them all to 1)
+    largest = int(x[1].argmax())
+    assert int((x[1] == x[1].max()).sum()) == 1
+    f = lambda v, d=torch.float32: torch.tensor([v], dtype=d, device="cuda")  # noqa: E731
+    probs = torch.empty(1, 5000, device="cuda")
+    token = zf.sample_tokens(x[1:2].cuda(), f(0.4), temperature=f(1.5e37), top_k=f(600, torch.int32), top_p=f(0.9),
+                             min_p=f(1.0), probs=probs)
+    assert token.item() == largest and probs[0, largest] == 1 and probs.sum() == 1
+    far = torch.tensor([[3e38, -3e38, 2e38, 1e38, -3.4e38]])
+    same = torch.tensor([[3e38, -float("inf"), 2e38, 1e38, -float("inf")]])
+    a, b = (torch.empty(1, 5, device="cuda") for _ in range(2))
+    one = torch.full((1,), 1e38, device="cuda")
+    zf.sample_tokens(far.cuda(), probs=a, temperature=one)
+    zf.sample_tokens(same.cuda(), probs=b, temperature=one)
+    assert torch.equal(a, b)
+    check(zf, same, [0.5], temperature=[1e38])
