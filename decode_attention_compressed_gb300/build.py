@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -19,6 +20,10 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libzf.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v", "--expt-relaxed-constexpr"]
+
+# Kernels whose warps share out the registers of their launch (kRegs in the source): with another count per thread a share
+# could not be had, so the library would refuse every call.
+REGISTERS = {"q4_chunk_kernel": 96}
 
 
 def nvcc() -> str:
@@ -32,6 +37,19 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
+def check_registers(said: str, want=None) -> None:
+    """Raises unless every instance of the kernels in `want` has its registers, by what ptxas -v said."""
+    name = None
+    for line in said.splitlines():
+        if m := re.search(r"Compiling entry function '(\w+)'", line):
+            name = m.group(1)
+        elif name and (m := re.search(r"Used (\d+) registers", line)):
+            for kernel, count in (REGISTERS if want is None else want).items():
+                if f"{len(kernel)}{kernel}" in name and int(m.group(1)) != count:      # (a mangled name has lengths)
+                    raise RuntimeError(f"{name}: {m.group(1)} registers per thread, expected {count}")
+            name = None
+
+
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     cmd = [nvcc(), *ARCH, *FLAGS, "-I", os.path.join(ROOT, "include"), "-c", src, "-o", obj]
@@ -40,6 +58,7 @@ def _compile(src: str, verbose: bool) -> str:
         raise RuntimeError(f"nvcc failed for {src}:\n{res.stdout}\n{res.stderr}")
     if verbose:
         sys.stderr.write(res.stderr)
+    check_registers(res.stdout + res.stderr)
     return obj
 
 
