@@ -6,8 +6,8 @@
 //
 // The first three are bound by latency: a few dependent passes over lists of a few hundred KB that lie in L2.
 // Each is one cluster of CTAs (1 or 16), whose barrier separates the passes and, as in zf_map_tokens, lets
-// outputs be the same arrays as inputs.  64 requests of 1024 tokens, 4096 entries: fork 5.9 us, release 9.4, compact 10.5,
-// of which a launch and the first dependent loads are some 4.  The copy is bound by its bytes, read and written once:
+// outputs be the same arrays as inputs.  64 requests of 1024 tokens, 4096 entries: fork 5.9 us, release 9.4, compact 10.5
+// (three quarters of the entries held), of which a launch and the first dependent loads are some 4.  The copy is bound by its bytes, read and written once:
 // 81 MB of pages in 28.0 us, 5.8 TB/s (6.7 is a plain copy's rate).
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -523,8 +523,10 @@ bool words_ok(std::initializer_list<const void*> needed, std::initializer_list<c
 }
 bool table_ok(int batch, int max_pages) { return batch >= 0 && batch <= ZF_MAX_BATCH && max_pages >= 1; }
 bool pool_ok(int num_pages) { return num_pages >= 0 && num_pages <= INT_MAX - (1 << 20); }
-// CTAs for passes over `entries` table entries: release and compact take 46 and 27 us with one CTA and 18.7 and 15.0 with 16
-// at 65536 entries, the same at 4096 (clusters of 4 and 8 lie between).
+// CTAs for passes over a table of so many entries.  Release + compaction, us, with all entries held, one CTA and 16: 2048
+// entries 9.6 + 8.1 and 10.1 + 11.1; 4096 14.7 + 10.1 and 10.4 + 11.5; 8192 24.8 + 13.6 and 12.9 + 11.7; 16384 46 + 23 and
+// 14 + 13; 65536 190 + 83 and 20 + 16; 262144 784 + 298 and 59 + 34 (8 CTAs: 13 + 11 at 8192, 108 + 56 at 262144).  A table
+// in use has room that is not held, so the border lies at twice the entries where the two are alike.
 int ctas_for(long long entries) { return entries <= 8192 ? 1 : kCluster; }
 
 }  // namespace

@@ -37,6 +37,9 @@
 // cycle.  Without any softmax arithmetic a step would take 8 % less, without decoding as long.  Starting and ending a
 // unit costs some 6 us, where instructions that run once wait for themselves, so code is kept short there (query rows
 // and output in one place each: mixed batch 447 -> 385 us).
+// A cap (up to 128) adds an exponential, a reciprocal and three more operations to each score: a job takes some 3000 cycles
+// instead of 1700, the special functions are at 44 % then, so it is the longer chain again (the counters: 0.53 instructions
+// per scheduler and cycle, waiting for tensor memory first).
 // Measured and not kept: jobs of 64 tokens with two buffers of scores (the issuing warp is the limit: mixed batch 419
 // where it was 512, long context 4500 us where it was 3450), two issuing warps, one loop that issues both kinds of units
 // (descriptors leave the uniform registers: long context 3270 -> 3560), query rows staged by the decoding warps (385 ->

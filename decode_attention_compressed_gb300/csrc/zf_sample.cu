@@ -26,11 +26,13 @@
 //      and the probabilities.
 // A bin with more entries than the list holds is divided again by bits of the places, with exact sums.
 //
-// Bound: a row's bytes once from memory are 1.7 to 4 us of the 22 to 40 that a cluster is busy.  The histogram's
+// What it takes: a row's bytes once from memory are 1.7 to 4 us of the 22 to 40 that a cluster is busy.  The histogram's
 // atomics (128000 entries on four CTAs, two CTAs per SM: 7.6 us) and the exponentials of steps 5 and 6 (10 and 7 us for
 // 50001 entries), about 55 instructions each, more than half of them on integers, are the rest, with a chain of 8 to 12
 // cluster barriers and exchanges of 1 to 2.5 us each.  64 rows of 128000 BF16 logits: 37 us; 320 rows of 50001 FP32
-// logits with their probabilities written: 182 us (4.2 rounds of the CTAs that fit).
+// logits with their probabilities written: 184 us (4.2 rounds of the CTAs that fit).  None of this is the operation's own
+// bound: integer weights are needed for the sums and at the border, but every kept entry is given one here, for its
+// probability too; equal 16-bit logits are not counted together; and the largest logit alone goes through the histogram.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
