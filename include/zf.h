@@ -505,8 +505,8 @@ size_t zf_q4_chunk_attn_workspace_size(int32_t batch, int32_t rows, int32_t num_
  *   out [rows][num_q_heads][128] BF16, lse [rows][num_q_heads] float32: the logarithm of the sum of exp(scores).  A
  *   row that sees nothing (a request with fewer tokens than new ones) gets out = 0 and lse = -inf.
  *   K and V are multiplied as the exact stored values; a query row's values enter as for zf_q4_decode_attn; scores
- *   and sums are float32 (with a softcap up to 128 a score is off by some 2^-22 of the cap besides, with a larger one by at most
- *   2^-20 of itself); the softmax weights enter the product as fp16 (off by at most 2^-11 of the weight, or
+ *   and sums are float32 (with a softcap up to 128 a score is off by some 2^-22 of the cap besides, with a larger one
+ *   by at most 2^-20 of itself); the softmax weights enter the product as fp16 (off by at most 2^-11 of the weight, or
  *   2^-32 of the row's largest one); the result is rounded once more, to BF16.  A NaN or an infinity in a query row
  *   stays in that row.
  *   A token_start entry that decreases or passes rows leaves that request out, a seq_len out of range is clamped;
@@ -514,10 +514,10 @@ size_t zf_q4_chunk_attn_workspace_size(int32_t batch, int32_t rows, int32_t num_
  *   A wait that takes 2 s gives up: it sets ZF_DEV_TIMEOUT, and out and lse of that call mean nothing.
  *   With a window, pages that lie before the windows of all new tokens of a request need not be there.
  *   batch <= ZF_MAX_BATCH, rows * num_q_heads < 2^31; ZF_ERR_UNSUPPORTED when all units (kv heads times the requests and
- *   the 256-row parts of the rows) times the steps (128 tokens) of the longest context that the page table has room for
- *   would pass 2^28.  rows == 0 or
- *   batch == 0 is a no-op.  Two kernels (attention, then the joining of units
- *   split over CTAs), launched with programmatic stream serialisation; results are deterministic (no atomics).
+ *   the 256-row parts of the rows) times the whole steps (128 tokens) of the longest context that the page table has room
+ *   for, with 6 more for a unit's ends, reach 2^31 / 7.  rows == 0 or batch == 0 is a no-op.  Two kernels (attention, then
+ *   the joining of units split over CTAs), launched with programmatic stream serialisation; results are deterministic
+ *   (no atomics).
  */
 zf_status zf_q4_chunk_attn(const zf_q4_cache* cache, const uint16_t* q, int32_t rows, int32_t batch,
                            int32_t num_q_heads, const int32_t* token_start, const int32_t* page_table,

@@ -1,5 +1,6 @@
 """Attention of a ragged batch of new tokens over the 4-bit cache, against the float64 oracle with bounds from the
 number of roundings."""
+import ctypes
 import math
 
 import numpy as np
@@ -9,6 +10,7 @@ import torch
 from oracle import zf_serve_oracle as R
 from oracle import zf_step_oracle as S
 from tests import helpers as H
+from tests.test_step_args import _desc
 
 pytestmark = pytest.mark.gpu
 
@@ -485,3 +487,18 @@ def test_wide_caps_against_the_oracle(zf, page, hkv, group, lens, new):
     assert torch.isnan(got[0].cpu()[hit]).all() and torch.isnan(got[1].cpu()[hit]).all()
     assert torch.equal(got[0].cpu()[~hit], want[0].cpu()[~hit]) and torch.equal(got[1].cpu()[~hit], want[1].cpu()[~hit])
     assert c.cache.status_word() == 0
+
+
+@pytest.mark.parametrize("batch,rows,hq,hkv", [(4096, 1, 1, 1), (16, 100000, 32, 8), (1, 3000, 28, 28)])
+def test_the_limit_of_units_and_steps(zf, batch, rows, hq, hkv):
+    """Refused from 7 * units * (steps + 6) = 2^31 - 1 on; below that the workspace, too small here, is looked at (nothing is
+    launched)."""
+    units = (rows * (hq // hkv) // 256 + batch) * hkv
+    steps = -(-(2 ** 31 - 1) // (7 * units)) - 6                     # the first that is too many
+    d = _desc(zf)
+    d.num_kv_heads, d.page_size = hkv, 16
+    call = lambda max_pages: zf.lib().zf_q4_chunk_attn(  # noqa: E731
+        ctypes.byref(d), 0x10000, rows, batch, hq, 0x20000, 0x30000, max_pages, 0x40000, 0.1, 0, 0.0, None, 0x50000, 0x60000,
+        0x70000, 16, None)
+    assert 8 * steps * 16 < 2 ** 31 - 4096
+    assert call(8 * steps - 1) == -3 and call(8 * steps) == -2
